@@ -12,7 +12,8 @@ import torch
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libgroupgemm.so")
 
-GG_DT = {torch.float32: 0, torch.bfloat16: 1, torch.uint8: 2, torch.float8_e4m3fn: 2}
+FP4 = torch.float4_e2m1fn_x2   # two 4-bit codes per element
+GG_DT = {torch.float32: 0, torch.bfloat16: 1, torch.uint8: 2, torch.float8_e4m3fn: 2, FP4: 3}
 OP = {"ragged_m": 0, "ragged_k": 1, "padded_m": 2, "padded_k": 3, "permute": 4}
 DEV_NEGATIVE_SIZE, DEV_SUM_EXCEEDS_M, DEV_OVER_CAPACITY, DEV_BAD_EXPERT = 0x1, 0x2, 0x4, 0x8
 
@@ -51,6 +52,12 @@ def lib():
                                  vp, vp, vp, sz, vp]
         L.moe_permute.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i64, i32, i64, i32, ctypes.c_int, vp, sz, vp]
         L.moe_unpermute.argtypes = [vp, vp, vp, vp, i64, i32, i64, ctypes.c_int, ctypes.c_int, vp]
+        L.moe_permute_grad.argtypes = [vp, vp, vp, i64, i32, i64, ctypes.c_int, ctypes.c_int, vp]
+        L.moe_unpermute_grad.argtypes = [vp, vp, vp, vp, vp, vp, vp, i64, i32, i64, ctypes.c_int, vp]
+        L.mxfp4_quantize.argtypes = [vp, vp, vp, i64, i64, i64, ctypes.c_int, vp]
+        L.mxfp4_quantize_weights.argtypes = [vp, vp, vp, i32, i64, i64, ctypes.c_int, vp]
+        L.mxfp4_dequantize.argtypes = [vp, vp, vp, i32, i64, i64, ctypes.c_int, vp]
+        L.ragged_dot_m_mxfp4.argtypes = [vp, vp, vp, vp, i64, i64, i64, i32, ctypes.c_int, vp, vp, vp, sz, vp]
         L.gg_schedule.argtypes = [vp, i64, i64, i32, i32, i32, vp, vp, vp, vp]
         L.gg_read_device_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32), vp]
         L.gg_status_string.argtypes = [ctypes.c_int]
@@ -58,7 +65,8 @@ def lib():
         L.gg_abi_version.restype = ctypes.c_int
         for f in ("ragged_dot_m", "ragged_dot_m_noalloc", "ragged_dot_m_nk", "ragged_dot_m_epilogue", "ragged_dot_m_gated", "ragged_dot_k",
                   "ragged_dot_k_epilogue",
-                  "padded_dot", "moe_permute", "moe_unpermute", "gg_schedule", "gg_read_device_status"):
+                  "padded_dot", "moe_permute", "moe_unpermute", "moe_permute_grad", "moe_unpermute_grad", "mxfp4_quantize",
+                  "mxfp4_quantize_weights", "mxfp4_dequantize", "ragged_dot_m_mxfp4", "gg_schedule", "gg_read_device_status"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -85,6 +93,16 @@ def _check(code, what):
         raise GGError(code, what)
 
 
+def _call(name, dev, *args):
+    """One call of the library on the current stream of `dev`, with `dev` the current device."""
+    if torch.cuda.current_device() != dev.index:
+        with torch.cuda.device(dev):
+            code = getattr(lib(), name)(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        code = getattr(lib(), name)(*args, torch.cuda.current_stream(dev).cuda_stream)
+    _check(code, name)
+
+
 def workspace_bytes(op, m, k, n, g, capacity=0, in_dtype=torch.bfloat16):
     return int(lib().gg_workspace_bytes(OP[op], m, k, n, g, capacity, GG_DT[in_dtype]))
 
@@ -104,6 +122,7 @@ def _workspace(op, m, k, n, g, capacity, in_dtype, device, workspace):
 
 # Every pointer handed to the library must address device memory of the right size: the
 # kernels trust the shapes they are given.  These checks run before any launch.
+_FLOATS = (torch.float32, torch.bfloat16)
 _IN_DTYPES = (torch.float32, torch.bfloat16, torch.uint8, torch.float8_e4m3fn)
 
 
@@ -112,7 +131,7 @@ def _tensor(t, name, device, shape=None, dtype=None, dtypes=None, contiguous=Tru
         raise TypeError(f"{name} must be a torch tensor")
     if t.device.type != "cuda":
         raise ValueError(f"{name} must be on a CUDA (HIP) device, not {t.device}")
-    if device is not None and t.device != torch.device(device):
+    if device is not None and t.device != (device if isinstance(device, torch.device) else torch.device(device)):
         raise ValueError(f"{name} is on {t.device}, the call runs on {device}")
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -352,40 +371,49 @@ def moe_permute(x, experts, g, x_scale=None, workspace=None, out=None):
     """Sort the top-k copies of the tokens of x [tokens, k] by expert (experts: int32
     [tokens, top_k]); returns (sorted_x [M, k], sorted_scale [M, k/32] or None, group_sizes
     int32 [g], sorted_to_copy int32 [M], copy_to_sorted int32 [M]) with M = tokens * top_k.
-    e4m3 inputs (uint8 codes) need their E8M0 x_scale [tokens, k/32].  `out` may supply
+    e4m3 inputs (uint8 codes) need their E8M0 x_scale [tokens, k/32]; MXFP4 inputs
+    (torch.float4_e2m1fn_x2 [tokens, k/2]) their scale panels [ceil(k/256), tokens, 8], and
+    sorted_scale is then [ceil(k/256), M, 8].  `out` may supply
     that tuple of output tensors (an entry None is allocated)."""
     dev = x.device
-    _tensor(x, "x", None, dtypes=_IN_DTYPES)
+    _tensor(x, "x", None, dtypes=_IN_DTYPES + (FP4,))
     if x.dim() != 2:
         raise ValueError("x must be [tokens, k]")
-    tokens, k = x.shape
+    tokens, width = x.shape
+    fp4 = x.dtype == FP4
+    k = 2 * width if fp4 else width
     _tensor(experts, "experts", dev, dtype=torch.int32)
     if experts.dim() != 2 or experts.shape[0] != tokens:
         raise ValueError("experts must be int32 [tokens, top_k]")
     top_k = experts.shape[1]
     M = tokens * top_k
-    if _is_e4m3(x):
+    sshape = ((k + 255) // 256, M, 8) if fp4 else (M, k // 32)
+    if fp4:
+        if x_scale is None or k % 32:
+            raise ValueError("MXFP4 rows need x_scale [ceil(k/256), tokens, 8] (k % 32 == 0)")
+        _tensor(x_scale, "x_scale", dev, (sshape[0], tokens, 8), torch.uint8)
+    elif _is_e4m3(x):
         if x_scale is None or k % 32:
             raise ValueError("e4m3 rows need x_scale [tokens, k/32] (k % 32 == 0)")
         _tensor(x_scale, "x_scale", dev, (tokens, k // 32), torch.uint8)
     elif x_scale is not None:
-        raise ValueError("x_scale is taken only with e4m3 rows")
+        raise ValueError("x_scale is taken only with e4m3 and MXFP4 rows")
     sorted_x, sorted_scale, group_sizes, s2c, c2s = out if out is not None else (None,) * 5
     if sorted_x is None:
-        sorted_x = torch.empty((M, k), dtype=x.dtype, device=dev)
+        sorted_x = torch.empty((M, width), dtype=x.dtype, device=dev)
     if x_scale is not None and sorted_scale is None:
-        sorted_scale = torch.empty((M, k // 32), dtype=torch.uint8, device=dev)
+        sorted_scale = torch.empty(sshape, dtype=torch.uint8, device=dev)
     if group_sizes is None:
         group_sizes = torch.empty((g,), dtype=torch.int32, device=dev)
     if s2c is None:
         s2c = torch.empty((M,), dtype=torch.int32, device=dev)
     if c2s is None:
         c2s = torch.empty((M,), dtype=torch.int32, device=dev)
-    _tensor(sorted_x, "sorted_x", dev, (M, k), x.dtype)
+    _tensor(sorted_x, "sorted_x", dev, (M, width), x.dtype)
     if x_scale is not None:
-        _tensor(sorted_scale, "sorted_scale", dev, (M, k // 32), torch.uint8)
+        _tensor(sorted_scale, "sorted_scale", dev, sshape, torch.uint8)
     elif sorted_scale is not None:
-        raise ValueError("sorted_scale is taken only with e4m3 rows")
+        raise ValueError("sorted_scale is taken only with e4m3 and MXFP4 rows")
     _tensor(group_sizes, "group_sizes", dev, (g,), torch.int32)
     _tensor(s2c, "sorted_to_copy", dev, (M,), torch.int32)
     _tensor(c2s, "copy_to_sorted", dev, (M,), torch.int32)
@@ -415,6 +443,153 @@ def moe_unpermute(y, copy_to_sorted, weights, out=None, out_dtype=None):
     code = lib().moe_unpermute(_p(y), _p(copy_to_sorted), _p(weights), _p(out), tokens, top_k, n, GG_DT[y.dtype],
                                GG_DT[out.dtype], _stream(dev))
     _check(code, "moe_unpermute")
+    return out
+
+def moe_permute_grad(dsorted, copy_to_sorted, top_k, out=None, out_dtype=None):
+    """The gradient of moe_permute with respect to x: dx[t, :] = sum_j
+    dsorted[copy_to_sorted[t * top_k + j], :] for dsorted [tokens * top_k, k] (fp32 or bf16);
+    copies that were not routed add nothing.  out_dtype defaults to dsorted's."""
+    dev = dsorted.device
+    _tensor(dsorted, "dsorted", None, dtypes=_FLOATS)
+    if dsorted.dim() != 2 or top_k < 1 or dsorted.shape[0] % top_k:
+        raise ValueError("dsorted must be [tokens * top_k, k] with top_k >= 1")
+    M, k = dsorted.shape
+    _tensor(copy_to_sorted, "copy_to_sorted", dev, (M,), torch.int32)
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else dsorted.dtype
+    out = _out(out, "out", dev, (M // top_k, k), out_dtype)
+    _call("moe_permute_grad", dev, dsorted.data_ptr(), copy_to_sorted.data_ptr(), out.data_ptr(), M // top_k, top_k, k,
+          GG_DT[dsorted.dtype], GG_DT[out.dtype])
+    return out
+
+
+def moe_unpermute_grad(dout, y, copy_to_sorted, sorted_to_copy, weights, out=None):
+    """The gradients of moe_unpermute(y, copy_to_sorted, weights): for dout [tokens, n] and y
+    [tokens * top_k, n] of one type (fp32 or bf16) and the index arrays of moe_permute, returns
+    (dy like y, dweights fp32 [tokens, top_k]).  Rows of dy that no copy was sorted to are 0.
+    `out` may supply the pair of outputs (an entry None is allocated)."""
+    dev = y.device
+    _tensor(y, "y", None, dtypes=_FLOATS)
+    if y.dim() != 2 or weights.dim() != 2:
+        raise ValueError("y must be [tokens * top_k, n] and weights [tokens, top_k]")
+    tokens, top_k = weights.shape
+    M, n = y.shape
+    if top_k < 1 or M != tokens * top_k:
+        raise ValueError(f"y has {M} rows, weights give {tokens} x {top_k}")
+    _tensor(dout, "dout", dev, (tokens, n), y.dtype)
+    _tensor(weights, "weights", dev, dtype=torch.float32)
+    _tensor(copy_to_sorted, "copy_to_sorted", dev, (M,), torch.int32)
+    _tensor(sorted_to_copy, "sorted_to_copy", dev, (M,), torch.int32)
+    dy, dweights = out if out is not None else (None, None)
+    if dy is None:
+        dy = torch.empty_like(y)
+    else:
+        _tensor(dy, "dy", dev, (M, n), y.dtype)
+    if dweights is None:
+        dweights = torch.empty((tokens, top_k), dtype=torch.float32, device=dev)
+    else:
+        _tensor(dweights, "dweights", dev, (tokens, top_k), torch.float32)
+    _call("moe_unpermute_grad", dev, dout.data_ptr(), y.data_ptr(), copy_to_sorted.data_ptr(), sorted_to_copy.data_ptr(),
+          weights.data_ptr(), dy.data_ptr(), dweights.data_ptr(), tokens, top_k, n, GG_DT[y.dtype])
+    return dy, dweights
+
+
+# ---------------------------------------------------------------------------------------
+# MXFP4: codes (torch.float4_e2m1fn_x2, or uint8 bytes) and E8M0 scale panels (uint8)
+
+_CODES = (FP4, torch.uint8)
+
+
+def _panels(k):
+    return (k + 255) // 256
+
+
+def _pair(out, codes_shape, scale_shape, dev):
+    codes, scale = out if out is not None else (None, None)
+    if codes is None:
+        codes = torch.empty(codes_shape, dtype=FP4, device=dev)
+    else:
+        _tensor(codes, "codes", dev, codes_shape, dtypes=_CODES)
+    if scale is None:
+        scale = torch.empty(scale_shape, dtype=torch.uint8, device=dev)
+    else:
+        _tensor(scale, "scale", dev, scale_shape, torch.uint8)
+    return codes, scale
+
+
+def mxfp4_quantize(x, out=None):
+    """Rows x [rows, k] (fp32 or bf16, k % 32 == 0, unit column stride, any row stride >= k) to MXFP4:
+    (codes torch.float4_e2m1fn_x2 [rows, k/2], scale uint8 [ceil(k/256), rows, 8]), one power-of-two
+    scale per 32 elements along k.  `out` may supply the pair (an entry None is allocated)."""
+    dev = x.device
+    _tensor(x, "x", None, dtypes=_FLOATS, contiguous=False)
+    if x.dim() != 2 or x.shape[1] % 32:
+        raise ValueError("x must be [rows, k] with k % 32 == 0")
+    rows, k = x.shape
+    stride = x.stride(0) if rows > 1 else k
+    if k and (x.stride(1) != 1 or stride < k):
+        raise ValueError("x must have unit column stride and rows that do not overlap")
+    codes, scale = _pair(out, (rows, k // 2), (_panels(k), rows, 8), dev)
+    _call("mxfp4_quantize", dev, x.data_ptr(), codes.data_ptr(), scale.data_ptr(), rows, k, max(stride, k), GG_DT[x.dtype])
+    return codes, scale
+
+
+def mxfp4_quantize_weights(w, out=None):
+    """Expert weights w [g, k, n] (fp32 or bf16, k % 32 == 0) to MXFP4 with k contiguous and blocked:
+    (codes [g, n, k/2], scale uint8 [g, ceil(k/256), n, 8]), the operands of ragged_dot_m_mxfp4."""
+    dev = w.device
+    _tensor(w, "w", None, dtypes=_FLOATS)
+    if w.dim() != 3 or w.shape[1] % 32:
+        raise ValueError("w must be [g, k, n] with k % 32 == 0")
+    g, k, n = w.shape
+    codes, scale = _pair(out, (g, n, k // 2), (g, _panels(k), n, 8), dev)
+    _call("mxfp4_quantize_weights", dev, w.data_ptr(), codes.data_ptr(), scale.data_ptr(), g, k, n, GG_DT[w.dtype])
+    return codes, scale
+
+
+def mxfp4_dequantize(codes, scale, out=None, out_dtype=None):
+    """The values of MXFP4 rows (codes [rows, k/2], scale [ceil(k/256), rows, 8]) as [rows, k], or of
+    weights (codes [g, n, k/2], scale [g, ceil(k/256), n, 8]) as [g, n, k]: bf16 (default) or fp32,
+    exact in both."""
+    dev = codes.device
+    _tensor(codes, "codes", None, dtypes=_CODES)
+    if codes.dim() not in (2, 3) or codes.shape[-1] % 16:
+        raise ValueError("codes must be [rows, k/2] or [g, n, k/2] with k % 32 == 0")
+    n, k = codes.shape[-2], 2 * codes.shape[-1]
+    lead = tuple(codes.shape[:-2])
+    _tensor(scale, "scale", dev, lead + (_panels(k), n, 8), torch.uint8)
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else torch.bfloat16
+    out = _out(out, "out", dev, lead + (n, k), out_dtype)
+    _call("mxfp4_dequantize", dev, codes.data_ptr(), scale.data_ptr(), out.data_ptr(), lead[0] if lead else 1, n, k,
+          GG_DT[out.dtype])
+    return out
+
+
+def ragged_dot_m_mxfp4(lhs, rhs, group_sizes, lhs_scale, rhs_scale, out=None, out_dtype=None, workspace=None):
+    """out[m,n]: row block of group h of the MXFP4 rows lhs (codes [m, k/2], scale panels lhs_scale
+    [ceil(k/256), m, 8]) times the MXFP4 weights rhs[h] (codes [g, n, k/2], rhs_scale
+    [g, ceil(k/256), n, 8]), contracted over k; rows past sum(group_sizes) are 0.  bf16 (default) or
+    fp32 output.  The operands are what mxfp4_quantize, moe_permute and mxfp4_quantize_weights give."""
+    dev = lhs.device
+    _tensor(lhs, "lhs", None, dtypes=_CODES)
+    if lhs.dim() != 2 or rhs.dim() != 3 or lhs.shape[1] % 16:
+        raise ValueError("lhs must be codes [m, k/2] and rhs codes [g, n, k/2] with k % 32 == 0")
+    m, half = lhs.shape
+    g, n, half2 = rhs.shape
+    if half2 != half:
+        raise ValueError(f"lhs has k = {2 * half}, rhs has {2 * half2}")
+    k = 2 * half
+    _tensor(rhs, "rhs", dev, dtypes=_CODES)
+    _tensor(group_sizes, "group_sizes", dev, (g,), torch.int32)
+    _tensor(lhs_scale, "lhs_scale", dev, (_panels(k), m, 8), torch.uint8)
+    _tensor(rhs_scale, "rhs_scale", dev, (g, _panels(k), n, 8), torch.uint8)
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else torch.bfloat16
+    out = _out(out, "out", dev, (m, n), out_dtype)
+    ws = _workspace("ragged_m", m, k, n, g, 0, FP4, dev, workspace)
+    _call("ragged_dot_m_mxfp4", dev, lhs.data_ptr(), rhs.data_ptr(), group_sizes.data_ptr(), out.data_ptr(), m, k, n, g,
+          GG_DT[out.dtype], lhs_scale.data_ptr(), rhs_scale.data_ptr(), ws.data_ptr(), ws.numel())
     return out
 
 

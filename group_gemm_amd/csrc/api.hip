@@ -216,7 +216,9 @@ const char* gg_status_string(gg_status s) {
 
 size_t gg_workspace_bytes(gg_op op, int64_t m, int64_t k, int64_t n, int32_t g, int64_t capacity, gg_dtype in) {
     if (m < 0 || k < 0 || n < 0 || g < 1 || g > GG_MAX_GROUPS) return 0;
-    if (in != GG_DT_F32 && in != GG_DT_BF16 && in != GG_DT_E4M3) return 0;
+    if (in != GG_DT_F32 && in != GG_DT_BF16 && in != GG_DT_E4M3 &&
+        !(in == GG_DT_E2M1 && (op == GG_OP_RAGGED_M || op == GG_OP_PERMUTE)))
+        return 0;
     switch (op) {
         case GG_OP_RAGGED_M:
         case GG_OP_RAGGED_K: return kHeader;
@@ -438,11 +440,11 @@ gg_status moe_permute(const void* x, const uint8_t* x_scale, const int32_t* expe
     if (!group_sizes || !workspace) return GG_ERR_NULL_PTR;
     if (tokens < 0 || top_k < 1 || k < 0 || g < 1 || g > GG_MAX_GROUPS || !fits_i32(k)) return GG_ERR_BAD_SHAPE;
     if (tokens > kMaxCopies / top_k) return GG_ERR_BAD_SHAPE;
-    if (dtype != GG_DT_F32 && dtype != GG_DT_BF16 && dtype != GG_DT_E4M3) return GG_ERR_BAD_DTYPE;
+    if (dtype != GG_DT_F32 && dtype != GG_DT_BF16 && dtype != GG_DT_E4M3 && dtype != GG_DT_E2M1) return GG_ERR_BAD_DTYPE;
     const int64_t M = tokens * top_k;
     if (M > 0 && (!experts || !sorted_to_copy || !copy_to_sorted)) return GG_ERR_NULL_PTR;
     if (tokens * k > 0 && (!x || !sorted_x)) return GG_ERR_NULL_PTR;
-    const bool mx = dtype == GG_DT_E4M3;
+    const bool fp4 = dtype == GG_DT_E2M1, mx = dtype == GG_DT_E4M3 || fp4;
     if (mx && k % 32 != 0) return GG_ERR_UNSUPPORTED;
     if (mx && tokens * k > 0 && (!x_scale || !sorted_scale)) return GG_ERR_NULL_PTR;
     if (!mx && (x_scale || sorted_scale)) return GG_ERR_BAD_DTYPE;
@@ -450,6 +452,8 @@ gg_status moe_permute(const void* x, const uint8_t* x_scale, const int32_t* expe
     if (!aligned(x, es) || !aligned(sorted_x, es) || !aligned(experts, 4) || !aligned(group_sizes, 4) ||
         !aligned(sorted_to_copy, 4) || !aligned(copy_to_sorted, 4) || !aligned(workspace, 16))
         return GG_ERR_MISALIGNED;
+    if (fp4 && (!aligned(x_scale, 8) || !aligned(sorted_scale, 8))) return GG_ERR_MISALIGNED;
+    if (fp4 && cdiv64(k, 256) > 65535) return GG_ERR_BAD_SHAPE;
     if (workspace_bytes < gg_workspace_bytes(GG_OP_PERMUTE, M, k, 0, g, 0, dtype)) return GG_ERR_WORKSPACE_TOO_SMALL;
     const gg::PermuteGeometry pg = gg::permute_geometry(M);
     uint8_t* ws = (uint8_t*)workspace;
@@ -462,8 +466,9 @@ gg_status moe_permute(const void* x, const uint8_t* x_scale, const int32_t* expe
     a.counts = (int*)(ws + kHeader);
     a.bad = (int*)(ws + kHeader + align_up((size_t)pg.nblk * (size_t)g * 4, 256));
     a.tokens = (int)tokens; a.top_k = top_k; a.g = g;
-    a.row_bytes = k * (int64_t)es;
-    a.scale_row_bytes = mx ? k / 32 : 0;
+    a.row_bytes = fp4 ? k / 2 : k * (int64_t)es;
+    a.scale_row_bytes = mx && !fp4 ? k / 32 : 0;
+    a.scale_panels = fp4 ? (int)cdiv64(k, 256) : 0;
     return gg::launch_permute(a, (hipStream_t)stream) == hipSuccess ? GG_OK : GG_ERR_HIP;
 }
 
@@ -482,6 +487,103 @@ gg_status moe_unpermute(const void* y, const int32_t* copy_to_sorted, const floa
                               top_k, (int)n, out, out_dtype == GG_DT_BF16, (hipStream_t)stream) == hipSuccess
                ? GG_OK
                : GG_ERR_HIP;
+}
+
+gg_status moe_permute_grad(const void* dsorted, const int32_t* copy_to_sorted, void* dx, int64_t tokens, int32_t top_k,
+                           int64_t k, gg_dtype in_dtype, gg_dtype out_dtype, void* stream) {
+    if (tokens < 0 || top_k < 1 || k < 0 || !fits_i32(k)) return GG_ERR_BAD_SHAPE;
+    if (tokens > kMaxCopies / top_k) return GG_ERR_BAD_SHAPE;
+    if ((in_dtype != GG_DT_F32 && in_dtype != GG_DT_BF16) || (out_dtype != GG_DT_F32 && out_dtype != GG_DT_BF16))
+        return GG_ERR_BAD_DTYPE;
+    if (tokens * k > 0 && (!copy_to_sorted || !dsorted || !dx)) return GG_ERR_NULL_PTR;
+    if (!aligned(dsorted, elem_bytes(in_dtype)) || !aligned(dx, elem_bytes(out_dtype)) || !aligned(copy_to_sorted, 4))
+        return GG_ERR_MISALIGNED;
+    return gg::launch_combine(dsorted, in_dtype == GG_DT_BF16, (int)(tokens * top_k), copy_to_sorted, nullptr, (int)tokens,
+                              top_k, (int)k, dx, out_dtype == GG_DT_BF16, (hipStream_t)stream) == hipSuccess
+               ? GG_OK
+               : GG_ERR_HIP;
+}
+
+gg_status moe_unpermute_grad(const void* dout, const void* y, const int32_t* copy_to_sorted, const int32_t* sorted_to_copy,
+                             const float* weights, void* dy, float* dweights, int64_t tokens, int32_t top_k, int64_t n,
+                             gg_dtype dtype, void* stream) {
+    if (tokens < 0 || top_k < 1 || n < 0 || !fits_i32(n)) return GG_ERR_BAD_SHAPE;
+    if (tokens > kMaxCopies / top_k) return GG_ERR_BAD_SHAPE;
+    if (dtype != GG_DT_F32 && dtype != GG_DT_BF16) return GG_ERR_BAD_DTYPE;
+    if (tokens > 0 && (!copy_to_sorted || !sorted_to_copy || !weights || !dweights)) return GG_ERR_NULL_PTR;
+    if (tokens * n > 0 && (!dout || !y || !dy)) return GG_ERR_NULL_PTR;
+    const size_t es = elem_bytes(dtype);
+    if (!aligned(dout, es) || !aligned(y, es) || !aligned(dy, es) || !aligned(copy_to_sorted, 4) ||
+        !aligned(sorted_to_copy, 4) || !aligned(weights, 4) || !aligned(dweights, 4))
+        return GG_ERR_MISALIGNED;
+    gg::UnpermuteGradArgs a{};
+    a.dout = dout; a.y = y; a.copy_to_sorted = copy_to_sorted; a.sorted_to_copy = sorted_to_copy; a.weights = weights;
+    a.dy = dy; a.dweights = dweights; a.tokens = (int)tokens; a.top_k = top_k; a.n = (int)n;
+    return gg::launch_unpermute_grad(a, dtype == GG_DT_BF16, (hipStream_t)stream) == hipSuccess ? GG_OK : GG_ERR_HIP;
+}
+
+gg_status mxfp4_quantize(const void* x, uint8_t* codes, uint8_t* scale, int64_t rows, int64_t k, int64_t x_stride,
+                         gg_dtype in_dtype, void* stream) {
+    // rows * panels bounds the launch and keeps every index of the kernels inside 63 bits
+    if (rows < 0 || k < 0 || !fits_i32(rows) || !fits_i32(k) || x_stride < k || x_stride > (int64_t(1) << 31) ||
+        !fits_i32(rows * cdiv64(k, 256)))
+        return GG_ERR_BAD_SHAPE;
+    if (in_dtype != GG_DT_F32 && in_dtype != GG_DT_BF16) return GG_ERR_BAD_DTYPE;
+    if (k % 32 != 0) return GG_ERR_UNSUPPORTED;
+    if (rows * k > 0 && (!x || !codes || !scale)) return GG_ERR_NULL_PTR;
+    if (!aligned(x, elem_bytes(in_dtype)) || !aligned(codes, 16) || !aligned(scale, 8)) return GG_ERR_MISALIGNED;
+    return gg::launch_fp4_quantize(x, in_dtype == GG_DT_BF16, rows, k, x_stride, codes, scale, (hipStream_t)stream) == hipSuccess
+               ? GG_OK
+               : GG_ERR_HIP;
+}
+
+gg_status mxfp4_quantize_weights(const void* w, uint8_t* codes, uint8_t* scale, int32_t g, int64_t k, int64_t n,
+                                 gg_dtype in_dtype, void* stream) {
+    if (k < 0 || n < 0 || g < 1 || g > GG_MAX_GROUPS || !fits_i32(k) || !fits_i32(n) || !fits_i32(n * cdiv64(k, 256)) ||
+        !fits_i32(n * cdiv64(k, 256) * g))
+        return GG_ERR_BAD_SHAPE;
+    if (in_dtype != GG_DT_F32 && in_dtype != GG_DT_BF16) return GG_ERR_BAD_DTYPE;
+    if (k % 32 != 0) return GG_ERR_UNSUPPORTED;
+    if (k * n > 0 && (!w || !codes || !scale)) return GG_ERR_NULL_PTR;
+    if (!aligned(w, elem_bytes(in_dtype)) || !aligned(codes, 16) || !aligned(scale, 8)) return GG_ERR_MISALIGNED;
+    return gg::launch_fp4_quantize_weights(w, in_dtype == GG_DT_BF16, g, k, n, codes, scale, (hipStream_t)stream) == hipSuccess
+               ? GG_OK
+               : GG_ERR_HIP;
+}
+
+gg_status mxfp4_dequantize(const uint8_t* codes, const uint8_t* scale, void* out, int32_t g, int64_t n, int64_t k,
+                           gg_dtype out_dtype, void* stream) {
+    if (k < 0 || n < 0 || g < 1 || g > GG_MAX_GROUPS || !fits_i32(k) || !fits_i32(n) || !fits_i32(n * cdiv64(k, 256)) ||
+        !fits_i32(n * cdiv64(k, 256) * g))
+        return GG_ERR_BAD_SHAPE;
+    if (out_dtype != GG_DT_F32 && out_dtype != GG_DT_BF16) return GG_ERR_BAD_DTYPE;
+    if (k % 32 != 0) return GG_ERR_UNSUPPORTED;
+    if (k * n > 0 && (!codes || !scale || !out)) return GG_ERR_NULL_PTR;
+    if (!aligned(out, elem_bytes(out_dtype)) || !aligned(codes, 16) || !aligned(scale, 8)) return GG_ERR_MISALIGNED;
+    return gg::launch_fp4_dequantize(codes, scale, g, n, k, out, out_dtype == GG_DT_BF16, (hipStream_t)stream) == hipSuccess
+               ? GG_OK
+               : GG_ERR_HIP;
+}
+
+gg_status ragged_dot_m_mxfp4(const void* lhs, const void* rhs, const int32_t* group_sizes, void* out, int64_t m, int64_t k,
+                             int64_t n, int32_t g, gg_dtype out_dtype, const uint8_t* lhs_scale, const uint8_t* rhs_scale,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+    gg_status st = check_common(m, k, n, g, group_sizes, workspace, workspace_bytes, kHeader);
+    if (st != GG_OK) return st;
+    if (out_dtype != GG_DT_BF16 && out_dtype != GG_DT_F32) return GG_ERR_BAD_DTYPE;
+    if (k % 32 != 0) return GG_ERR_UNSUPPORTED;
+    if ((m * k > 0 && (!lhs || !lhs_scale)) || (k * n > 0 && (!rhs || !rhs_scale)) || (m * n > 0 && !out)) return GG_ERR_NULL_PTR;
+    if (!aligned(lhs, 16) || !aligned(rhs, 16) || !aligned(lhs_scale, 8) || !aligned(rhs_scale, 8) ||
+        !aligned(out, elem_bytes(out_dtype)))
+        return GG_ERR_MISALIGNED;
+    gg::Fp4Params p{};
+    p.lhs = (const uint8_t*)lhs; p.rhs = (const uint8_t*)rhs; p.lhs_scale = lhs_scale; p.rhs_scale = rhs_scale;
+    p.group_sizes = group_sizes; p.out = out; p.status = (uint32_t*)workspace;
+    p.m = (int)m; p.k = (int)k; p.n = (int)n; p.g = g; p.out_f32 = out_dtype == GG_DT_F32;
+    if (!gg::ragged_m_fp4_grid_ok(p)) return GG_ERR_BAD_SHAPE;
+    int cus;
+    if (device_cus(&cus) != 0) return GG_ERR_HIP;
+    return gg::launch_ragged_m_fp4(p, cus, (hipStream_t)stream) == hipSuccess ? GG_OK : GG_ERR_HIP;
 }
 
 gg_status gg_schedule(const int32_t* group_sizes, int64_t m, int64_t n, int32_t g, int32_t block_m, int32_t block_n,

@@ -86,6 +86,27 @@ bool ragged_k_bf16_fast_ok(const KParams& p);
 hipError_t launch_ragged_k_bf16_fast(const KParams& p, int grid, hipStream_t s);
 hipError_t launch_ragged_k_f32(const KParams& p, int grid, hipStream_t s);
 
+// MXFP4 (e2m1 codes, E8M0 scale panels [ceil(k/256), rows, 8]).
+struct Fp4Params {              // ragged_dot_m_mxfp4
+    const uint8_t* lhs;         // [m, k/2]
+    const uint8_t* rhs;         // [g, n, k/2]
+    const uint8_t* lhs_scale;   // [ceil(k/256), m, 8]
+    const uint8_t* rhs_scale;   // [g, ceil(k/256), n, 8]
+    const int32_t* group_sizes;
+    void* out;                  // [m, n]
+    uint32_t* status;
+    int m, k, n, g;
+    int out_f32;
+};
+bool ragged_m_fp4_grid_ok(const Fp4Params& p);   // the launch fits 2^31 - 1 workgroups
+hipError_t launch_ragged_m_fp4(const Fp4Params& p, int cus, hipStream_t s);
+hipError_t launch_fp4_quantize(const void* x, bool bf16, int64_t rows, int64_t k, int64_t stride, uint8_t* codes,
+                               uint8_t* scale, hipStream_t s);
+hipError_t launch_fp4_quantize_weights(const void* w, bool bf16, int g, int64_t k, int64_t n, uint8_t* codes,
+                                       uint8_t* scale, hipStream_t s);
+hipError_t launch_fp4_dequantize(const uint8_t* codes, const uint8_t* scale, int g, int64_t n, int64_t k, void* out,
+                                 bool out_bf16, hipStream_t s);
+
 // MoE permute / un-permute.
 constexpr int kMaxChunks = 64;   // upper bound on the permute's histogram / rank workgroups
 struct PermuteGeometry { int chunk, nblk; };   // copies per chunk, number of chunks
@@ -105,10 +126,23 @@ struct PermuteArgs {
     uint32_t* status;
     int tokens, top_k, g;
     int64_t row_bytes, scale_row_bytes;
+    int scale_panels;              // > 0: the scales are panels [scale_panels, rows, 8] (e2m1), not rows
 };
 hipError_t launch_permute(const PermuteArgs& a, hipStream_t s);
+// w == NULL: every weight is 1 (the permute's gradient)
 hipError_t launch_combine(const void* y, bool y_bf16, int rows, const int32_t* copy_to_sorted, const float* w,
                           int tokens, int top_k, int n, void* out, bool out_bf16, hipStream_t s);
+struct UnpermuteGradArgs {
+    const void* dout;              // [tokens, n]
+    const void* y;                 // [tokens * top_k, n]
+    const int32_t* copy_to_sorted;
+    const int32_t* sorted_to_copy;
+    const float* weights;          // [tokens, top_k]
+    void* dy;                      // [tokens * top_k, n]
+    float* dweights;               // [tokens, top_k]
+    int tokens, top_k, n;
+};
+hipError_t launch_unpermute_grad(const UnpermuteGradArgs& a, bool bf16, hipStream_t s);
 
 // Static tile geometry of each family (host-side grid sizing).
 struct TileShape { int bm, bn; };

@@ -241,6 +241,18 @@ __global__ __launch_bounds__(256) void scatter(const uint8_t* __restrict__ x, co
     }
 }
 
+// Scale panels [panels, rows, 8] (e2m1 rows) to their sorted places, 8 bytes a thread: the sorted side is
+// written in order and the tokens' side, 8 bytes a token and panel, comes from the caches; rows past the
+// routed total are zero.
+__global__ __launch_bounds__(256) void scatter_panels(const uint64_t* __restrict__ xs, int T, int top_k, int M,
+                                                      const int32_t* __restrict__ s2c, const int* __restrict__ total_routed,
+                                                      uint64_t* __restrict__ sorted_s) {
+    const int p = blockIdx.x * 256 + threadIdx.x;
+    if (p >= M) return;
+    const bool routed = p < *total_routed;
+    sorted_s[(size_t)blockIdx.y * M + p] = routed ? xs[(size_t)blockIdx.y * T + s2c[p] / top_k] : 0;
+}
+
 // out[t, :] = sum_j w[t, j] * y[copy_to_sorted[t * top_k + j], :], fp32 sum in j order;
 // entries outside [0, rows) contribute nothing.  WPR waves per token; VEC: 8 consecutive
 // columns per lane with 16-byte (bf16) or 2 x 16-byte (fp32) accesses.
@@ -281,7 +293,9 @@ __device__ inline float ld1(const float* p) { return *p; }
 __device__ inline void st1(uint16_t* p, float v) { *p = f32_to_bf16(v); }
 __device__ inline void st1(float* p, float v) { *p = v; }
 
-template <typename InT, typename OutT, bool VEC>
+// WEIGHTED = false: every weight is 1 (the gradient of the permute: a token's row is the plain sum
+// of its copies' gradients).
+template <typename InT, typename OutT, bool VEC, bool WEIGHTED>
 __global__ __launch_bounds__(256) void combine(const InT* __restrict__ y, int rows, const int32_t* __restrict__ c2s,
                                                const float* __restrict__ w, int T, int top_k, int n,
                                                OutT* __restrict__ out) {
@@ -290,7 +304,7 @@ __global__ __launch_bounds__(256) void combine(const InT* __restrict__ y, int ro
     const int t = blockIdx.x * TPB + wv / WPR, h = wv % WPR;
     if (t >= T) return;
     const int32_t* pos = c2s + (size_t)t * top_k;
-    const float* wt = w + (size_t)t * top_k;
+    const float* wt = WEIGHTED ? w + (size_t)t * top_k : nullptr;
     OutT* orow = out + (size_t)t * n;
     if constexpr (VEC) {
         // eight copies at a time.  Copies without a sorted row (and slots past top_k) read
@@ -304,7 +318,7 @@ __global__ __launch_bounds__(256) void combine(const InT* __restrict__ y, int ro
                 const int p = j < top_k ? pos[j] : -1;
                 q.ok[jj] = p >= 0 && p < rows;
                 q.p[jj] = q.ok[jj] ? p : 0;
-                q.w[jj] = q.ok[jj] ? wt[j] : 0.f;
+                q.w[jj] = q.ok[jj] ? (WEIGHTED ? wt[j] : 1.f) : 0.f;
             }
         };
         auto accumulate = [&](const Eight& q, int c0, float (&acc)[8]) {
@@ -334,22 +348,28 @@ __global__ __launch_bounds__(256) void combine(const InT* __restrict__ y, int ro
             for (int j = 0; j < top_k; ++j) {
                 const int p = pos[j];
                 if (p < 0 || p >= rows) continue;
-                acc = __builtin_fmaf(wt[j], ld1(y + (size_t)p * n + c), acc);
+                acc = __builtin_fmaf(WEIGHTED ? wt[j] : 1.f, ld1(y + (size_t)p * n + c), acc);
             }
             st1(orow + c, acc);
         }
     }
 }
 
-template <typename InT, typename OutT>
-hipError_t launch_combine_t(const void* y, int rows, const int32_t* c2s, const float* w, int T, int top_k, int n,
+template <typename InT, typename OutT, bool WEIGHTED>
+hipError_t launch_combine_w(const void* y, int rows, const int32_t* c2s, const float* w, int T, int top_k, int n,
                             void* out, bool vec, hipStream_t s) {
     const dim3 grid((T + TPB - 1) / TPB), block(256);
     if (vec)
-        hipLaunchKernelGGL((combine<InT, OutT, true>), grid, block, 0, s, (const InT*)y, rows, c2s, w, T, top_k, n, (OutT*)out);
+        hipLaunchKernelGGL((combine<InT, OutT, true, WEIGHTED>), grid, block, 0, s, (const InT*)y, rows, c2s, w, T, top_k, n, (OutT*)out);
     else
-        hipLaunchKernelGGL((combine<InT, OutT, false>), grid, block, 0, s, (const InT*)y, rows, c2s, w, T, top_k, n, (OutT*)out);
+        hipLaunchKernelGGL((combine<InT, OutT, false, WEIGHTED>), grid, block, 0, s, (const InT*)y, rows, c2s, w, T, top_k, n, (OutT*)out);
     return hipGetLastError();
+}
+template <typename InT, typename OutT>
+hipError_t launch_combine_t(const void* y, int rows, const int32_t* c2s, const float* w, int T, int top_k, int n,
+                            void* out, bool vec, hipStream_t s) {
+    return w ? launch_combine_w<InT, OutT, true>(y, rows, c2s, w, T, top_k, n, out, vec, s)
+             : launch_combine_w<InT, OutT, false>(y, rows, c2s, w, T, top_k, n, out, vec, s);
 }
 
 }  // namespace perm
@@ -375,7 +395,7 @@ hipError_t launch_permute(const PermuteArgs& a, hipStream_t s) {
                        a.status);
     if (M == 0) return hipGetLastError();
     const bool vec = (uintptr_t)a.x % 16 == 0 && (uintptr_t)a.sorted_x % 16 == 0 && a.row_bytes % 16 == 0 &&
-                     (!a.x_scale || ((uintptr_t)a.x_scale % 16 == 0 && (uintptr_t)a.sorted_scale % 16 == 0 &&
+                     (!a.x_scale || a.scale_panels > 0 || ((uintptr_t)a.x_scale % 16 == 0 && (uintptr_t)a.sorted_scale % 16 == 0 &&
                                      a.scale_row_bytes % 16 == 0));
     const int tok_blocks = (a.tokens + perm::TPB - 1) / perm::TPB;
     const int zero_blocks = min((M + 3) / 4, 256);
@@ -390,6 +410,10 @@ hipError_t launch_permute(const PermuteArgs& a, hipStream_t s) {
         hipLaunchKernelGGL(perm::scatter<false>, grid, block, 0, s, (const uint8_t*)a.x, xs, a.tokens, a.top_k,
                            a.row_bytes, a.scale_row_bytes, a.copy_to_sorted, a.total_routed, zero_blocks,
                            a.sorted_to_copy, (uint8_t*)a.sorted_x, ss);
+    if (a.scale_panels > 0)
+        hipLaunchKernelGGL(perm::scatter_panels, dim3((M + 255) / 256, a.scale_panels), dim3(256), 0, s,
+                           (const uint64_t*)a.x_scale, a.tokens, a.top_k, M, a.sorted_to_copy, a.total_routed,
+                           (uint64_t*)a.sorted_scale);
     return hipGetLastError();
 }
 

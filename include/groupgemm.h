@@ -65,6 +65,9 @@ typedef enum {
     GG_DT_F32 = 0,                 /* IEEE binary32                                         */
     GG_DT_BF16 = 1,                /* bfloat16                                              */
     GG_DT_E4M3 = 2,                /* OCP float8 e4m3 ("e4m3fn"), with E8M0 block scales    */
+    GG_DT_E2M1 = 3,                /* OCP float4 e2m1, two per byte, with E8M0 block scales in
+                                      panels (MXFP4, see mxfp4_quantize): ragged_dot_m_mxfp4 and
+                                      moe_permute only                                      */
     GG_DT_RANGE_MIN = INT32_MIN, GG_DT_RANGE_MAX = INT32_MAX
 } gg_dtype;
 
@@ -146,6 +149,51 @@ gg_status ragged_dot_m_nk(const void* lhs, const void* rhs_nk, const int32_t* gr
                           int64_t m, int64_t k, int64_t n, int32_t g, gg_dtype in_dtype,
                           gg_dtype out_dtype, void* workspace, size_t workspace_bytes, void* stream);
 
+/* MXFP4 tensors -- OCP e2m1 elements with one E8M0 scale per 32 elements along k, k % 32 == 0.
+ *   codes  [rows, k/2]  bytes: element 2i in the low half of byte i, 2i + 1 in the high half; an
+ *     element is a sign bit over one of 0, 0.5, 1, 1.5, 2, 3, 4, 6.
+ *   scales in panels of 256 elements along k: [ceil(k/256), rows, 8] bytes; byte j of panel p and
+ *     row r belongs to elements 256 p + 32 j .. + 31 of that row (value 2^(byte - 127), 255 is NaN).
+ *     Bytes past k are written as 0 and never used.  All scales that a 256-wide slice of a tile of
+ *     rows needs are contiguous, which a row-major [rows, k/32] array is not.
+ *   Weights [g, k, n] become codes [g, n, k/2] and scales [g, ceil(k/256), n, 8].
+ *   Code arrays are 16-byte aligned, scale arrays 8-byte aligned.
+ *
+ * mxfp4_quantize -- rows to MXFP4 (the blocked form that ragged_dot_m_mxfp4 multiplies).
+ * ("[Triton/Gluon] Merge MoE MXFP8 GEMM into existing _moe_gemm_a8w8 kernel": one E8M0 scale per 32
+ * elements along k; here with 4-bit elements.)
+ *   x [rows, k]  in_dtype (fp32 or bf16), rows x_stride >= k elements apart
+ *   Per block: scale byte = max(E - 2, 0), E the biased fp32 exponent of the block's largest
+ *   magnitude (255 where the block holds an infinity or a NaN: all its values read as NaN);
+ *   codes = x / 2^(byte - 127) rounded to nearest, ties to even, and saturated at 6.
+ * Every byte of codes and scale is written.  No workspace. */
+gg_status mxfp4_quantize(const void* x, uint8_t* codes, uint8_t* scale, int64_t rows, int64_t k,
+                         int64_t x_stride, gg_dtype in_dtype, void* stream);
+
+/* mxfp4_quantize_weights -- expert weights w [g, k, n] (fp32 or bf16, n fastest, as the other calls
+ * take them) to MXFP4 codes [g, n, k/2] and scales [g, ceil(k/256), n, 8], blocked along k. */
+gg_status mxfp4_quantize_weights(const void* w, uint8_t* codes, uint8_t* scale, int32_t g, int64_t k,
+                                 int64_t n, gg_dtype in_dtype, void* stream);
+
+/* mxfp4_dequantize -- the values of MXFP4 codes [g, n, k/2] and scales [g, ceil(k/256), n, 8] as
+ * out [g, n, k] (bf16 or fp32); rows [rows, k] are g = 1, n = rows.  Exact in both types (values past
+ * their largest finite one become infinite).  Dequantised weights [g, n, k] are the `rhs` of the data
+ * gradient: ragged_dot_m(dout [m, n], out [g, n, k]) = [m, k]. */
+gg_status mxfp4_dequantize(const uint8_t* codes, const uint8_t* scale, void* out, int32_t g, int64_t n,
+                           int64_t k, gg_dtype out_dtype, void* stream);
+
+/* ragged_dot_m_mxfp4 -- ragged_dot_m over MXFP4 operands, the weights stored [g, n, k] (k contiguous):
+ *   out[r, :] = lhs[r, :] . rhs[h]^T   for every row r of group h;   rows r >= sum(sizes) = 0.
+ *   lhs [m, k/2], lhs_scale [ceil(k/256), m, 8]; rhs [g, n, k/2], rhs_scale [g, ceil(k/256), n, 8]
+ *   out [m, n]  bf16 or fp32; every element written
+ * k % 32 == 0 (GG_ERR_UNSUPPORTED otherwise); any m and n.  Few rows per group (single tokens,
+ * decoding batches) and many (prompts) take different kernels.  Workspace, status and errors as
+ * ragged_dot_m: gg_workspace_bytes(GG_OP_RAGGED_M, m, k, n, g, 0, GG_DT_E2M1). */
+gg_status ragged_dot_m_mxfp4(const void* lhs, const void* rhs, const int32_t* group_sizes, void* out,
+                             int64_t m, int64_t k, int64_t n, int32_t g, gg_dtype out_dtype,
+                             const uint8_t* lhs_scale, const uint8_t* rhs_scale, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
 /* ragged_dot_m_epilogue -- ragged_dot_m with a fused epilogue, in place on out:
  *   out[r, :] = alpha * (lhs[r, :] . rhs[h]) + bias[h, :] + beta * out[r, :]
  * for every row r of group h; rows r >= sum(sizes) are 0 as in ragged_dot_m.
@@ -226,14 +274,16 @@ gg_status padded_dot(gg_op mode, const void* a, const void* b, const int32_t* gr
  * each token top_k times, argsort the flattened expert ids, sort the activations with that
  * order, bincount the ids into group_sizes.)  M = tokens * top_k copies; copy i is token
  * i / top_k routed to experts[i].
- *   x              [tokens, k]      dtype (fp32, bf16 or e4m3)
- *   x_scale        [tokens, k/32]   E8M0 bytes, e4m3 only (k % 32 == 0), else NULL
+ *   x              [tokens, k]      dtype (fp32, bf16, e4m3, or e2m1: [tokens, k/2] bytes)
+ *   x_scale        [tokens, k/32]   E8M0 bytes, e4m3 only (k % 32 == 0), else NULL; for e2m1
+ *                                   the panels [ceil(k/256), tokens, 8], 8-byte aligned
  *   experts        [tokens, top_k]  int32 expert ids; an id outside [0, g) is not routed
  *                                   (that copy gets no row) and sets GG_DEV_BAD_EXPERT
  *   sorted_x       [M, k]           dtype: the routed copies' rows grouped by expert, equal
  *                                   ids in copy order (a stable sort); rows past the routed
  *                                   total are zero
- *   sorted_scale   [M, k/32]        e4m3 only, else NULL: the scale rows in the same order
+ *   sorted_scale   [M, k/32]        e4m3 only, else NULL: the scale rows in the same order;
+ *                                   for e2m1 the panels [ceil(k/256), M, 8]
  *   group_sizes    [g]   int32      rows per expert (the bincount); sums to the routed total
  *   sorted_to_copy [M]   int32      copy index of each sorted row (the pages' argsort
  *                                   result), -1 past the routed total
@@ -263,6 +313,34 @@ gg_status moe_permute(const void* x, const uint8_t* x_scale, const int32_t* expe
 gg_status moe_unpermute(const void* y, const int32_t* copy_to_sorted, const float* weights, void* out,
                         int64_t tokens, int32_t top_k, int64_t n, gg_dtype in_dtype,
                         gg_dtype out_dtype, void* stream);
+
+/* moe_permute_grad -- the gradient of moe_permute with respect to x: every copy of a token was that
+ * token's row, so its gradient is the sum over its copies.
+ *   dsorted        [tokens * top_k, k]  in_dtype (fp32 or bf16): gradient of sorted_x
+ *   copy_to_sorted [tokens * top_k]     int32, as written by moe_permute; an entry outside
+ *                                       [0, tokens * top_k) (-1: not routed) adds nothing
+ *   dx             [tokens, k]          out_dtype (fp32 or bf16):
+ *     dx[t, :] = sum_j dsorted[copy_to_sorted[t * top_k + j], :]
+ * fp32 accumulation in j order, one rounding; every element of dx is written.  No workspace. */
+gg_status moe_permute_grad(const void* dsorted, const int32_t* copy_to_sorted, void* dx, int64_t tokens,
+                           int32_t top_k, int64_t k, gg_dtype in_dtype, gg_dtype out_dtype, void* stream);
+
+/* moe_unpermute_grad -- the gradients of moe_unpermute with respect to y and the router weights.
+ *   dout           [tokens, n]          dtype (fp32 or bf16): gradient of moe_unpermute's out
+ *   y              [tokens * top_k, n]  dtype: the call's input, rows in sorted order
+ *   copy_to_sorted, sorted_to_copy      int32 [tokens * top_k], as written by moe_permute
+ *   weights        [tokens, top_k]      fp32 router weights
+ *   dy             [tokens * top_k, n]  dtype: row p of copy i = sorted_to_copy[p] (with
+ *     copy_to_sorted[i] == p) is weights[i] * dout[i / top_k, :], rounded once; a row that no copy
+ *     claims so (past the routed total) is 0
+ *   dweights       [tokens, top_k]      fp32: dweights[i] = dout[i / top_k, :] . y[copy_to_sorted[i], :],
+ *     summed in fp32 in an order that depends on n alone; 0 where the entry is outside
+ *     [0, tokens * top_k)
+ * Every element of dy and dweights is written; no atomics.  No workspace. */
+gg_status moe_unpermute_grad(const void* dout, const void* y, const int32_t* copy_to_sorted,
+                             const int32_t* sorted_to_copy, const float* weights, void* dy,
+                             float* dweights, int64_t tokens, int32_t top_k, int64_t n, gg_dtype dtype,
+                             void* stream);
 
 /* gg_schedule -- runs only the group_sizes -> offsets scan that opens every launch, and
  * writes its tables, so the scan can be tested on its own.

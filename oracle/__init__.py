@@ -334,6 +334,108 @@ def moe_unpermute(y, copy_to_sorted, weights):
     return np.einsum("tkn,tk->tn", unsorted.reshape(T, K, n), w)
 
 
+# ---------------------------------------------------------------------------------------
+# MXFP4: OCP e2m1 elements, one E8M0 scale per 32 elements along k, scales in panels of 256
+
+E2M1 = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+
+
+def mxfp4_panels(scale):
+    """Row-major E8M0 bytes [..., rows, k/32] as panels [..., ceil(k/256), rows, 8], 0 past k."""
+    scale = np.asarray(scale, dtype=np.uint8)
+    kb = scale.shape[-1]
+    pad = np.zeros(scale.shape[:-1] + (-kb % 8,), dtype=np.uint8)
+    s = np.concatenate([scale, pad], axis=-1)
+    s = s.reshape(s.shape[:-1] + (-1, 8))
+    return np.ascontiguousarray(np.moveaxis(s, -2, -3))
+
+
+def mxfp4_values(codes, panels):
+    """fp64 values [..., rows, k] of MXFP4 codes [..., rows, k/2] and scale panels; a scale byte of 255
+    makes its 32 values NaN."""
+    codes = np.asarray(codes, dtype=np.uint8)
+    c = np.stack([codes & 15, codes >> 4], axis=-1).reshape(codes.shape[:-1] + (-1,)).astype(np.int64)
+    v = np.where(c & 8, -1.0, 1.0) * E2M1[c & 7]
+    k = v.shape[-1]
+    s = np.moveaxis(np.asarray(panels, dtype=np.uint8), -3, -2)
+    s = s.reshape(s.shape[:-2] + (-1,))[..., :k // 32].astype(np.float64)
+    scale = np.where(s == 255, np.nan, 2.0 ** (s - 127))
+    return v * np.repeat(scale, 32, axis=-1)
+
+
+def mxfp4_quantize(x):
+    """fp64 rows [..., rows, k] to (codes uint8 [..., rows, k/2], scale bytes [..., rows, k/32]): per block
+    the exponent E = floor(log2 max|x|) - 2, at least -127, byte E + 127 (255 for a block with an infinity
+    or a NaN, whose codes are returned as 0); codes the nearest e2m1 value to x / 2^E, a tie to the even
+    code, at most 6."""
+    x = np.asarray(x, dtype=np.float64)
+    b = x.reshape(x.shape[:-1] + (-1, 32))
+    ok = np.isfinite(b).all(axis=-1)
+    b = np.where(ok[..., None], b, 0.0)
+    amax = np.abs(b).max(axis=-1) if b.size else np.zeros(b.shape[:-1])
+    _, e = np.frexp(amax)
+    e = np.where(amax > 0, np.maximum(e - 1 - 2, -127), -127)
+    a = np.ldexp(np.abs(b), -e[..., None])
+    code = np.zeros(b.shape, dtype=np.int64)
+    for i in range(7):   # midpoint between code i and i + 1; the tie goes to the even one
+        mid = (E2M1[i] + E2M1[i + 1]) / 2
+        code += (a >= mid) if i % 2 else (a > mid)
+    code |= np.where(np.signbit(b), 8, 0)
+    code = code.reshape(x.shape).astype(np.uint8)
+    return code[..., 0::2] | (code[..., 1::2] << 4), np.where(ok, e + 127, 255).astype(np.uint8)
+
+
+def ragged_dot_m_mxfp4(lhs, lhs_panels, rhs, rhs_panels, group_sizes):
+    """fp64 rows of lhs (MXFP4 [m, k]) times their group's weights (MXFP4 [g, n, k]) transposed; sizes
+    clamped as in the other ragged products.  Returns (out, sum of |products|), both [m, n]."""
+    a, b = mxfp4_values(lhs, lhs_panels), mxfp4_values(rhs, rhs_panels)
+    m, n = a.shape[0], b.shape[1]
+    out, mag = np.zeros((m, n)), np.zeros((m, n))
+    at = 0
+    for h, s in enumerate(np.asarray(group_sizes, dtype=np.int64)):
+        s = min(max(int(s), 0), m - at)
+        if s:
+            out[at:at + s] = a[at:at + s] @ b[h].T
+            mag[at:at + s] = np.abs(a[at:at + s]) @ np.abs(b[h]).T
+        at += s
+    return out, mag
+
+
+def moe_permute_grad(dsorted, copy_to_sorted, top_k):
+    """fp64 gradient of moe_permute's x: the sum over a token's routed copies of their rows of dsorted
+    [M, k] (float32 or bfloat16 bit patterns)."""
+    d = np.asarray(dsorted)
+    d = bf16_values(d) if d.dtype == np.uint16 else d.astype(np.float64)
+    c2s = np.asarray(copy_to_sorted, dtype=np.int64)
+    M, k = d.shape
+    dx = np.zeros((M // top_k, k))
+    for i, p in enumerate(c2s):
+        if 0 <= p < M:
+            dx[i // top_k] += d[p]
+    return dx
+
+
+def moe_unpermute_grad(dout, y, copy_to_sorted, sorted_to_copy, weights):
+    """fp64 gradients of moe_unpermute: (dy [M, n], dweights [tokens, top_k], sum of |dout . y| terms)."""
+    def val(a):
+        a = np.asarray(a)
+        return bf16_values(a) if a.dtype == np.uint16 else a.astype(np.float64)
+    d, yv, w = val(dout), val(y), np.asarray(weights, dtype=np.float64)
+    T, K = w.shape
+    M = T * K
+    c2s, s2c = np.asarray(copy_to_sorted, dtype=np.int64), np.asarray(sorted_to_copy, dtype=np.int64)
+    dy = np.zeros_like(yv)
+    for p, i in enumerate(s2c):
+        if 0 <= i < M and c2s[i] == p:
+            dy[p] = w.reshape(-1)[i] * d[i // K]
+    dw, mag = np.zeros(M), np.zeros(M)
+    for i, p in enumerate(c2s):
+        if 0 <= p < M:
+            dw[i] = d[i // K] @ yv[p]
+            mag[i] = np.abs(d[i // K]) @ np.abs(yv[p])
+    return dy, dw.reshape(T, K), mag.reshape(T, K)
+
+
 def num_threads():
     return lib().oracle_num_threads()
 
