@@ -17,6 +17,15 @@ using namespace ring;
 constexpr int kFp4 = 4;   // operand format selector of e2m1
 __device__ inline i32x8 widen(i32x4 v) { return i32x8{v[0], v[1], v[2], v[3], 0, 0, 0, 0}; }
 
+// 16 (or 4) bytes a lane straight into LDS, as ring.hpp's loads, with the wait state that this target asks for
+// between a scalar write of m0 and the load that takes its LDS address from it.
+__device__ inline void load16(i32x4 r, uint32_t lds_addr, uint32_t off) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds_addr), "v"(off), "s"(r) : "memory", "m0");
+}
+__device__ inline void load4(i32x4 r, uint32_t lds_addr, uint32_t off) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds_addr), "v"(off), "s"(r) : "memory", "m0");
+}
+
 constexpr int kPanel = 256;           // elements along k of one scale panel
 constexpr int kRowBytes = kPanel / 2; // code bytes of one row of a panel: one cache line
 
@@ -151,8 +160,9 @@ __global__ __launch_bounds__(256) void split_kernel(Fp4Params p, int ntiles) {
         return;
     }
     const int rows = rt.rows, panels = (p.k + kPanel - 1) / kPanel, rb = p.k >> 1;
-    const i32x4 rx = make_rsrc_v(p.lhs + (size_t)rt.row0 * rb, (uint32_t)rows * (uint32_t)rb);
-    const i32x4 rw = make_rsrc_v(p.rhs + ((size_t)rt.grp * p.n + col0) * rb, (uint32_t)cols * (uint32_t)rb);
+    i32x4 rx = make_rsrc_v(p.lhs + (size_t)rt.row0 * rb, (uint32_t)rows * (uint32_t)rb);
+    i32x4 rw = make_rsrc_v(p.rhs + ((size_t)rt.grp * p.n + col0) * rb, (uint32_t)cols * (uint32_t)rb);
+    asm volatile("s_nop 4" : "+s"(rx), "+s"(rw));
     const uint8_t* xs0 = p.lhs_scale + (size_t)rt.row0 * 8;
     const uint8_t* ws0 = p.rhs_scale + ((size_t)rt.grp * panels * p.n + col0) * 8;
     const uint32_t ring0 = lds_u32(smem) + (uint32_t)(wave * D * R::SLOT);
@@ -169,17 +179,18 @@ __global__ __launch_bounds__(256) void split_kernel(Fp4Params p, int ntiles) {
                 const int chunk = (l & 7) ^ swizzle(8 * i + lr);
                 const uint32_t byte = (uint32_t)panel * kRowBytes + 16u * (uint32_t)chunk;
                 const bool ok = live && byte < (uint32_t)rb;
-                load_lds16(rsrc, at + 1024u * (uint32_t)i, ok ? (uint32_t)(8 * i + lr) * (uint32_t)rb + byte : kOOB);
+                load16(rsrc, at + 1024u * (uint32_t)i, ok ? (uint32_t)(8 * i + lr) * (uint32_t)rb + byte : kOOB);
             }
         };
         rows_of(rw, base, 2 * NT);
         rows_of(rx, base + R::W, 2 * MT);
-        const i32x4 rws = make_rsrc_v(ws0 + (size_t)(live ? panel : 0) * p.n * 8, (uint32_t)cols * 8u);
-        const i32x4 rxs = make_rsrc_v(xs0 + (size_t)(live ? panel : 0) * p.m * 8, (uint32_t)rows * 8u);
+        i32x4 rws = make_rsrc_v(ws0 + (size_t)(live ? panel : 0) * p.n * 8, (uint32_t)cols * 8u);
+        i32x4 rxs = make_rsrc_v(xs0 + (size_t)(live ? panel : 0) * p.m * 8, (uint32_t)rows * 8u);
+        asm volatile("s_nop 4" : "+s"(rws), "+s"(rxs));   // five states between writing a descriptor and a load that reads it
 #pragma unroll
-        for (int i = 0; i < (NT + 1) / 2; ++i) load_lds4(rws, base + R::W + R::X + 256u * i, live ? 256u * i + 4u * l : kOOB);
+        for (int i = 0; i < (NT + 1) / 2; ++i) load4(rws, base + R::W + R::X + 256u * i, live ? 256u * i + 4u * l : kOOB);
 #pragma unroll
-        for (int i = 0; i < (MT + 1) / 2; ++i) load_lds4(rxs, base + R::W + R::X + R::WS + 256u * i, live ? 256u * i + 4u * l : kOOB);
+        for (int i = 0; i < (MT + 1) / 2; ++i) load4(rxs, base + R::W + R::X + R::WS + 256u * i, live ? 256u * i + 4u * l : kOOB);
     };
 
     f32x4 acc[MT][NT];
@@ -271,6 +282,320 @@ hipError_t launch_split(const Fp4Params& p, hipStream_t s) {
     return launch_split_per<MT, NT, D, 16>(p, grid, nt, s);
 }
 
+// Tile kernel: 256 x 256 tiles, four waves of 128 x 128 (4 x 4 blocks of 32x32x64 instructions, the results
+// in 256 accumulator registers), one workgroup a CU, each walking its tiles as one stream of panels (256
+// along k).  A panel is 128 bytes of each of the tile's 512 rows, one cache line a row, and 4 KiB of scales,
+// in one of two LDS slots.  While the instructions of panel c run, from registers, the operands of panel
+// c + 1 come out of their slot into the registers that panel c has done with, and panel c + 2 is loaded into
+// panel c's slot, which was emptied before panel c began: a load has all but the first MFMAs of a panel to
+// arrive.  The stream runs on into the workgroup's next tile, so a tile begins with its first panel in
+// registers and its second in LDS, and the results of the tile before leave meanwhile.
+namespace tile {
+constexpr int BM = 256, BN = 256, NT = 256, MI = 4, NJ = 4, SUB = 4;   // SUB: instructions along k of a panel
+constexpr int OPER = 256 * kRowBytes;     // one operand's slot
+constexpr int SC = 256 * 8;               // one operand's scales of a panel
+constexpr int LOADS = 20;                 // a wave's loads of a panel: 8 + 8 of eight rows, 4 of 256 bytes of scales
+struct alignas(16) Smem {
+    uint8_t a[2][OPER];
+    uint8_t b[2][OPER];
+    uint8_t sc[2][2 * SC];                // row scales, column scales
+    Tables tab;
+};
+
+// A wave-uniform value in a scalar register.  (Where the compiler knows a value to be uniform it folds
+// readfirstlane away; a value read from LDS, or one carried around a loop, then stays in vector registers, and
+// with it the descriptors that the loads below need in scalar ones.  So the value is made opaque first.)
+__device__ inline int scalar(int v) {
+    asm volatile("" : "+v"(v));
+    return __builtin_amdgcn_readfirstlane(v);
+}
+
+// the largest h with tile_off[h] <= t (find_group, in two steps of one read a lane)
+__device__ inline int find_group_wave(const int* tile_off, int g, int t) {
+    const int l = threadIdx.x & 63;
+    const int c = tile_off[min(16 * l, g)];
+    const int blk = __popcll(__ballot(16 * l < g && c <= t)) - 1;
+    const int h = 16 * blk + (l & 15);
+    const int f = tile_off[min(h, g)];
+    return __builtin_amdgcn_readfirstlane(16 * blk + __popcll(__ballot(l < 16 && h < g && f <= t)) - 1);
+}
+
+template <typename OutT, bool PAIRS>
+__global__ __launch_bounds__(NT, 1) void kernel(Fp4Params p) {
+    __shared__ Smem sm;
+    const int t = threadIdx.x, l = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    const int r0w = 128 * (wave >> 1), c0w = 128 * (wave & 1);
+    const int ntn = cdiv(p.n, BN);
+    int gemm_tiles, covered;
+    build_tables<NT>(p.group_sizes, p.g, p.m, BM, ntn, sm.tab, &gemm_tiles, &covered);
+    gemm_tiles = scalar(gemm_tiles);
+    covered = scalar(covered);
+    if (blockIdx.x == 0 && t == 0) *p.status = sm.tab.flags;
+    const int rb = p.k >> 1, panels = (p.k + kPanel - 1) / kPanel;
+    OutT* const out = (OutT*)p.out;
+    const int first = xcd_virtual_id(blockIdx.x, gridDim.x);
+
+    struct Info { int row0, rows, col0; };
+    // the load stream's tile: rows, weights, and the scales this wave loads, as the parts of descriptors (whole
+    // ones, carried around the loop, end up in vector registers)
+    struct Desc {
+        int lo, hi, bytes;
+        __device__ void set(const void* base, uint32_t n) {
+            lo = (int)(uint32_t)(uintptr_t)base;
+            hi = (int)((uint32_t)((uintptr_t)base >> 32) & 0xffffu);
+            bytes = (int)n;
+        }
+        __device__ i32x4 get() const { return i32x4{lo, hi, bytes, kRsrcWord3}; }
+        // into scalar registers (five states before a load may read them)
+        __device__ void pin() { lo = scalar(lo); hi = scalar(hi); bytes = scalar(bytes); asm volatile("s_nop 4"); }
+    };
+    Desc ra, rw, rs;
+    auto decode = [&](int tile) {
+        const int grp = find_group_wave(sm.tab.tile_off, p.g, tile);
+        const int local = tile - scalar(sm.tab.tile_off[grp]);
+        int row0 = scalar(sm.tab.row_off[grp]);
+        const int size = scalar(sm.tab.row_off[grp + 1]) - row0;
+        const int mtg = cdiv(size, BM);
+        int mt, nt;
+        if (size <= p.n) { mt = local % mtg; nt = local / mtg; }   // neighbours share the larger operand
+        else { nt = local % ntn; mt = local / ntn; }
+        Info i{row0 + mt * BM, min(BM, size - mt * BM), nt * BN};
+        ra.set(p.lhs + (size_t)i.row0 * rb, (uint32_t)i.rows * (uint32_t)rb);
+        rw.set(p.rhs + ((size_t)grp * p.n + i.col0) * rb, (uint32_t)min(BN, p.n - i.col0) * (uint32_t)rb);
+        // a panel's scales of rows past the tile belong to rows that are not stored
+        const uint8_t* s = wave < 2 ? p.lhs_scale + (size_t)i.row0 * 8 : p.rhs_scale + ((size_t)grp * panels * p.n + i.col0) * 8;
+        const int rows = wave < 2 ? p.m : p.n, at = wave < 2 ? i.row0 : i.col0;
+        rs.set(s, ((uint32_t)panels * (uint32_t)rows - (uint32_t)at) * 8u);
+        return i;
+    };
+
+    // Load number d of the stream's panel lp: d < 8 rows 64 wave + 8 d .. + 7, d < 16 the same of the weights,
+    // then the scales.  Lane l brings row l / 8 of the eight, chunk (l % 8) ^ swizzle(row); the swizzle of row
+    // 64 wave + 8 d + l / 8 is (4 d + l / 16) % 8.  v: lane offsets for even and odd d; in a last panel that k
+    // does not fill, the chunks past k are out of range and read as zeros.
+    const int lc = (l & 7) ^ (l >> 4);
+    const uint32_t v0 = (uint32_t)(l >> 3) * (uint32_t)rb + 16u * (uint32_t)lc, v1 = (uint32_t)(l >> 3) * (uint32_t)rb + 16u * (uint32_t)(lc ^ 4);
+    const int in_last = rb - (panels - 1) * kRowBytes;   // code bytes of the last panel
+    const uint32_t vt0 = 16 * lc < in_last ? v0 : kOOB, vt1 = 16 * (lc ^ 4) < in_last ? v1 : kOOB;
+    const uint32_t lds_a = lds_u32(&sm.a[0][0]), lds_b = lds_u32(&sm.b[0][0]), lds_s = lds_u32(&sm.sc[0][0]);
+    const uint32_t srows = (uint32_t)(wave < 2 ? p.m : p.n) * 8u;
+    uint32_t lslot = 0, past = 0;   // past: set once the stream has no more tiles, its loads then read nothing
+    auto issue = [&](auto d_c, int lp) {
+        constexpr int d = decltype(d_c)::value;
+        if constexpr (d < 16) {
+            const bool last = lp == panels - 1;
+            const uint32_t v = d & 1 ? (last ? vt1 : v1) : (last ? vt0 : v0);
+            const uint32_t s = (uint32_t)(64 * wave + 8 * (d & 7)) * (uint32_t)rb + (uint32_t)lp * kRowBytes + past;
+            load16(d < 8 ? ra.get() : rw.get(), (d < 8 ? lds_a : lds_b) + lslot * OPER + (uint32_t)(8 * wave + (d & 7)) * 1024u, v + s);
+        } else {
+            // (4 bytes a lane: the last panel of an odd number of rows ends 8 bytes into a 16-byte piece)
+            constexpr uint32_t e = 256u * (d - 16);
+            load4(rs.get(), lds_s + lslot * (2 * SC) + (uint32_t)wave * 1024u + e, (uint32_t)lp * srows + past + (uint32_t)(wave & 1) * 1024u + e + 4u * (uint32_t)l);
+        }
+    };
+
+    // Fragments: lane l holds row l % 32 of a block and k blocks 4 (l / 32) + sub of the panel, one chunk and
+    // one scale byte each; the four scale bytes are one word.  The chunk's place is (4 (l / 32) + sub) ^
+    // swizzle(l), so a sub-slice's and a slot's address differ from the lane's own in single bits, and the
+    // blocks of 32 rows by constants.
+    const int h = l >> 5;
+    const uint32_t chunk0 = (uint32_t)((4 * h) ^ ((l >> 1) & 7)) << 4;
+    const uint32_t la = (uint32_t)(r0w + (l & 31)) * kRowBytes + chunk0, lb = (uint32_t)(c0w + (l & 31)) * kRowBytes + chunk0;
+    const uint32_t lsa = lds_s + (uint32_t)(r0w + (l & 31)) * 8u + 4u * (uint32_t)h, lsb = lds_s + SC + (uint32_t)(c0w + (l & 31)) * 8u + 4u * (uint32_t)h;
+    i32x4 fa[SUB][MI], fb[SUB][NJ];
+    int sa[MI], sb[NJ], na[MI], nb_[NJ];
+    uint32_t rslot = 0, aa = 0, ab = 0;   // the slot that is read, and the addresses of the sub-slice that is
+    auto aim = [&](int s) {
+        const uint32_t k = rslot * OPER ^ (uint32_t)(s << 4);
+        aa = lds_a + (la ^ k);
+        ab = lds_b + (lb ^ k);
+        asm volatile("" : "+v"(aa), "+v"(ab));   // kept as one address each, or every block's is computed and held
+    };
+    auto read_a = [&](int s, int i) { fa[s][i] = *(const __attribute__((address_space(3))) i32x4*)(uintptr_t)(aa + (uint32_t)(32 * i * kRowBytes)); };
+    auto read_b = [&](int s, int j) { fb[s][j] = *(const __attribute__((address_space(3))) i32x4*)(uintptr_t)(ab + (uint32_t)(32 * j * kRowBytes)); };
+    const int tail_valid = (p.k >> 5) - 8 * (panels - 1) - 4 * h;
+    auto aim_scales = [&] {
+        aa = lsa + rslot * (2 * SC);
+        ab = lsb + rslot * (2 * SC);
+        asm volatile("" : "+v"(aa), "+v"(ab));
+    };
+    auto read_sa = [&](int i) { na[i] = *(const __attribute__((address_space(3))) int*)(uintptr_t)(aa + (uint32_t)(32 * i * 8)); };
+    auto read_sb = [&](int j) { nb_[j] = *(const __attribute__((address_space(3))) int*)(uintptr_t)(ab + (uint32_t)(32 * j * 8)); };
+    auto take_scales = [&](int panel) {   // of the panel whose fragments were read last
+        const uint32_t keep = panel == panels - 1 ? keep_bytes(~0u, tail_valid) : ~0u;
+#pragma unroll
+        for (int i = 0; i < MI; ++i) sa[i] = na[i] & (int)keep;
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) sb[j] = nb_[j] & (int)keep;
+    };
+    // the slot read last is empty and the panel after it has arrived, for every wave
+    auto turn = [&] {
+        __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0), known to the compiler
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    };
+
+    f32x16 acc[MI][NJ];
+    if (first < gemm_tiles) {
+        Info cur = decode(first);
+        auto issue_all = [&](int lp) {
+            asm volatile("" : "+s"(lp));   // (or the offsets of a fixed panel are all computed ahead and held)
+            static_for<0, LOADS>([&](auto d_c) { issue(d_c, lp); });
+            lslot ^= 1;
+        };
+        issue_all(0);
+        issue_all(1);
+        wait_vm<LOADS>();
+        lds_barrier();
+        static_for<0, SUB>([&](auto s_c) {
+            aim(s_c);
+            static_for<0, MI>([&](auto i_c) { read_a(s_c, i_c); });
+            static_for<0, NJ>([&](auto j_c) { read_b(s_c, j_c); });
+        });
+        aim_scales();
+        static_for<0, MI>([&](auto i_c) { read_sa(i_c); });
+        static_for<0, NJ>([&](auto j_c) { read_sb(j_c); });
+        turn();
+        take_scales(0);
+        rslot = 1;
+        issue_all(2);
+        for (int tile = first; tile < gemm_tiles;) {
+        Info next = cur;
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int j = 0; j < NJ; ++j)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+        const int blocks = max(0, min(MI, cdiv(cur.rows - r0w, 32)));
+        tile += gridDim.x;
+        with_nb<2>((blocks + 1) >> 1, [&](auto nb_c) {
+            constexpr int NB = 2 * decltype(nb_c)::value;
+            // One panel: 16 steps a sub-slice, each at most one MFMA and the reads and loads that go with it.
+            // FIRST: the tile's first panel, whose turn and loads are done already.  lp: the panel to load.
+            auto panel = [&](auto first_c, int at, int lp) {
+                constexpr bool FIRST = decltype(first_c)::value;
+                static_for<0, SUB>([&](auto s_c) {
+                    constexpr int S = decltype(s_c)::value;
+                    static_for<0, 16>([&](auto m_c) {
+                        constexpr int M = decltype(m_c)::value;
+                        // (A0 A1) x (B0 B1), x (B2 B3), (A2 A3) x (B2 B3), x (B0 B1): fragments are done with in pairs
+                        constexpr int Q = M >> 2, I = 2 * (Q >> 1) + ((M >> 1) & 1), J = 2 * (Q == 1 || Q == 2) + (M & 1);
+                        if constexpr (I < NB)
+                            acc[I][J] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(widen(fa[S][I]), widen(fb[S][J]), acc[I][J], kFp4, kFp4, S, sa[I], S, sb[J]);
+                        if constexpr (!FIRST) {
+                            if constexpr (S == 0 && M == 3) turn();
+                            if constexpr (S == 0 && M >= 4) issue(std::integral_constant<int, M - 4>{}, lp);
+                            if constexpr (S == 1 && M < LOADS - 12) issue(std::integral_constant<int, 12 + M>{}, lp);
+                        }
+                        // the next panel's sub-slice S - 1, with the last of them its scales and, as the
+                        // registers come free, its last sub-slice
+                        if constexpr (S > 0 && S < 3) {
+                            if constexpr (M == 0) aim(S - 1);
+                            if constexpr (M & 1) {
+                                if constexpr (M < 8) read_a(S - 1, M >> 1);
+                                else read_b(S - 1, (M >> 1) - 4);
+                            }
+                        }
+                        if constexpr (S == 3) {
+                            if constexpr (M == 0) aim(2);
+                            if constexpr (M < 4) { read_a(2, M); read_b(2, M); }
+                            if constexpr (M == 4) aim_scales();
+                            if constexpr (M >= 4 && M < 8) { read_sa(M - 4); read_sb(M - 4); }
+                            if constexpr (M == 8) { aim(3); read_a(3, 0); read_a(3, 1); }
+                            if constexpr (M == 12) { read_b(3, 2); read_b(3, 3); }
+                            if constexpr (M == 15) { read_a(3, 2); read_a(3, 3); read_b(3, 0); read_b(3, 1); }
+                        }
+                        __builtin_amdgcn_sched_barrier(0);
+                    });
+                });
+                take_scales(at + 1 == panels ? 0 : at + 1);
+                rslot ^= 1;
+                if constexpr (!FIRST) lslot ^= 1;
+            };
+            panel(std::true_type{}, 0, 0);
+            // panels 1 .. P - 3 load this tile's panels 3 .. P - 1, the last two the next tile's first two
+            int at = 1, lp = 3;
+            for (int half = 0; half < 2; ++half) {
+                ra.pin(); rw.pin(); rs.pin();
+                for (const int end = half ? panels : panels - 2; at < end; ++at, ++lp) panel(std::false_type{}, at, lp);
+                if (half == 0) {
+                    lp = 0;
+                    if (tile < gemm_tiles) next = decode(tile);
+                    else past = kOOB;
+                }
+            }
+        });
+        turn();
+        ra.pin(); rw.pin(); rs.pin();
+        issue_all(2);
+        // Results: element 4 q + u of a block is row 8 q + 4 h + u, column l % 32.  For bf16, two rows are rounded
+        // into one register and exchanged with the neighbouring column's, so that a lane stores two columns of one
+        // row (PAIRS: n even and the output 4-byte aligned); fp32 columns are contiguous over the lanes as they are.
+        // One address a block column and lane; the rows of a store are a scalar away.
+        constexpr bool TWO = sizeof(OutT) == 2 && PAIRS;
+        const rsrc_t ro = make_rsrc(out + (size_t)cur.row0 * p.n, (uint32_t)cur.rows * (uint32_t)p.n * (uint32_t)sizeof(OutT));
+        const int odd = TWO ? l & 1 : 0;
+        const uint32_t pick = odd ? 0x03020706u : 0x05040100u;   // v_perm of (received, own)
+        const uint32_t row_bytes = (uint32_t)p.n * (uint32_t)sizeof(OutT);
+        uint32_t at[NJ];
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+            const int col = cur.col0 + c0w + 32 * j + (l & 31);
+            at[j] = col < p.n ? (uint32_t)(r0w + 4 * h + odd) * row_bytes + (uint32_t)(col - odd) * (uint32_t)sizeof(OutT) : kOOB;
+            asm volatile("" : "+v"(at[j]));
+        }
+        static_for<0, MI>([&](auto i_c) {
+            constexpr int i = decltype(i_c)::value;
+            if (i >= blocks) return;
+            static_for<0, 4>([&](auto q_c) {
+                constexpr int q = decltype(q_c)::value;
+#pragma unroll
+                for (int u = 0; u < 4; u += TWO ? 2 : 1) {
+                    uint32_t down = (uint32_t)(32 * i + 8 * q + u) * row_bytes;
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j) {
+                        const float v = acc[i][j][4 * q + u];
+                        if constexpr (TWO) {
+                            const uint32_t own = pack_bf16(v, acc[i][j][4 * q + u + 1]);
+                            const uint32_t got = (uint32_t)__builtin_amdgcn_mov_dpp((int)own, 0xB1, 0xF, 0xF, true);   // lanes 2 i and 2 i + 1 swapped
+                            __builtin_amdgcn_raw_buffer_store_b32(__builtin_amdgcn_perm(got, own, pick), ro, at[j] + down, 0, 0);
+                        } else if constexpr (sizeof(OutT) == 2) {
+                            __builtin_amdgcn_raw_buffer_store_b16((uint16_t)pack_bf16(v, 0.f), ro, at[j] + down, 0, 0);
+                        } else {
+                            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), ro, at[j] + down, 0, 0);
+                        }
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            });
+        });
+        cur.row0 = scalar(next.row0); cur.rows = scalar(next.rows); cur.col0 = scalar(next.col0);
+    }
+    wait_vm<0>();   // no load may still be writing LDS when the workgroup ends
+    }
+    // rows past the groups' total
+    const size_t lo = (size_t)covered * p.n, hi = (size_t)p.m * p.n;
+    for (size_t i = lo + (size_t)blockIdx.x * NT + t; i < hi; i += (size_t)gridDim.x * NT) store1(out + i, 0.f);
+}
+}  // namespace tile
+
+// 32-bit offsets of the tile kernel's descriptors, and at least three panels
+inline bool tile_ok(const Fp4Params& p) {
+    const int64_t panels = (p.k + kPanel - 1) / kPanel;
+    const int64_t tiles = ((int64_t)p.m / tile::BM + p.g + 1) * ((p.n + tile::BN - 1) / tile::BN);
+    return p.k > 2 * kPanel && (int64_t)256 * (p.k >> 1) < (int64_t(1) << 30) && (int64_t)256 * p.n * 4 < (int64_t(1) << 31) &&
+           panels * p.m * 8 < (int64_t(1) << 31) && panels * p.n * 8 < (int64_t(1) << 31) && tiles < (int64_t(1) << 30);
+}
+
+inline hipError_t launch_tile(const Fp4Params& p, int cus, hipStream_t s) {
+    const int64_t tiles = ((int64_t)p.m / tile::BM + (p.g < p.m ? p.g : p.m)) * ((p.n + tile::BN - 1) / tile::BN);
+    const int grid = (int)(tiles < cus ? (tiles < 1 ? 1 : tiles) : cus);
+    if (p.out_f32) hipLaunchKernelGGL((tile::kernel<float, false>), dim3(grid), dim3(tile::NT), 0, s, p);
+    else if (p.n % 2 == 0 && (uintptr_t)p.out % 4 == 0) hipLaunchKernelGGL((tile::kernel<uint16_t, true>), dim3(grid), dim3(tile::NT), 0, s, p);
+    else hipLaunchKernelGGL((tile::kernel<uint16_t, false>), dim3(grid), dim3(tile::NT), 0, s, p);
+    return hipGetLastError();
+}
+
 }  // namespace fp4
 
 bool ragged_m_fp4_grid_ok(const Fp4Params& p) {
@@ -279,8 +604,8 @@ bool ragged_m_fp4_grid_ok(const Fp4Params& p) {
 }
 
 hipError_t launch_ragged_m_fp4(const Fp4Params& p, int cus, hipStream_t s) {
-    (void)cus;
     const int64_t per = p.m / p.g;
+    if (per > 48 && fp4::tile_ok(p)) return fp4::launch_tile(p, cus, s);
     if (per <= 4) return fp4::launch_split<1, 1, 4>(p, s);
     return fp4::launch_split<2, 2, 2>(p, s);
 }

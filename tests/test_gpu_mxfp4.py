@@ -209,6 +209,34 @@ def test_product(case, out_dtype):
     check_product(lc, lp, rc, rp, gs, out_dtype)
 
 
+TILES = [
+    # long groups: whole tiles, partly filled ones, k of three panels and more, with and without a part panel
+    (1000, 768, 512, [1000], BF),
+    (1000, 1056, 511, [256, 500, 0, 31, 213], BF),
+    (700, 2880, 96, [130, 470, 90], BF),
+    (700, 544, 260, [700], F32),
+    (2700, 1024, 6000, [2560, 0, 140], BF),          # more tiles than compute units: several a workgroup
+    (5000, 800, 2100, [1, 1024, 77, 1500, 0, 33, 300, 2000], F32),
+    (300, 7168, 300, [290], BF),
+]
+
+
+@pytest.mark.parametrize("case", range(len(TILES)))
+def test_product_tiles(case):
+    m, k, n, gs, out_dtype = TILES[case]
+    say("tiles", TILES[case])
+    check_product(*operands(np.random.default_rng(70 + case), m, k, n, len(gs)), gs, out_dtype)
+
+
+def test_product_tiles_of_many_groups():
+    say("tiles of many groups")
+    r = np.random.default_rng(80)
+    gs = r.integers(0, 110, 300)
+    gs[r.random(300) < 0.1] = 0
+    lc, lp, rc, rp = operands(r, int(gs.sum()) + 40, 800, 24, 300)
+    check_product(lc, lp, rc, rp, gs)
+
+
 @pytest.mark.parametrize("tokens", [3, 40, 700])
 @pytest.mark.parametrize("g", [65, 300, 1024])
 def test_product_many_groups(g, tokens):
