@@ -104,10 +104,13 @@ __device__ inline RowTile find_row_tile(const int32_t* __restrict__ sizes, int g
     return r;
 }
 
+// row tiles (and tiles of rows past the total) that any group_sizes can give
+inline int64_t slot_bound(const Fp4Params& p, int tile_rows) { return (p.g < p.m ? p.g : p.m) + (int64_t)p.m / tile_rows + 1; }
+
 // scale bytes of k blocks at and past `valid` (of the four in the word) cleared
 __device__ inline uint32_t keep_bytes(uint32_t w, int valid) { return valid >= 4 ? w : valid <= 0 ? 0u : w & ((1u << (8 * valid)) - 1u); }
 
-__device__ inline void store1(uint16_t* p, float v) { *p = f32_to_bf16(v); }
+__device__ inline void store1(uint16_t* p, float v) { *p = (uint16_t)pack_bf16(v, 0.f); }
 __device__ inline void store1(float* p, float v) { *p = v; }
 
 // Four consecutive columns of one row; `left` = columns of the row from here on.
@@ -269,9 +272,6 @@ hipError_t launch_split_per(const Fp4Params& p, int64_t grid, int ntiles, hipStr
     return hipGetLastError();
 }
 
-// row tiles (and tiles of rows past the total) that any group_sizes can give
-inline int64_t slot_bound(const Fp4Params& p, int tile_rows) { return (p.g < p.m ? p.g : p.m) + (int64_t)p.m / tile_rows + 1; }
-
 template <int MT, int NT, int D>
 hipError_t launch_split(const Fp4Params& p, hipStream_t s) {
     const int ntiles = (p.n + 16 * NT - 1) / (16 * NT);
@@ -281,6 +281,154 @@ hipError_t launch_split(const Fp4Params& p, hipStream_t s) {
     if (p.g <= 256) return launch_split_per<MT, NT, D, 4>(p, grid, nt, s);
     return launch_split_per<MT, NT, D, 16>(p, grid, nt, s);
 }
+
+// Stream kernel, for few rows a group: a workgroup holds the rows of one row tile (up to 16, all of k) in LDS
+// and its four waves each stream weights past them, 16 columns (a column tile) at a time, through a private
+// LDS ring of D panels (2 KiB of codes and their scales, loaded straight into LDS).  A wave's stream runs
+// through its column tiles without a stop and without a barrier; results leave as each tile ends.  Bound by
+// memory: what counts is the bytes in flight, 4 D panels of 2 KiB a workgroup and two workgroups or more a CU.
+namespace stream {
+constexpr int WAVES = 4;
+constexpr int WPANEL = 16 * kRowBytes, SLOT = WPANEL + 256;   // scales: 128 bytes, loaded 4 bytes a lane
+constexpr int LOADS = 3;
+
+template <int D, int XCAP, int PER, typename OutT>
+__global__ __launch_bounds__(64 * WAVES) void kernel(Fp4Params p, int splits, int xrows) {
+    // rows: panel by panel [xrows][128 bytes], then scales [panels][16][8]; 1 KiB of slack, as lanes of rows
+    // that are not there (their results are not stored) read on
+    __shared__ __attribute__((aligned(16))) uint8_t smem[WAVES * D * SLOT + XCAP + 1024];
+    const int t = threadIdx.x, l = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    // split c of every row tile runs on XCD c % 8 (a group's row tiles share their weights in its L2)
+    const int idx = blockIdx.x >> 3, per = splits >> 3;
+    const int slot = idx / per, split = (idx % per) * 8 + (blockIdx.x & 7);
+    uint32_t flags;
+    const RowTile rt = find_row_tile<PER>(p.group_sizes, p.g, p.m, 16, slot, &flags);
+    if (blockIdx.x == 0 && t == 0) *p.status = flags;
+    if (rt.grp == -1) return;
+    OutT* out = (OutT*)p.out;
+    const int nct = (p.n + 15) >> 4;
+    const int ct0 = (int)((int64_t)split * nct / splits), ct1 = (int)((int64_t)(split + 1) * nct / splits);
+    if (rt.grp == -2) {
+        const int c0 = 16 * ct0, width = min(16 * ct1, p.n) - c0;
+        for (int i = t; i < width * rt.rows; i += 64 * WAVES) store1(out + (size_t)(rt.row0 + i / width) * p.n + c0 + i % width, 0.f);
+        return;
+    }
+    const int rows = rt.rows, panels = (p.k + kPanel - 1) / kPanel, rb = p.k >> 1;
+    uint8_t* xl = smem + WAVES * D * SLOT;
+    uint8_t* xs = xl + panels * xrows * kRowBytes;
+
+    // the wave's stream of (column tile, panel)
+    const int tiles = ct1 - ct0 > wave ? (ct1 - ct0 - wave + WAVES - 1) / WAVES : 0;
+    const uint32_t ring0 = lds_u32(smem) + (uint32_t)(wave * D * SLOT);
+    const uint8_t* mine = smem + wave * D * SLOT;
+    const int lr = l >> 3;
+    const uint32_t byte0 = 16u * (uint32_t)((l & 7) ^ swizzle(lr)), byte1 = 16u * (uint32_t)((l & 7) ^ swizzle(8 + lr));
+    const uint8_t* const wbase = p.rhs + (size_t)rt.grp * p.n * rb;
+    const uint8_t* const sbase = p.rhs_scale + (size_t)rt.grp * panels * p.n * 8;
+    int lc = 0, lp = 0;   // tile and panel to load next
+    auto load = [&](int s) {
+        const int col = 16 * (ct0 + wave + WAVES * lc), cols = min(16, p.n - col);
+        const bool live = lc < tiles;
+        i32x4 rw = make_rsrc_v(wbase + (size_t)(live ? col : 0) * rb, live ? (uint32_t)cols * (uint32_t)rb : 0u);
+        i32x4 rs = make_rsrc_v(sbase + ((size_t)lp * p.n + (live ? col : 0)) * 8, live ? (uint32_t)cols * 8u : 0u);
+        asm volatile("s_nop 4" : "+s"(rw), "+s"(rs));   // five states between writing a descriptor and a load that reads it
+        const uint32_t at = ring0 + (uint32_t)(s * SLOT), pb = (uint32_t)lp * kRowBytes;
+        const bool ok0 = pb + byte0 < (uint32_t)rb, ok1 = pb + byte1 < (uint32_t)rb;   // chunks past k
+        load16(rw, at, ok0 ? (uint32_t)lr * (uint32_t)rb + pb + byte0 : kOOB);
+        load16(rw, at + 1024u, ok1 ? (uint32_t)(8 + lr) * (uint32_t)rb + pb + byte1 : kOOB);
+        load4(rs, at + WPANEL, 4u * (uint32_t)l);
+        if (++lp == panels) { lp = 0; ++lc; }
+    };
+#pragma unroll
+    for (int s = 0; s < D; ++s) load(s);
+
+    // the rows, once
+    {
+        i32x4 rx = make_rsrc_v(p.lhs + (size_t)rt.row0 * rb, (uint32_t)rows * (uint32_t)rb);
+        asm volatile("s_nop 4" : "+s"(rx));
+        const uint32_t x0 = lds_u32(xl);
+        for (int i = wave; i < panels * (xrows >> 3); i += WAVES) {
+            const int panel = xrows == 8 ? i : i >> 1, half = xrows == 8 ? 0 : i & 1;
+            const uint32_t b = (uint32_t)panel * kRowBytes + (half ? byte1 : byte0);
+            load16(rx, x0 + 1024u * (uint32_t)i, b < (uint32_t)rb ? (uint32_t)(8 * half + lr) * (uint32_t)rb + b : kOOB);
+        }
+        for (int i = t; i < panels * 16; i += 64 * WAVES) {
+            const int r = i & 15;
+            uint64_t v = 0;
+            if (r < rows) v = *(const uint64_t*)(p.lhs_scale + ((size_t)(i >> 4) * p.m + rt.row0 + r) * 8);
+            *(uint64_t*)(xs + 8 * i) = v;
+        }
+        wait_vm<0>();
+        __syncthreads();
+    }
+
+    const int r = l & 15, q = l >> 4;
+    const uint32_t c0 = (uint32_t)(((2 * q) ^ swizzle(r)) << 4), c1 = c0 ^ 16u;   // chunks 2 q and 2 q + 1 of row r
+    const bool vec = (p.n & 3) == 0 && ((uintptr_t)p.out & (4 * sizeof(OutT) - 1)) == 0;
+    int s = 0;
+    for (int c = 0; c < tiles; ++c) {
+        f32x4 acc0 = {0.f, 0.f, 0.f, 0.f}, acc1 = {0.f, 0.f, 0.f, 0.f};
+        for (int panel = 0; panel < panels; ++panel) {
+            wait_vm<LOADS * (D - 1)>();   // the oldest panel is in LDS
+            const uint8_t* w = mine + s * SLOT + r * kRowBytes;
+            const uint8_t* x = xl + panel * (xrows * kRowBytes) + r * kRowBytes;
+            const i32x4 w0 = *(const i32x4*)(w + c0), w1 = *(const i32x4*)(w + c1);
+            const i32x4 y0 = *(const i32x4*)(x + c0), y1 = *(const i32x4*)(x + c1);
+            const int valid = (p.k >> 5) - panel * 8 - 2 * q;   // the lane's k blocks inside k
+            const uint32_t sw = keep_bytes(*(const uint16_t*)(mine + s * SLOT + WPANEL + r * 8 + 2 * q), valid);
+            const uint32_t sx = keep_bytes(*(const uint16_t*)(xs + (panel * 16 + r) * 8 + 2 * q), valid);
+            __builtin_amdgcn_s_waitcnt(0xc07f);   // the slot has been read (lgkmcnt(0)): it can be filled again
+            __builtin_amdgcn_sched_barrier(0);
+            load(s);
+            s = s + 1 == D ? 0 : s + 1;
+            acc0 = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(w0), widen(y0), acc0, kFp4, kFp4, 0, (int)sw, 0, (int)sx);
+            acc1 = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(w1), widen(y1), acc1, kFp4, kFp4, 1, (int)sw, 1, (int)sx);
+        }
+        const int col = 16 * (ct0 + wave + WAVES * c) + 4 * q;
+        if (r < rows && col < p.n) {
+            f32x4 v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = acc0[e] + acc1[e];
+            store4(out + (size_t)(rt.row0 + r) * p.n + col, v, p.n - col, vec);
+        }
+    }
+    wait_vm<0>();   // no load may still be writing LDS when the workgroup ends
+}
+
+constexpr int kMaxRowBytes = 63 * 1024;   // rows of one tile in LDS, the largest size built
+
+inline int row_bytes(const Fp4Params& p) {
+    const int panels = (p.k + kPanel - 1) / kPanel;
+    return panels * ((p.m <= 8 ? 8 : 16) * kRowBytes + 128);
+}
+
+template <int D, int XCAP, int PER>
+hipError_t launch_per(const Fp4Params& p, int64_t grid, int splits, int xrows, hipStream_t s) {
+    if (p.out_f32) hipLaunchKernelGGL((kernel<D, XCAP, PER, float>), dim3((uint32_t)grid), dim3(64 * WAVES), 0, s, p, splits, xrows);
+    else hipLaunchKernelGGL((kernel<D, XCAP, PER, uint16_t>), dim3((uint32_t)grid), dim3(64 * WAVES), 0, s, p, splits, xrows);
+    return hipGetLastError();
+}
+template <int D, int XCAP>
+hipError_t launch_d(const Fp4Params& p, int64_t grid, int splits, int xrows, hipStream_t s) {
+    if (p.g <= 64) return launch_per<D, XCAP, 1>(p, grid, splits, xrows, s);
+    if (p.g <= 256) return launch_per<D, XCAP, 4>(p, grid, splits, xrows, s);
+    return launch_per<D, XCAP, 16>(p, grid, splits, xrows, s);
+}
+
+inline hipError_t launch(const Fp4Params& p, int cus, hipStream_t s) {
+    const int nct = (p.n + 15) / 16;
+    const int64_t slots = slot_bound(p, 16);
+    // about eight workgroups a CU, none with fewer than a column tile a wave; a multiple of 8 (XCDs)
+    int64_t splits = (8 * (int64_t)cus + slots - 1) / slots;
+    if (splits > nct / WAVES) splits = nct / WAVES;
+    splits = splits < 8 ? 8 : (splits + 7) / 8 * 8;
+    const int64_t grid = slots * splits;
+    const int xrows = p.m <= 8 ? 8 : 16, bytes = row_bytes(p);
+    if (bytes <= 8 * 1024) return launch_d<4, 8 * 1024>(p, grid, (int)splits, xrows, s);
+    if (bytes <= 41 * 1024) return launch_d<4, 41 * 1024>(p, grid, (int)splits, xrows, s);
+    return launch_d<8, kMaxRowBytes>(p, grid, (int)splits, xrows, s);
+}
+}  // namespace stream
 
 // Tile kernel: 256 x 256 tiles, four waves of 128 x 128 (4 x 4 blocks of 32x32x64 instructions, the results
 // in 256 accumulator registers), one workgroup a CU, each walking its tiles as one stream of panels (256
@@ -606,7 +754,7 @@ bool ragged_m_fp4_grid_ok(const Fp4Params& p) {
 hipError_t launch_ragged_m_fp4(const Fp4Params& p, int cus, hipStream_t s) {
     const int64_t per = p.m / p.g;
     if (per > 48 && fp4::tile_ok(p)) return fp4::launch_tile(p, cus, s);
-    if (per <= 4) return fp4::launch_split<1, 1, 4>(p, s);
+    if (per <= 24 && p.k > 0 && fp4::stream::row_bytes(p) <= fp4::stream::kMaxRowBytes) return fp4::stream::launch(p, cus, s);
     return fp4::launch_split<2, 2, 2>(p, s);
 }
 

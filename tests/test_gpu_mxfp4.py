@@ -197,6 +197,11 @@ CASES = [
     (300, 512, 264, [0, 257, 0, 43]),
     (513, 1056, 520, [513]),
     (600, 768, 300, [255, 1, 256, 20, 60]),
+    (21, 7168, 70, [9, 0, 11]),
+    (8, 7168, 530, [1, 5, 2]),
+    (40, 4128, 1100, [16, 0, 23, 1]),
+    (3, 16384, 40, [1, 2]),
+    (2, 64, 4000, [0, 1, 0, 0, 1]),
 ]
 
 
