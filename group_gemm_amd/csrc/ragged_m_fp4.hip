@@ -442,6 +442,7 @@ namespace tile {
 constexpr int BM = 256, BN = 256, NT = 256, MI = 4, NJ = 4, SUB = 4;   // SUB: instructions along k of a panel
 constexpr int OPER = 256 * kRowBytes;     // one operand's slot
 constexpr int SC = 256 * 8;               // one operand's scales of a panel
+constexpr int ROT = 2;                    // panels between the starts of neighbouring column tiles
 constexpr int LOADS = 20;                 // a wave's loads of a panel: 8 + 8 of eight rows, 4 of 256 bytes of scales
 struct alignas(16) Smem {
     uint8_t a[2][OPER];
@@ -468,7 +469,8 @@ __device__ inline int find_group_wave(const int* tile_off, int g, int t) {
     return __builtin_amdgcn_readfirstlane(16 * blk + __popcll(__ballot(l < 16 && h < g && f <= t)) - 1);
 }
 
-template <typename OutT, bool PAIRS>
+// WHOLE: rows of the output are multiples of 16 bytes and aligned so
+template <typename OutT, bool WHOLE>
 __global__ __launch_bounds__(NT, 1) void kernel(Fp4Params p) {
     __shared__ Smem sm;
     const int t = threadIdx.x, l = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
@@ -483,7 +485,7 @@ __global__ __launch_bounds__(NT, 1) void kernel(Fp4Params p) {
     OutT* const out = (OutT*)p.out;
     const int first = xcd_virtual_id(blockIdx.x, gridDim.x);
 
-    struct Info { int row0, rows, col0; };
+    struct Info { int row0, rows, col0, turn0; };   // turn0: the panel that the tile begins with
     // the load stream's tile: rows, weights, and the scales this wave loads, as the parts of descriptors (whole
     // ones, carried around the loop, end up in vector registers)
     struct Desc {
@@ -507,7 +509,10 @@ __global__ __launch_bounds__(NT, 1) void kernel(Fp4Params p) {
         int mt, nt;
         if (size <= p.n) { mt = local % mtg; nt = local / mtg; }   // neighbours share the larger operand
         else { nt = local % ntn; mt = local / ntn; }
-        Info i{row0 + mt * BM, min(BM, size - mt * BM), nt * BN};
+        // Rows are a multiple of a large power of two apart, so that one panel of a tile lies in few of L2's
+        // channels: tiles side by side begin at different panels and go around, those with the same weights at
+        // the same one.
+        Info i{row0 + mt * BM, min(BM, size - mt * BM), nt * BN, (ROT * nt) % panels};
         ra.set(p.lhs + (size_t)i.row0 * rb, (uint32_t)i.rows * (uint32_t)rb);
         rw.set(p.rhs + ((size_t)grp * p.n + i.col0) * rb, (uint32_t)min(BN, p.n - i.col0) * (uint32_t)rb);
         // a panel's scales of rows past the tile belong to rows that are not stored
@@ -550,7 +555,7 @@ __global__ __launch_bounds__(NT, 1) void kernel(Fp4Params p) {
     const uint32_t chunk0 = (uint32_t)((4 * h) ^ ((l >> 1) & 7)) << 4;
     const uint32_t la = (uint32_t)(r0w + (l & 31)) * kRowBytes + chunk0, lb = (uint32_t)(c0w + (l & 31)) * kRowBytes + chunk0;
     const uint32_t lsa = lds_s + (uint32_t)(r0w + (l & 31)) * 8u + 4u * (uint32_t)h, lsb = lds_s + SC + (uint32_t)(c0w + (l & 31)) * 8u + 4u * (uint32_t)h;
-    i32x4 fa[SUB][MI], fb[SUB][NJ];
+    i32x4 fa[SUB][MI], fb[SUB][NJ], ta[MI], tb[NJ];   // ta, tb: the next panel's last sub-slice, which is read ahead of its turn
     int sa[MI], sb[NJ], na[MI], nb_[NJ];
     uint32_t rslot = 0, aa = 0, ab = 0;   // the slot that is read, and the addresses of the sub-slice that is
     auto aim = [&](int s) {
@@ -559,8 +564,8 @@ __global__ __launch_bounds__(NT, 1) void kernel(Fp4Params p) {
         ab = lds_b + (lb ^ k);
         asm volatile("" : "+v"(aa), "+v"(ab));   // kept as one address each, or every block's is computed and held
     };
-    auto read_a = [&](int s, int i) { fa[s][i] = *(const __attribute__((address_space(3))) i32x4*)(uintptr_t)(aa + (uint32_t)(32 * i * kRowBytes)); };
-    auto read_b = [&](int s, int j) { fb[s][j] = *(const __attribute__((address_space(3))) i32x4*)(uintptr_t)(ab + (uint32_t)(32 * j * kRowBytes)); };
+    auto read_a = [&](i32x4& f, int i) { f = *(const __attribute__((address_space(3))) i32x4*)(uintptr_t)(aa + (uint32_t)(32 * i * kRowBytes)); };
+    auto read_b = [&](i32x4& f, int j) { f = *(const __attribute__((address_space(3))) i32x4*)(uintptr_t)(ab + (uint32_t)(32 * j * kRowBytes)); };
     const int tail_valid = (p.k >> 5) - 8 * (panels - 1) - 4 * h;
     auto aim_scales = [&] {
         aa = lsa + rslot * (2 * SC);
@@ -582,142 +587,161 @@ __global__ __launch_bounds__(NT, 1) void kernel(Fp4Params p) {
         asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
     };
 
-    f32x16 acc[MI][NJ];
     if (first < gemm_tiles) {
         Info cur = decode(first);
-        auto issue_all = [&](int lp) {
+        auto issue_some = [&](auto b_c, auto e_c, int lp) {
             asm volatile("" : "+s"(lp));   // (or the offsets of a fixed panel are all computed ahead and held)
-            static_for<0, LOADS>([&](auto d_c) { issue(d_c, lp); });
+            static_for<decltype(b_c)::value, decltype(e_c)::value>([&](auto d_c) { issue(d_c, lp); });
+        };
+        auto issue_all = [&](int lp) {
+            issue_some(std::integral_constant<int, 0>{}, std::integral_constant<int, LOADS>{}, lp);
             lslot ^= 1;
         };
-        issue_all(0);
-        issue_all(1);
+        auto around = [&](int panel) { return panel < panels ? panel : panel - panels; };
+        issue_all(around(cur.turn0));
+        issue_all(around(cur.turn0 + 1));
         wait_vm<LOADS>();
         lds_barrier();
         static_for<0, SUB>([&](auto s_c) {
             aim(s_c);
-            static_for<0, MI>([&](auto i_c) { read_a(s_c, i_c); });
-            static_for<0, NJ>([&](auto j_c) { read_b(s_c, j_c); });
+            static_for<0, MI>([&](auto i_c) { read_a(s_c == SUB - 1 ? ta[i_c] : fa[s_c][i_c], i_c); });
+            static_for<0, NJ>([&](auto j_c) { read_b(s_c == SUB - 1 ? tb[j_c] : fb[s_c][j_c], j_c); });
         });
         aim_scales();
         static_for<0, MI>([&](auto i_c) { read_sa(i_c); });
         static_for<0, NJ>([&](auto j_c) { read_sb(j_c); });
         turn();
-        take_scales(0);
+        take_scales(cur.turn0);
         rslot = 1;
-        issue_all(2);
+        issue_all(around(cur.turn0 + 2));
         for (int tile = first; tile < gemm_tiles;) {
         Info next = cur;
-#pragma unroll
-        for (int i = 0; i < MI; ++i)
-#pragma unroll
-            for (int j = 0; j < NJ; ++j)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
         const int blocks = max(0, min(MI, cdiv(cur.rows - r0w, 32)));
         tile += gridDim.x;
         with_nb<2>((blocks + 1) >> 1, [&](auto nb_c) {
             constexpr int NB = 2 * decltype(nb_c)::value;
+            f32x16 acc[NB > 0 ? NB : 1][NJ];
             // One panel: 16 steps a sub-slice, each at most one MFMA and the reads and loads that go with it.
-            // FIRST: the tile's first panel, whose turn and loads are done already.  lp: the panel to load.
-            auto panel = [&](auto first_c, int at, int lp) {
+            // FIRST: the tile's first panel, whose turn and loads are done already.  follow: the panel after it,
+            // lp: the panel to load.
+            auto panel = [&](auto first_c, int follow, int lp) {
                 constexpr bool FIRST = decltype(first_c)::value;
                 static_for<0, SUB>([&](auto s_c) {
                     constexpr int S = decltype(s_c)::value;
                     static_for<0, 16>([&](auto m_c) {
                         constexpr int M = decltype(m_c)::value;
-                        // (A0 A1) x (B0 B1), x (B2 B3), (A2 A3) x (B2 B3), x (B0 B1): fragments are done with in pairs
-                        constexpr int Q = M >> 2, I = 2 * (Q >> 1) + ((M >> 1) & 1), J = 2 * (Q == 1 || Q == 2) + (M & 1);
-                        if constexpr (I < NB)
-                            acc[I][J] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(widen(fa[S][I]), widen(fb[S][J]), acc[I][J], kFp4, kFp4, S, sa[I], S, sb[J]);
+                        constexpr int I = M >> 2, J = M & 3;
+                        if constexpr (I < NB) {
+                            const f32x16 zero = {};
+                            // (the weights first, so that a lane holds columns of one row)
+                            acc[I][J] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(widen(fb[S][J]), widen(fa[S][I]), FIRST && S == 0 ? zero : acc[I][J], kFp4,
+                                                                                        kFp4, S, sb[J], S, sa[I]);
+                        }
+                        // the last sub-slice, read during the panel before, to its place
+                        if constexpr (S == 0 && M < 4) { fa[SUB - 1][M] = ta[M]; fb[SUB - 1][M] = tb[M]; }
                         if constexpr (!FIRST) {
                             if constexpr (S == 0 && M == 3) turn();
                             if constexpr (S == 0 && M >= 4) issue(std::integral_constant<int, M - 4>{}, lp);
                             if constexpr (S == 1 && M < LOADS - 12) issue(std::integral_constant<int, 12 + M>{}, lp);
                         }
-                        // the next panel's sub-slice S - 1, with the last of them its scales and, as the
-                        // registers come free, its last sub-slice
-                        if constexpr (S > 0 && S < 3) {
+                        // reads of the next panel: eight 16-byte ones a sub-slice, early in the last one, so that
+                        // none is on its way when the panel turns
+                        if constexpr (S == 0) {
+                            if constexpr (M == 4) aim(SUB - 1);
+                            if constexpr (M >= 4 && M < 8) read_a(ta[M - 4], M - 4);
+                            if constexpr (M >= 8 && M < 12) read_b(tb[M - 8], M - 8);
+                        } else {
+                            constexpr int T = S == 3 ? M : M >> 1;
                             if constexpr (M == 0) aim(S - 1);
-                            if constexpr (M & 1) {
-                                if constexpr (M < 8) read_a(S - 1, M >> 1);
-                                else read_b(S - 1, (M >> 1) - 4);
+                            if constexpr (S == 3 || (M & 1)) {
+                                if constexpr (T < 4) read_a(fa[S - 1][T & 3], T);
+                                else if constexpr (T < 8) read_b(fb[S - 1][T & 3], T - 4);
                             }
-                        }
-                        if constexpr (S == 3) {
-                            if constexpr (M == 0) aim(2);
-                            if constexpr (M < 4) { read_a(2, M); read_b(2, M); }
-                            if constexpr (M == 4) aim_scales();
-                            if constexpr (M >= 4 && M < 8) { read_sa(M - 4); read_sb(M - 4); }
-                            if constexpr (M == 8) { aim(3); read_a(3, 0); read_a(3, 1); }
-                            if constexpr (M == 12) { read_b(3, 2); read_b(3, 3); }
-                            if constexpr (M == 15) { read_a(3, 2); read_a(3, 3); read_b(3, 0); read_b(3, 1); }
+                            if constexpr (S == 3 && M == 8) aim_scales();
+                            if constexpr (S == 3 && M >= 8 && M < 12) { read_sa(M - 8); read_sb(M - 8); }
                         }
                         __builtin_amdgcn_sched_barrier(0);
                     });
                 });
-                take_scales(at + 1 == panels ? 0 : at + 1);
+                take_scales(follow);
                 rslot ^= 1;
                 if constexpr (!FIRST) lslot ^= 1;
             };
-            panel(std::true_type{}, 0, 0);
-            // panels 1 .. P - 3 load this tile's panels 3 .. P - 1, the last two the next tile's first two
-            int at = 1, lp = 3;
+            int follow = around(cur.turn0 + 1), lp = around(cur.turn0 + 2);
+            panel(std::true_type{}, follow, 0);
+            // the tile's panels but the first and the last two load the panel two after, the last two the next
+            // tile's first two
+            int left = panels - 3;
             for (int half = 0; half < 2; ++half) {
                 ra.pin(); rw.pin(); rs.pin();
-                for (const int end = half ? panels : panels - 2; at < end; ++at, ++lp) panel(std::false_type{}, at, lp);
+                for (; left > 0; --left) {
+                    follow = half && left == 1 ? next.turn0 : around(follow + 1);
+                    lp = around(lp + 1);
+                    panel(std::false_type{}, follow, lp);
+                }
                 if (half == 0) {
-                    lp = 0;
                     if (tile < gemm_tiles) next = decode(tile);
                     else past = kOOB;
+                    lp = next.turn0 - 1;
+                    left = 2;
                 }
             }
-        });
         turn();
         ra.pin(); rw.pin(); rs.pin();
-        issue_all(2);
-        // Results: element 4 q + u of a block is row 8 q + 4 h + u, column l % 32.  For bf16, two rows are rounded
-        // into one register and exchanged with the neighbouring column's, so that a lane stores two columns of one
-        // row (PAIRS: n even and the output 4-byte aligned); fp32 columns are contiguous over the lanes as they are.
-        // One address a block column and lane; the rows of a store are a scalar away.
-        constexpr bool TWO = sizeof(OutT) == 2 && PAIRS;
-        const rsrc_t ro = make_rsrc(out + (size_t)cur.row0 * p.n, (uint32_t)cur.rows * (uint32_t)p.n * (uint32_t)sizeof(OutT));
-        const int odd = TWO ? l & 1 : 0;
-        const uint32_t pick = odd ? 0x03020706u : 0x05040100u;   // v_perm of (received, own)
-        const uint32_t row_bytes = (uint32_t)p.n * (uint32_t)sizeof(OutT);
-        uint32_t at[NJ];
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-            const int col = cur.col0 + c0w + 32 * j + (l & 31);
-            at[j] = col < p.n ? (uint32_t)(r0w + 4 * h + odd) * row_bytes + (uint32_t)(col - odd) * (uint32_t)sizeof(OutT) : kOOB;
-            asm volatile("" : "+v"(at[j]));
-        }
-        static_for<0, MI>([&](auto i_c) {
-            constexpr int i = decltype(i_c)::value;
+        // The slot that has just been emptied takes the panel after the next: its rows and scales at once, its
+        // weights once the results have passed through their place (8 KiB a wave, the part that its own loads fill).
+        const int lp2 = around(next.turn0 + 2);
+        issue_some(std::integral_constant<int, 0>{}, std::integral_constant<int, 8>{}, lp2);
+        issue_some(std::integral_constant<int, 16>{}, std::integral_constant<int, LOADS>{}, lp2);
+        // Results: element 4 q + u of block (i, j) is row 32 i + l % 32, column 32 j + 8 q + 4 h + u.  They turn in
+        // LDS, 256 bytes of 32 rows at a time (16-byte pieces XORed by the row), and leave as whole lines.
+        constexpr int OSZ = sizeof(OutT), PIECE = 16 / OSZ, JS = OSZ == 2 ? NJ : NJ / 2;   // JS: blocks of a strip
+        uint8_t* const strip = &sm.b[0][0] + lslot * OPER + (uint32_t)wave * 8192u;
+        const rsrc_t ro = make_rsrc(out + (size_t)cur.row0 * p.n, (uint32_t)cur.rows * (uint32_t)p.n * (uint32_t)OSZ);
+        const uint32_t row_bytes = (uint32_t)p.n * (uint32_t)OSZ;
+        // (lane parts of the addresses, opaque: every piece's would else be computed ahead and held)
+        uint32_t put = lds_u32(strip) + (uint32_t)(l & 31) * 256u, turned = (uint32_t)(l & 15) << 4, take = lds_u32(strip) + (uint32_t)(l >> 4) * 256u, srow = (uint32_t)(l >> 4) << 4;
+        asm volatile("" : "+v"(put), "+v"(turned), "+v"(take), "+v"(srow));
+        static_for<0, NB * (NJ / JS)>([&](auto is_c) {
+            constexpr int i = decltype(is_c)::value / (NJ / JS), j0 = decltype(is_c)::value % (NJ / JS) * JS;
             if (i >= blocks) return;
-            static_for<0, 4>([&](auto q_c) {
-                constexpr int q = decltype(q_c)::value;
-#pragma unroll
-                for (int u = 0; u < 4; u += TWO ? 2 : 1) {
-                    uint32_t down = (uint32_t)(32 * i + 8 * q + u) * row_bytes;
-#pragma unroll
-                    for (int j = 0; j < NJ; ++j) {
-                        const float v = acc[i][j][4 * q + u];
-                        if constexpr (TWO) {
-                            const uint32_t own = pack_bf16(v, acc[i][j][4 * q + u + 1]);
-                            const uint32_t got = (uint32_t)__builtin_amdgcn_mov_dpp((int)own, 0xB1, 0xF, 0xF, true);   // lanes 2 i and 2 i + 1 swapped
-                            __builtin_amdgcn_raw_buffer_store_b32(__builtin_amdgcn_perm(got, own, pick), ro, at[j] + down, 0, 0);
-                        } else if constexpr (sizeof(OutT) == 2) {
-                            __builtin_amdgcn_raw_buffer_store_b16((uint16_t)pack_bf16(v, 0.f), ro, at[j] + down, 0, 0);
-                        } else {
-                            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), ro, at[j] + down, 0, 0);
-                        }
+            static_for<0, JS>([&](auto j_c) {
+                static_for<0, 4>([&](auto q_c) {
+                    constexpr int j = decltype(j_c)::value, q = decltype(q_c)::value;
+                    const f32x16& c = acc[i][j0 + j];
+                    if constexpr (OSZ == 2) {
+                        const i32x2 v = {(int)pack_bf16(c[4 * q], c[4 * q + 1]), (int)pack_bf16(c[4 * q + 2], c[4 * q + 3])};
+                        *(__attribute__((address_space(3))) i32x2*)(uintptr_t)(put + (((4 * j + q) << 4) ^ turned) + 8 * h) = v;
+                    } else {
+                        *(__attribute__((address_space(3))) f32x4*)(uintptr_t)(put + (((uint32_t)(8 * j + 2 * q + h) << 4) ^ turned)) = f32x4{c[4 * q], c[4 * q + 1], c[4 * q + 2], c[4 * q + 3]};
                     }
-                    __builtin_amdgcn_sched_barrier(0);
-                }
+                });
             });
+            const int col = cur.col0 + c0w + 32 * j0 + PIECE * (l & 15);
+            uint32_t off = (uint32_t)(r0w + 32 * i + (int)(srow >> 4)) * row_bytes + (uint32_t)col * (uint32_t)OSZ;
+#pragma unroll
+            for (int r = 0; r < 32; r += 4) {
+                // row r + l / 16, whose pieces are XORed by its low four bits
+                const i32x4 v = *(const __attribute__((address_space(3))) i32x4*)(uintptr_t)(take + 256u * r + (turned ^ (srow + ((r & 15) << 4))));
+                if constexpr (WHOLE) {
+                    bstore(ro, col < p.n ? off : kOOB, v);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < PIECE; ++e) {
+                        const uint32_t at = col + e < p.n ? off + (uint32_t)(e * OSZ) : kOOB;
+                        if constexpr (OSZ == 2) __builtin_amdgcn_raw_buffer_store_b16((uint16_t)((uint32_t)v[e >> 1] >> (16 * (e & 1))), ro, at, 0, 0);
+                        else __builtin_amdgcn_raw_buffer_store_b32((uint32_t)v[e & 3], ro, at, 0, 0);
+                    }
+                }
+                off += 4 * row_bytes;
+            }
         });
-        cur.row0 = scalar(next.row0); cur.rows = scalar(next.rows); cur.col0 = scalar(next.col0);
+        __builtin_amdgcn_s_waitcnt(0xc07f);   // the strip has been read (lgkmcnt(0))
+        __builtin_amdgcn_sched_barrier(0);
+        issue_some(std::integral_constant<int, 8>{}, std::integral_constant<int, 16>{}, lp2);
+        lslot ^= 1;
+        });
+        cur.row0 = scalar(next.row0); cur.rows = scalar(next.rows); cur.col0 = scalar(next.col0); cur.turn0 = scalar(next.turn0);
     }
     wait_vm<0>();   // no load may still be writing LDS when the workgroup ends
     }
@@ -738,9 +762,14 @@ inline bool tile_ok(const Fp4Params& p) {
 inline hipError_t launch_tile(const Fp4Params& p, int cus, hipStream_t s) {
     const int64_t tiles = ((int64_t)p.m / tile::BM + (p.g < p.m ? p.g : p.m)) * ((p.n + tile::BN - 1) / tile::BN);
     const int grid = (int)(tiles < cus ? (tiles < 1 ? 1 : tiles) : cus);
-    if (p.out_f32) hipLaunchKernelGGL((tile::kernel<float, false>), dim3(grid), dim3(tile::NT), 0, s, p);
-    else if (p.n % 2 == 0 && (uintptr_t)p.out % 4 == 0) hipLaunchKernelGGL((tile::kernel<uint16_t, true>), dim3(grid), dim3(tile::NT), 0, s, p);
-    else hipLaunchKernelGGL((tile::kernel<uint16_t, false>), dim3(grid), dim3(tile::NT), 0, s, p);
+    const bool whole = ((uintptr_t)p.out & 15) == 0 && (p.n * (p.out_f32 ? 4 : 2)) % 16 == 0;
+    if (p.out_f32) {
+        if (whole) hipLaunchKernelGGL((tile::kernel<float, true>), dim3(grid), dim3(tile::NT), 0, s, p);
+        else hipLaunchKernelGGL((tile::kernel<float, false>), dim3(grid), dim3(tile::NT), 0, s, p);
+    } else {
+        if (whole) hipLaunchKernelGGL((tile::kernel<uint16_t, true>), dim3(grid), dim3(tile::NT), 0, s, p);
+        else hipLaunchKernelGGL((tile::kernel<uint16_t, false>), dim3(grid), dim3(tile::NT), 0, s, p);
+    }
     return hipGetLastError();
 }
 
