@@ -17,13 +17,15 @@ using namespace ring;
 constexpr int kFp4 = 4;   // operand format selector of e2m1
 __device__ inline i32x8 widen(i32x4 v) { return i32x8{v[0], v[1], v[2], v[3], 0, 0, 0, 0}; }
 
-// 16 (or 4) bytes a lane straight into LDS, as ring.hpp's loads, with the wait state that this target asks for
-// between a scalar write of m0 and the load that takes its LDS address from it.
+// 16 (or 4) bytes a lane straight into LDS, as ring.hpp's loads, with the wait states that this target asks
+// for: one between a scalar write of m0 and the load that takes its LDS address from it, five between a vector
+// instruction's write of a scalar register (a readfirstlane, or a spilled descriptor's reload) and a load that
+// reads it.  The compiler puts them in where it sees both instructions; it does not look into asm.
 __device__ inline void load16(i32x4 r, uint32_t lds_addr, uint32_t off) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds_addr), "v"(off), "s"(r) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(lds_addr), "v"(off), "s"(r) : "memory", "m0");
 }
 __device__ inline void load4(i32x4 r, uint32_t lds_addr, uint32_t off) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds_addr), "v"(off), "s"(r) : "memory", "m0");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds_addr), "v"(off), "s"(r) : "memory", "m0");
 }
 
 constexpr int kPanel = 256;           // elements along k of one scale panel
@@ -163,9 +165,8 @@ __global__ __launch_bounds__(256) void split_kernel(Fp4Params p, int ntiles) {
         return;
     }
     const int rows = rt.rows, panels = (p.k + kPanel - 1) / kPanel, rb = p.k >> 1;
-    i32x4 rx = make_rsrc_v(p.lhs + (size_t)rt.row0 * rb, (uint32_t)rows * (uint32_t)rb);
-    i32x4 rw = make_rsrc_v(p.rhs + ((size_t)rt.grp * p.n + col0) * rb, (uint32_t)cols * (uint32_t)rb);
-    asm volatile("s_nop 4" : "+s"(rx), "+s"(rw));
+    const i32x4 rx = make_rsrc_v(p.lhs + (size_t)rt.row0 * rb, (uint32_t)rows * (uint32_t)rb);
+    const i32x4 rw = make_rsrc_v(p.rhs + ((size_t)rt.grp * p.n + col0) * rb, (uint32_t)cols * (uint32_t)rb);
     const uint8_t* xs0 = p.lhs_scale + (size_t)rt.row0 * 8;
     const uint8_t* ws0 = p.rhs_scale + ((size_t)rt.grp * panels * p.n + col0) * 8;
     const uint32_t ring0 = lds_u32(smem) + (uint32_t)(wave * D * R::SLOT);
@@ -187,9 +188,8 @@ __global__ __launch_bounds__(256) void split_kernel(Fp4Params p, int ntiles) {
         };
         rows_of(rw, base, 2 * NT);
         rows_of(rx, base + R::W, 2 * MT);
-        i32x4 rws = make_rsrc_v(ws0 + (size_t)(live ? panel : 0) * p.n * 8, (uint32_t)cols * 8u);
-        i32x4 rxs = make_rsrc_v(xs0 + (size_t)(live ? panel : 0) * p.m * 8, (uint32_t)rows * 8u);
-        asm volatile("s_nop 4" : "+s"(rws), "+s"(rxs));   // five states between writing a descriptor and a load that reads it
+        const i32x4 rws = make_rsrc_v(ws0 + (size_t)(live ? panel : 0) * p.n * 8, (uint32_t)cols * 8u);
+        const i32x4 rxs = make_rsrc_v(xs0 + (size_t)(live ? panel : 0) * p.m * 8, (uint32_t)rows * 8u);
 #pragma unroll
         for (int i = 0; i < (NT + 1) / 2; ++i) load4(rws, base + R::W + R::X + 256u * i, live ? 256u * i + 4u * l : kOOB);
 #pragma unroll
@@ -329,9 +329,8 @@ __global__ __launch_bounds__(64 * WAVES) void kernel(Fp4Params p, int splits, in
     auto load = [&](int s) {
         const int col = 16 * (ct0 + wave + WAVES * lc), cols = min(16, p.n - col);
         const bool live = lc < tiles;
-        i32x4 rw = make_rsrc_v(wbase + (size_t)(live ? col : 0) * rb, live ? (uint32_t)cols * (uint32_t)rb : 0u);
-        i32x4 rs = make_rsrc_v(sbase + ((size_t)lp * p.n + (live ? col : 0)) * 8, live ? (uint32_t)cols * 8u : 0u);
-        asm volatile("s_nop 4" : "+s"(rw), "+s"(rs));   // five states between writing a descriptor and a load that reads it
+        const i32x4 rw = make_rsrc_v(wbase + (size_t)(live ? col : 0) * rb, live ? (uint32_t)cols * (uint32_t)rb : 0u);
+        const i32x4 rs = make_rsrc_v(sbase + ((size_t)lp * p.n + (live ? col : 0)) * 8, live ? (uint32_t)cols * 8u : 0u);
         const uint32_t at = ring0 + (uint32_t)(s * SLOT), pb = (uint32_t)lp * kRowBytes;
         const bool ok0 = pb + byte0 < (uint32_t)rb, ok1 = pb + byte1 < (uint32_t)rb;   // chunks past k
         load16(rw, at, ok0 ? (uint32_t)lr * (uint32_t)rb + pb + byte0 : kOOB);
@@ -344,8 +343,7 @@ __global__ __launch_bounds__(64 * WAVES) void kernel(Fp4Params p, int splits, in
 
     // the rows, once
     {
-        i32x4 rx = make_rsrc_v(p.lhs + (size_t)rt.row0 * rb, (uint32_t)rows * (uint32_t)rb);
-        asm volatile("s_nop 4" : "+s"(rx));
+        const i32x4 rx = make_rsrc_v(p.lhs + (size_t)rt.row0 * rb, (uint32_t)rows * (uint32_t)rb);
         const uint32_t x0 = lds_u32(xl);
         for (int i = wave; i < panels * (xrows >> 3); i += WAVES) {
             const int panel = xrows == 8 ? i : i >> 1, half = xrows == 8 ? 0 : i & 1;
@@ -443,7 +441,14 @@ constexpr int BM = 256, BN = 256, NT = 256, MI = 4, NJ = 4, SUB = 4;   // SUB: i
 constexpr int OPER = 256 * kRowBytes;     // one operand's slot
 constexpr int SC = 256 * 8;               // one operand's scales of a panel
 constexpr int ROT = 2;                    // panels between the starts of neighbouring column tiles
-constexpr int LOADS = 20;                 // a wave's loads of a panel: 8 + 8 of eight rows, 4 of 256 bytes of scales
+constexpr int LOADS = 17;                 // a wave's loads of a panel: 8 + 8 of eight rows, 1 KiB of scales
+constexpr int READ = 15;                  // MFMA of a panel after which the next panel's reads begin
+constexpr int load_step(int d) { return d * 31 / LOADS; }   // MFMA after which load d goes out
+constexpr int loads_before(int step) {
+    int n = 0;
+    while (n < LOADS && load_step(n) <= step) ++n;
+    return n;
+}
 struct alignas(16) Smem {
     uint8_t a[2][OPER];
     uint8_t b[2][OPER];
@@ -483,6 +488,7 @@ __global__ __launch_bounds__(NT, 1) void kernel(Fp4Params p) {
     if (blockIdx.x == 0 && t == 0) *p.status = sm.tab.flags;
     const int rb = p.k >> 1, panels = (p.k + kPanel - 1) / kPanel;
     OutT* const out = (OutT*)p.out;
+    constexpr int OSZ = sizeof(OutT), PIECE = 16 / OSZ, JS = OSZ == 2 ? NJ : NJ / 2;   // JS: blocks of a 256-byte strip
     const int first = xcd_virtual_id(blockIdx.x, gridDim.x);
 
     struct Info { int row0, rows, col0, turn0; };   // turn0: the panel that the tile begins with
@@ -496,8 +502,7 @@ __global__ __launch_bounds__(NT, 1) void kernel(Fp4Params p) {
             bytes = (int)n;
         }
         __device__ i32x4 get() const { return i32x4{lo, hi, bytes, kRsrcWord3}; }
-        // into scalar registers (five states before a load may read them)
-        __device__ void pin() { lo = scalar(lo); hi = scalar(hi); bytes = scalar(bytes); asm volatile("s_nop 4"); }
+        __device__ void pin() { lo = scalar(lo); hi = scalar(hi); bytes = scalar(bytes); }   // into scalar registers
     };
     Desc ra, rw, rs;
     auto decode = [&](int tile) {
@@ -541,9 +546,14 @@ __global__ __launch_bounds__(NT, 1) void kernel(Fp4Params p) {
             const uint32_t s = (uint32_t)(64 * wave + 8 * (d & 7)) * (uint32_t)rb + (uint32_t)lp * kRowBytes + past;
             load16(d < 8 ? ra.get() : rw.get(), (d < 8 ? lds_a : lds_b) + lslot * OPER + (uint32_t)(8 * wave + (d & 7)) * 1024u, v + s);
         } else {
-            // (4 bytes a lane: the last panel of an odd number of rows ends 8 bytes into a 16-byte piece)
-            constexpr uint32_t e = 256u * (d - 16);
-            load4(rs.get(), lds_s + lslot * (2 * SC) + (uint32_t)wave * 1024u + e, (uint32_t)lp * srows + past + (uint32_t)(wave & 1) * 1024u + e + 4u * (uint32_t)l);
+            const uint32_t to = lds_s + lslot * (2 * SC) + (uint32_t)wave * 1024u, from = (uint32_t)lp * srows + past + (uint32_t)(wave & 1) * 1024u;
+            if (lp == panels - 1 && ((rs.bytes - lp * (int)srows) & 8)) {
+                // the array may end 8 bytes into a 16-byte piece: 4 bytes a lane (the waits count the fewer loads)
+#pragma unroll
+                for (uint32_t e = 0; e < 1024; e += 256) load4(rs.get(), to + e, from + e + 4u * (uint32_t)l);
+            } else {
+                load16(rs.get(), to, from + 16u * (uint32_t)l);
+            }
         }
     };
 
@@ -581,11 +591,13 @@ __global__ __launch_bounds__(NT, 1) void kernel(Fp4Params p) {
 #pragma unroll
         for (int j = 0; j < NJ; ++j) sb[j] = nb_[j] & (int)keep;
     };
-    // the slot read last is empty and the panel after it has arrived, for every wave
-    auto turn = [&] {
-        __builtin_amdgcn_s_waitcnt(0xc07f);   // lgkmcnt(0), known to the compiler
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    // for every wave: the panel after the one that is computed has arrived (its loads are older than the YOUNGER
+    // youngest), and: its slot has been read
+    auto arrived = [&](auto younger_c) {
+        constexpr int YOUNGER = decltype(younger_c)::value;
+        asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" ::"n"(YOUNGER < 63 ? YOUNGER : 63) : "memory");
     };
+    auto emptied = [&] { lds_barrier(); };
 
     if (first < gemm_tiles) {
         Info cur = decode(first);
@@ -610,10 +622,11 @@ __global__ __launch_bounds__(NT, 1) void kernel(Fp4Params p) {
         aim_scales();
         static_for<0, MI>([&](auto i_c) { read_sa(i_c); });
         static_for<0, NJ>([&](auto j_c) { read_sb(j_c); });
-        turn();
+        emptied();
         take_scales(cur.turn0);
         rslot = 1;
         issue_all(around(cur.turn0 + 2));
+        bool stored = false;   // the tile before left all of its STORES
         for (int tile = first; tile < gemm_tiles;) {
         Info next = cur;
         const int blocks = max(0, min(MI, cdiv(cur.rows - r0w, 32)));
@@ -621,6 +634,7 @@ __global__ __launch_bounds__(NT, 1) void kernel(Fp4Params p) {
         with_nb<2>((blocks + 1) >> 1, [&](auto nb_c) {
             constexpr int NB = 2 * decltype(nb_c)::value;
             f32x16 acc[NB > 0 ? NB : 1][NJ];
+            constexpr int STORES = MI * (NJ / JS) * 8 * (WHOLE ? 1 : PIECE);   // a wave's of a whole tile
             // One panel: 16 steps a sub-slice, each at most one MFMA and the reads and loads that go with it.
             // FIRST: the tile's first panel, whose turn and loads are done already.  follow: the panel after it,
             // lp: the panel to load.
@@ -639,27 +653,45 @@ __global__ __launch_bounds__(NT, 1) void kernel(Fp4Params p) {
                         }
                         // the last sub-slice, read during the panel before, to its place
                         if constexpr (S == 0 && M < 4) { fa[SUB - 1][M] = ta[M]; fb[SUB - 1][M] = tb[M]; }
-                        if constexpr (!FIRST) {
-                            if constexpr (S == 0 && M == 3) turn();
-                            if constexpr (S == 0 && M >= 4) issue(std::integral_constant<int, M - 4>{}, lp);
-                            if constexpr (S == 1 && M < LOADS - 12) issue(std::integral_constant<int, 12 + M>{}, lp);
-                        }
-                        // reads of the next panel: eight 16-byte ones a sub-slice, early in the last one, so that
-                        // none is on its way when the panel turns
-                        if constexpr (S == 0) {
-                            if constexpr (M == 4) aim(SUB - 1);
-                            if constexpr (M >= 4 && M < 8) read_a(ta[M - 4], M - 4);
-                            if constexpr (M >= 8 && M < 12) read_b(tb[M - 8], M - 8);
-                        } else {
-                            constexpr int T = S == 3 ? M : M >> 1;
-                            if constexpr (M == 0) aim(S - 1);
-                            if constexpr (S == 3 || (M & 1)) {
-                                if constexpr (T < 4) read_a(fa[S - 1][T & 3], T);
-                                else if constexpr (T < 8) read_b(fb[S - 1][T & 3], T - 4);
+                        constexpr int G = 16 * S + M;
+                        // the loads, spread over the first half (a load takes a compute unit's address path 16
+                        // clocks, so the four waves' go out no faster than one each in 64)
+                        if constexpr (!FIRST) static_for<0, LOADS>([&](auto d_c) { if constexpr (load_step(decltype(d_c)::value) == G) issue(d_c, lp); });
+                        // the next panel's reads, spread over the rest: its loads have had a panel and a quarter to
+                        // arrive, and are older than those just begun
+                        if constexpr (G == READ) {
+                            if constexpr (!FIRST) {
+                                arrived(std::integral_constant<int, loads_before(READ)>{});
+                            } else if (stored) {
+                                arrived(std::integral_constant<int, LOADS + STORES>{});
+                            } else {
+                                arrived(std::integral_constant<int, LOADS>{});
                             }
-                            if constexpr (S == 3 && M == 8) aim_scales();
-                            if constexpr (S == 3 && M >= 8 && M < 12) { read_sa(M - 8); read_sb(M - 8); }
                         }
+                        if constexpr (G >= 16 && G < 32) {
+                            constexpr int K = G & 15;
+                            if constexpr ((K & 7) == 0) aim(0);
+                            if constexpr ((K & 7) == 4) aim(SUB - 1);
+                            if constexpr (K < 4) read_a(fa[0][K], K);
+                            else if constexpr (K < 8) read_a(ta[K & 3], K & 3);
+                            else if constexpr (K < 12) read_b(fb[0][K & 3], K & 3);
+                            else read_b(tb[K & 3], K & 3);
+                        }
+                        if constexpr (G >= 32 && G < 48) {
+                            constexpr int K = G & 15;
+                            if constexpr (K == 0) aim(1);
+                            if constexpr (K == 8) aim_scales();
+                            if constexpr (K < 4) read_a(fa[1][K], K);
+                            else if constexpr (K < 8) read_b(fb[1][K & 3], K & 3);
+                            else if constexpr (K < 12) read_sa(K & 3);
+                            else read_sb(K & 3);
+                        }
+                        if constexpr (G >= 48 && G < 56) {
+                            if constexpr (G == 48) aim(2);
+                            if constexpr (G < 52) read_a(fa[2][G & 3], G & 3);
+                            else read_b(fb[2][G & 3], G & 3);
+                        }
+                        if constexpr (G == 60) emptied();
                         __builtin_amdgcn_sched_barrier(0);
                     });
                 });
@@ -686,7 +718,6 @@ __global__ __launch_bounds__(NT, 1) void kernel(Fp4Params p) {
                     left = 2;
                 }
             }
-        turn();
         ra.pin(); rw.pin(); rs.pin();
         // The slot that has just been emptied takes the panel after the next: its rows and scales at once, its
         // weights once the results have passed through their place (8 KiB a wave, the part that its own loads fill).
@@ -695,7 +726,6 @@ __global__ __launch_bounds__(NT, 1) void kernel(Fp4Params p) {
         issue_some(std::integral_constant<int, 16>{}, std::integral_constant<int, LOADS>{}, lp2);
         // Results: element 4 q + u of block (i, j) is row 32 i + l % 32, column 32 j + 8 q + 4 h + u.  They turn in
         // LDS, 256 bytes of 32 rows at a time (16-byte pieces XORed by the row), and leave as whole lines.
-        constexpr int OSZ = sizeof(OutT), PIECE = 16 / OSZ, JS = OSZ == 2 ? NJ : NJ / 2;   // JS: blocks of a strip
         uint8_t* const strip = &sm.b[0][0] + lslot * OPER + (uint32_t)wave * 8192u;
         const rsrc_t ro = make_rsrc(out + (size_t)cur.row0 * p.n, (uint32_t)cur.rows * (uint32_t)p.n * (uint32_t)OSZ);
         const uint32_t row_bytes = (uint32_t)p.n * (uint32_t)OSZ;
@@ -704,7 +734,7 @@ __global__ __launch_bounds__(NT, 1) void kernel(Fp4Params p) {
         asm volatile("" : "+v"(put), "+v"(turned), "+v"(take), "+v"(srow));
         static_for<0, NB * (NJ / JS)>([&](auto is_c) {
             constexpr int i = decltype(is_c)::value / (NJ / JS), j0 = decltype(is_c)::value % (NJ / JS) * JS;
-            if (i >= blocks) return;
+            if (NB < MI && i >= blocks) return;   // (whole tiles' stores are counted: see arrived)
             static_for<0, JS>([&](auto j_c) {
                 static_for<0, 4>([&](auto q_c) {
                     constexpr int j = decltype(j_c)::value, q = decltype(q_c)::value;
@@ -740,6 +770,7 @@ __global__ __launch_bounds__(NT, 1) void kernel(Fp4Params p) {
         __builtin_amdgcn_sched_barrier(0);
         issue_some(std::integral_constant<int, 8>{}, std::integral_constant<int, 16>{}, lp2);
         lslot ^= 1;
+        stored = NB == MI;
         });
         cur.row0 = scalar(next.row0); cur.rows = scalar(next.rows); cur.col0 = scalar(next.col0); cur.turn0 = scalar(next.turn0);
     }
