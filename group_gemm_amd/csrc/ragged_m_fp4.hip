@@ -128,160 +128,6 @@ __device__ inline void store4(OutT* o, f32x4 v, int left, bool vec) {
     }
 }
 
-// Split-k kernel: one workgroup makes a tile of 16 MT rows x 16 NT columns, its four waves taking every
-// fourth panel of k each and adding their results in LDS.  A wave streams its panels through a private LDS
-// ring of D slots (loads straight into LDS, eight rows of 128 bytes an instruction; the waits are on the
-// wave's own loads, so the main loop has no barrier), reads the operands back in the instruction's layout
-// and multiplies with 16x16x128 instructions, the weights as the first operand so that a lane holds four
-// consecutive columns.
-template <int MT, int NT, int D>
-struct SplitRing {
-    static constexpr int X = MT * 16 * kRowBytes, W = NT * 16 * kRowBytes;
-    static constexpr int XS = (MT + 1) / 2 * 256, WS = (NT + 1) / 2 * 256;   // 4 bytes a lane and load
-    static constexpr int SLOT = X + W + XS + WS;
-    static constexpr int LOADS = 2 * MT + 2 * NT + (MT + 1) / 2 + (NT + 1) / 2;
-    static constexpr int RED = 4 * MT * NT * 1024;
-    static constexpr int BYTES = 4 * D * SLOT > RED ? 4 * D * SLOT : RED;
-    static_assert(LOADS * D <= 63, "vmcnt range");
-};
-
-template <int MT, int NT, int D, int PER, typename OutT>
-__global__ __launch_bounds__(256) void split_kernel(Fp4Params p, int ntiles) {
-    using R = SplitRing<MT, NT, D>;
-    __shared__ __attribute__((aligned(16))) uint8_t smem[R::BYTES];
-    const int t = threadIdx.x, l = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
-    const int slot = blockIdx.x / ntiles, col0 = (blockIdx.x % ntiles) * (16 * NT);
-    uint32_t flags;
-    const RowTile rt = find_row_tile<PER>(p.group_sizes, p.g, p.m, 16 * MT, slot, &flags);
-    if (blockIdx.x == 0 && t == 0) *p.status = flags;
-    if (rt.grp == -1) return;
-    OutT* out = (OutT*)p.out;
-    const int cols = min(16 * NT, p.n - col0);
-    if (rt.grp == -2) {
-        for (int i = t; i < 16 * NT * rt.rows; i += 256) {
-            const int r = i / (16 * NT), c = i % (16 * NT);
-            if (c < cols) store1(out + (size_t)(rt.row0 + r) * p.n + col0 + c, 0.f);
-        }
-        return;
-    }
-    const int rows = rt.rows, panels = (p.k + kPanel - 1) / kPanel, rb = p.k >> 1;
-    const i32x4 rx = make_rsrc_v(p.lhs + (size_t)rt.row0 * rb, (uint32_t)rows * (uint32_t)rb);
-    const i32x4 rw = make_rsrc_v(p.rhs + ((size_t)rt.grp * p.n + col0) * rb, (uint32_t)cols * (uint32_t)rb);
-    const uint8_t* xs0 = p.lhs_scale + (size_t)rt.row0 * 8;
-    const uint8_t* ws0 = p.rhs_scale + ((size_t)rt.grp * panels * p.n + col0) * 8;
-    const uint32_t ring0 = lds_u32(smem) + (uint32_t)(wave * D * R::SLOT);
-    uint8_t* mine = smem + wave * D * R::SLOT;
-
-    // a load brings rows 8 i .. 8 i + 7: lane l row l / 8, into chunk place l % 8
-    const int lr = l >> 3;
-    auto load = [&](int panel, int s) {
-        const uint32_t base = ring0 + (uint32_t)(s * R::SLOT);
-        const bool live = panel < panels;
-        auto rows_of = [&](i32x4 rsrc, uint32_t at, int count) {
-#pragma unroll
-            for (int i = 0; i < count; ++i) {
-                const int chunk = (l & 7) ^ swizzle(8 * i + lr);
-                const uint32_t byte = (uint32_t)panel * kRowBytes + 16u * (uint32_t)chunk;
-                const bool ok = live && byte < (uint32_t)rb;
-                load16(rsrc, at + 1024u * (uint32_t)i, ok ? (uint32_t)(8 * i + lr) * (uint32_t)rb + byte : kOOB);
-            }
-        };
-        rows_of(rw, base, 2 * NT);
-        rows_of(rx, base + R::W, 2 * MT);
-        const i32x4 rws = make_rsrc_v(ws0 + (size_t)(live ? panel : 0) * p.n * 8, (uint32_t)cols * 8u);
-        const i32x4 rxs = make_rsrc_v(xs0 + (size_t)(live ? panel : 0) * p.m * 8, (uint32_t)rows * 8u);
-#pragma unroll
-        for (int i = 0; i < (NT + 1) / 2; ++i) load4(rws, base + R::W + R::X + 256u * i, live ? 256u * i + 4u * l : kOOB);
-#pragma unroll
-        for (int i = 0; i < (MT + 1) / 2; ++i) load4(rxs, base + R::W + R::X + R::WS + 256u * i, live ? 256u * i + 4u * l : kOOB);
-    };
-
-    f32x4 acc[MT][NT];
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-
-#pragma unroll
-    for (int s = 0; s < D; ++s) load(wave + 4 * s, s);
-    const int r = l & 15, q = l >> 4;
-    int s = 0;
-    for (int panel = wave; panel < panels; panel += 4) {
-        wait_vm<R::LOADS * (D - 1)>();   // the oldest slot is in LDS
-        const uint8_t* w = mine + s * R::SLOT;
-        const uint8_t* x = w + R::W;
-        const uint8_t* ws = x + R::X;
-        const uint8_t* xs = ws + R::WS;
-        // the lane's k blocks 2 q and 2 q + 1 of the panel: chunks 2 q + h, scale bytes likewise
-        i32x4 fw[NT][2], fx[MT][2];
-        uint32_t sw[NT], sx[MT];
-        const int valid = (p.k >> 5) - panel * 8 - 2 * q;   // blocks of the lane's two that lie inside k
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            const int row = 16 * j + r;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) fw[j][h] = *(const i32x4*)(w + row * kRowBytes + (((2 * q + h) ^ swizzle(row)) << 4));
-            sw[j] = keep_bytes(*(const uint16_t*)(ws + row * 8 + 2 * q), valid);
-        }
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            const int row = 16 * i + r;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) fx[i][h] = *(const i32x4*)(x + row * kRowBytes + (((2 * q + h) ^ swizzle(row)) << 4));
-            sx[i] = keep_bytes(*(const uint16_t*)(xs + row * 8 + 2 * q), valid);
-        }
-        __builtin_amdgcn_s_waitcnt(0xc07f);   // the slot has been read (lgkmcnt(0)): it can be filled again
-        __builtin_amdgcn_sched_barrier(0);
-        load(panel + 4 * D, s);
-        s = s + 1 == D ? 0 : s + 1;
-#pragma unroll
-        for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(fw[j][0]), widen(fx[i][0]), acc[i][j], kFp4, kFp4, 0, (int)sw[j], 0, (int)sx[i]);
-                acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(fw[j][1]), widen(fx[i][1]), acc[i][j], kFp4, kFp4, 1, (int)sw[j], 1, (int)sx[i]);
-            }
-    }
-    // add the four waves' results (in wave order) and store
-    wait_vm<0>();
-    __syncthreads();
-    f32x4* red = (f32x4*)smem;
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) red[((wave * MT + i) * NT + j) * 64 + l] = acc[i][j];
-    __syncthreads();
-    const bool vec = (p.n & 3) == 0 && ((uintptr_t)p.out & (4 * sizeof(OutT) - 1)) == 0;
-    for (int tile = wave; tile < MT * NT; tile += 4) {
-        f32x4 v = red[tile * 64 + l];
-#pragma unroll
-        for (int w = 1; w < 4; ++w) {
-            const f32x4 a = red[(w * MT * NT + tile) * 64 + l];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] += a[e];
-        }
-        const int row = 16 * (tile / NT) + r, col = 16 * (tile % NT) + 4 * q;
-        if (row < rows && col < cols) store4(out + (size_t)(rt.row0 + row) * p.n + col0 + col, v, cols - col, vec);
-    }
-}
-
-template <int MT, int NT, int D, int PER>
-hipError_t launch_split_per(const Fp4Params& p, int64_t grid, int ntiles, hipStream_t s) {
-    if (p.out_f32) hipLaunchKernelGGL((split_kernel<MT, NT, D, PER, float>), dim3((uint32_t)grid), dim3(256), 0, s, p, ntiles);
-    else hipLaunchKernelGGL((split_kernel<MT, NT, D, PER, uint16_t>), dim3((uint32_t)grid), dim3(256), 0, s, p, ntiles);
-    return hipGetLastError();
-}
-
-template <int MT, int NT, int D>
-hipError_t launch_split(const Fp4Params& p, hipStream_t s) {
-    const int ntiles = (p.n + 16 * NT - 1) / (16 * NT);
-    const int64_t grid = slot_bound(p, 16 * MT) * (ntiles > 0 ? ntiles : 1);
-    const int nt = ntiles > 0 ? ntiles : 1;
-    if (p.g <= 64) return launch_split_per<MT, NT, D, 1>(p, grid, nt, s);
-    if (p.g <= 256) return launch_split_per<MT, NT, D, 4>(p, grid, nt, s);
-    return launch_split_per<MT, NT, D, 16>(p, grid, nt, s);
-}
-
 // Stream kernel, for few rows a group: a workgroup holds the rows of one row tile (up to 16, all of k) in LDS
 // and its four waves each stream weights past them, 16 columns (a column tile) at a time, through a private
 // LDS ring of D panels (2 KiB of codes and their scales, loaded straight into LDS).  A wave's stream runs
@@ -290,13 +136,14 @@ hipError_t launch_split(const Fp4Params& p, hipStream_t s) {
 namespace stream {
 constexpr int WAVES = 4;
 constexpr int WPANEL = 16 * kRowBytes, SLOT = WPANEL + 256;   // scales: 128 bytes, loaded 4 bytes a lane
-constexpr int LOADS = 3;
+constexpr int LOADS = 3, D = 4;
+constexpr int kMaxRowBytes = 28 * 1024;   // rows of one tile in LDS, so that a CU holds two workgroups
 
-template <int D, int XCAP, int PER, typename OutT>
+template <int PER, typename OutT>
 __global__ __launch_bounds__(64 * WAVES) void kernel(Fp4Params p, int splits, int xrows) {
     // rows: panel by panel [xrows][128 bytes], then scales [panels][16][8]; 1 KiB of slack, as lanes of rows
     // that are not there (their results are not stored) read on
-    __shared__ __attribute__((aligned(16))) uint8_t smem[WAVES * D * SLOT + XCAP + 1024];
+    __shared__ __attribute__((aligned(16))) uint8_t smem[WAVES * D * SLOT + kMaxRowBytes + 1024];
     const int t = threadIdx.x, l = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
     // split c of every row tile runs on XCD c % 8 (a group's row tiles share their weights in its L2)
     const int idx = blockIdx.x >> 3, per = splits >> 3;
@@ -393,26 +240,17 @@ __global__ __launch_bounds__(64 * WAVES) void kernel(Fp4Params p, int splits, in
     wait_vm<0>();   // no load may still be writing LDS when the workgroup ends
 }
 
-constexpr int kMaxRowBytes = 63 * 1024;   // rows of one tile in LDS, the largest size built
-
 inline int row_bytes(const Fp4Params& p) {
     const int panels = (p.k + kPanel - 1) / kPanel;
     return panels * ((p.m <= 8 ? 8 : 16) * kRowBytes + 128);
 }
 
-template <int D, int XCAP, int PER>
+template <int PER>
 hipError_t launch_per(const Fp4Params& p, int64_t grid, int splits, int xrows, hipStream_t s) {
-    if (p.out_f32) hipLaunchKernelGGL((kernel<D, XCAP, PER, float>), dim3((uint32_t)grid), dim3(64 * WAVES), 0, s, p, splits, xrows);
-    else hipLaunchKernelGGL((kernel<D, XCAP, PER, uint16_t>), dim3((uint32_t)grid), dim3(64 * WAVES), 0, s, p, splits, xrows);
+    if (p.out_f32) hipLaunchKernelGGL((kernel<PER, float>), dim3((uint32_t)grid), dim3(64 * WAVES), 0, s, p, splits, xrows);
+    else hipLaunchKernelGGL((kernel<PER, uint16_t>), dim3((uint32_t)grid), dim3(64 * WAVES), 0, s, p, splits, xrows);
     return hipGetLastError();
 }
-template <int D, int XCAP>
-hipError_t launch_d(const Fp4Params& p, int64_t grid, int splits, int xrows, hipStream_t s) {
-    if (p.g <= 64) return launch_per<D, XCAP, 1>(p, grid, splits, xrows, s);
-    if (p.g <= 256) return launch_per<D, XCAP, 4>(p, grid, splits, xrows, s);
-    return launch_per<D, XCAP, 16>(p, grid, splits, xrows, s);
-}
-
 inline hipError_t launch(const Fp4Params& p, int cus, hipStream_t s) {
     const int nct = (p.n + 15) / 16;
     const int64_t slots = slot_bound(p, 16);
@@ -421,12 +259,180 @@ inline hipError_t launch(const Fp4Params& p, int cus, hipStream_t s) {
     if (splits > nct / WAVES) splits = nct / WAVES;
     splits = splits < 8 ? 8 : (splits + 7) / 8 * 8;
     const int64_t grid = slots * splits;
-    const int xrows = p.m <= 8 ? 8 : 16, bytes = row_bytes(p);
-    if (bytes <= 8 * 1024) return launch_d<4, 8 * 1024>(p, grid, (int)splits, xrows, s);
-    if (bytes <= 41 * 1024) return launch_d<4, 41 * 1024>(p, grid, (int)splits, xrows, s);
-    return launch_d<8, kMaxRowBytes>(p, grid, (int)splits, xrows, s);
+    const int xrows = p.m <= 8 ? 8 : 16;
+    if (p.g <= 64) return launch_per<1>(p, grid, (int)splits, xrows, s);
+    if (p.g <= 256) return launch_per<4>(p, grid, (int)splits, xrows, s);
+    return launch_per<16>(p, grid, (int)splits, xrows, s);
 }
 }  // namespace stream
+
+// Block kernel, for some tens of rows a group and for every shape that the other two do not take: a workgroup
+// walks a run of column tiles of one row tile, 64 rows x 128 columns each, as one stream of panels.  A panel
+// (both operands' codes and scales) is loaded straight into one of D LDS slots, each wave an equal share; a
+// panel that every wave has is read by all four, 64 rows x 32 columns of 32x32x64 instructions a wave, while
+// the next D - 1 are on their way.  One barrier a panel, and two workgroups a CU cover each other's.  The
+// weights are read once for 64 rows of their group, which leaves it bound by memory: a panel's instructions
+// take 260 of the 2100 clocks in which a CU's share of the bandwidth brings its weights.
+namespace block {
+constexpr int ROWS = 64, COLS = 128, NT = 256, D = 3, SUB = 4, MI = ROWS / 32;
+constexpr int W = COLS * kRowBytes, X = ROWS * kRowBytes, WS = COLS * 8, XS = ROWS * 8, SLOT = W + X + WS + XS;
+constexpr int LOADS = 8;   // a wave's loads of a panel: 4 of weights, 2 of rows, 1 of each one's scales
+
+// VEC: four consecutive columns of a row are one aligned store
+template <int PER, typename OutT, bool VEC>
+__global__ __launch_bounds__(NT, 2) void kernel(Fp4Params p, int splits, int run) {
+    __shared__ __attribute__((aligned(16))) uint8_t smem[D * SLOT];
+    const int t = threadIdx.x, l = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    // split c of every row tile runs on XCD c % 8 (a group's row tiles share their weights in its L2)
+    const int idx = blockIdx.x >> 3, per = splits >> 3;
+    const int slot = idx / per, split = (idx % per) * 8 + (blockIdx.x & 7);
+    uint32_t flags;
+    const RowTile rt = find_row_tile<PER>(p.group_sizes, p.g, p.m, ROWS, slot, &flags);
+    if (blockIdx.x == 0 && t == 0) *p.status = flags;
+    if (rt.grp == -1) return;
+    OutT* out = (OutT*)p.out;
+    const int nct = (p.n + COLS - 1) / COLS;
+    const int ct0 = min(split * run, nct), ct1 = min(ct0 + run, nct);
+    const int panels = (p.k + kPanel - 1) / kPanel, rb = p.k >> 1;
+    if (rt.grp == -2 || panels == 0) {
+        const int c0 = COLS * ct0, width = min(COLS * ct1, p.n) - c0;
+        for (int i = t >> 6; i < rt.rows; i += NT / 64)
+            for (int c = l; c < width; c += 64) store1(out + (size_t)(rt.row0 + i) * p.n + c0 + c, 0.f);
+        return;
+    }
+    const int rows = rt.rows, tiles = ct1 - ct0;
+
+    // the stream of (column tile, panel); a load brings eight rows, lane l row l / 8 into chunk place l % 8
+    const uint32_t ring0 = lds_u32(smem);
+    const int lr = l >> 3, lcol = 32 * wave + lr, lrow = 8 * MI * wave + lr;
+    const uint32_t byte0 = 16u * (uint32_t)((l & 7) ^ (lr >> 1)), byte1 = byte0 ^ 64u;   // of even and odd eights
+    const i32x4 rx = make_rsrc_v(p.lhs + (size_t)rt.row0 * rb, (uint32_t)rows * (uint32_t)rb);
+    const uint8_t* const wbase = p.rhs + (size_t)rt.grp * p.n * rb;
+    const uint8_t* const sbase = p.rhs_scale + (size_t)rt.grp * panels * p.n * 8;
+    const uint8_t* const xbase = p.lhs_scale + (size_t)rt.row0 * 8;
+    int lc = 0, lp = 0;   // tile and panel to load next
+    auto load = [&](int s) {
+        const bool live = lc < tiles;
+        const int col = live ? COLS * (ct0 + lc) : 0, cols = live ? min(COLS, p.n - col) : 0;
+        const i32x4 rw = make_rsrc_v(wbase + (size_t)col * rb, (uint32_t)cols * (uint32_t)rb);
+        const i32x4 rws = make_rsrc_v(sbase + ((size_t)lp * p.n + col) * 8, (uint32_t)cols * 8u);
+        const i32x4 rxs = make_rsrc_v(xbase + (size_t)lp * p.m * 8, live ? (uint32_t)rows * 8u : 0u);
+        const uint32_t at = ring0 + (uint32_t)(s * SLOT), pb = (uint32_t)lp * kRowBytes;
+        const bool ok0 = live && pb + byte0 < (uint32_t)rb, ok1 = live && pb + byte1 < (uint32_t)rb;   // chunks past k
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            load16(rw, at + 1024u * (uint32_t)(4 * wave + i), (i & 1 ? ok1 : ok0) ? (uint32_t)(lcol + 8 * i) * (uint32_t)rb + pb + (i & 1 ? byte1 : byte0) : kOOB);
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+            load16(rx, at + W + 1024u * (uint32_t)(MI * wave + i), (i & 1 ? ok1 : ok0) ? (uint32_t)(lrow + 8 * i) * (uint32_t)rb + pb + (i & 1 ? byte1 : byte0) : kOOB);
+        load4(rws, at + W + X + 256u * (uint32_t)wave, 256u * (uint32_t)wave + 4u * (uint32_t)l);
+        load4(rxs, at + W + X + WS + 256u * (uint32_t)(wave & 1), 256u * (uint32_t)(wave & 1) + 4u * (uint32_t)l);   // (two waves bring the same)
+        if (++lp == panels) { lp = 0; ++lc; }
+    };
+#pragma unroll
+    for (int s = 0; s < D - 1; ++s) load(s);
+
+    // fragments: lane l holds row l % 32 of a block of 32 and k blocks 4 (l / 32) + sub of the panel
+    const int h = l >> 5, r = l & 31;
+    const uint32_t chunk0 = (uint32_t)((4 * h) ^ ((l >> 1) & 7)) << 4;
+    const uint32_t aw = (uint32_t)(32 * wave + r) * kRowBytes + chunk0, ax = W + (uint32_t)r * kRowBytes + chunk0;
+    const uint32_t aws = W + X + (uint32_t)(32 * wave + r) * 8u + 4u * (uint32_t)h, axs = W + X + WS + (uint32_t)r * 8u + 4u * (uint32_t)h;
+    const int blocks = (rows + 31) >> 5;
+    int s = 0, ls = D - 1;
+    for (int c = 0; c < tiles; ++c) {
+        f32x16 acc[MI];
+#pragma unroll
+        for (int i = 0; i < MI; ++i)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[i][e] = 0.f;
+        for (int panel = 0; panel < panels; ++panel) {
+            // every wave's share of the oldest panel is in LDS, and the panel before it has been read
+            asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(LOADS * (D - 2)) : "memory");
+            load(ls);
+            ls = ls + 1 == D ? 0 : ls + 1;
+            const uint8_t* const at = smem + s * SLOT;
+            s = s + 1 == D ? 0 : s + 1;
+            i32x4 fw[SUB], fx[MI][SUB];
+            const int valid = (p.k >> 5) - panel * 8 - 4 * h;   // the lane's four k blocks inside k
+            const int sw = (int)keep_bytes(*(const uint32_t*)(at + aws), valid);
+            int sx[MI];
+#pragma unroll
+            for (int e = 0; e < SUB; ++e) fw[e] = *(const i32x4*)(at + (aw ^ (uint32_t)(e << 4)));
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+                sx[i] = (int)keep_bytes(*(const uint32_t*)(at + axs + 256 * i), valid);
+#pragma unroll
+                for (int e = 0; e < SUB; ++e) fx[i][e] = *(const i32x4*)(at + (ax ^ (uint32_t)(e << 4)) + 32 * i * kRowBytes);
+            }
+            // (without aligned rows of the output a lane holds rows of one column, and the lanes of a store are
+            // neighbours of one row)
+            static_for<0, MI>([&](auto i_c) {
+                constexpr int i = decltype(i_c)::value;
+                if (i > 0 && i >= blocks) return;
+                static_for<0, SUB>([&](auto e_c) {
+                    constexpr int e = decltype(e_c)::value;
+                    if constexpr (VEC) acc[i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(widen(fw[e]), widen(fx[i][e]), acc[i], kFp4, kFp4, e, sw, e, sx[i]);
+                    else acc[i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(widen(fx[i][e]), widen(fw[e]), acc[i], kFp4, kFp4, e, sx[i], e, sw);
+                });
+            });
+        }
+        // element 4 q + u of a block: its first operand's row 8 q + 4 h + u, its second's row l % 32
+        const int col0 = COLS * (ct0 + c) + 32 * wave;
+        const int col = VEC ? col0 + 4 * h : col0 + r;
+        int row = VEC ? r : 4 * h;
+        size_t o = (size_t)(rt.row0 + row) * p.n + col;
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+            if constexpr (VEC) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (row < rows && col + 8 * q < p.n) store4(out + o + 8 * q, f32x4{acc[i][4 * q], acc[i][4 * q + 1], acc[i][4 * q + 2], acc[i][4 * q + 3]}, 4, true);
+                row += 32;
+                o += (size_t)32 * p.n;
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    asm volatile("" : "+v"(o), "+v"(row));   // (or every store's address is computed ahead and held)
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        if (row + u < rows && col < p.n) store1(out + o + (size_t)u * p.n, acc[i][4 * q + u]);
+                    row += 8;
+                    o += (size_t)8 * p.n;
+                }
+            }
+        }
+    }
+    wait_vm<0>();   // no load may still be writing LDS when the workgroup ends
+}
+
+template <int PER>
+hipError_t launch_per(const Fp4Params& p, int64_t grid, int splits, int run, hipStream_t s) {
+    const bool vec = (p.n & 3) == 0 && ((uintptr_t)p.out & (p.out_f32 ? 15 : 7)) == 0;
+    const dim3 gr((uint32_t)grid), bl(NT);
+    if (p.out_f32) {
+        if (vec) hipLaunchKernelGGL((kernel<PER, float, true>), gr, bl, 0, s, p, splits, run);
+        else hipLaunchKernelGGL((kernel<PER, float, false>), gr, bl, 0, s, p, splits, run);
+    } else {
+        if (vec) hipLaunchKernelGGL((kernel<PER, uint16_t, true>), gr, bl, 0, s, p, splits, run);
+        else hipLaunchKernelGGL((kernel<PER, uint16_t, false>), gr, bl, 0, s, p, splits, run);
+    }
+    return hipGetLastError();
+}
+
+inline hipError_t launch(const Fp4Params& p, int cus, hipStream_t s) {
+    const int nct = (p.n + COLS - 1) / COLS;
+    const int64_t slots = slot_bound(p, ROWS);
+    // about eight workgroups a CU, none without a column tile but for the multiple of 8 (XCDs)
+    int64_t splits = (8 * (int64_t)cus + slots - 1) / slots;
+    if (splits > nct) splits = nct;
+    splits = splits < 8 ? 8 : (splits + 7) / 8 * 8;
+    const int run = (int)((nct + splits - 1) / splits);
+    const int64_t grid = slots * splits;
+    if (p.g <= 64) return launch_per<1>(p, grid, (int)splits, run, s);
+    if (p.g <= 256) return launch_per<4>(p, grid, (int)splits, run, s);
+    return launch_per<16>(p, grid, (int)splits, run, s);
+}
+}  // namespace block
 
 // Tile kernel: 256 x 256 tiles, four waves of 128 x 128 (4 x 4 blocks of 32x32x64 instructions, the results
 // in 256 accumulator registers), one workgroup a CU, each walking its tiles as one stream of panels (256
@@ -808,14 +814,20 @@ inline hipError_t launch_tile(const Fp4Params& p, int cus, hipStream_t s) {
 
 bool ragged_m_fp4_grid_ok(const Fp4Params& p) {
     // (column indices past n must not leave 32 bits either)
-    return p.n <= INT32_MAX - 256 && fp4::slot_bound(p, 16) * ((p.n + 15) / 16) <= INT32_MAX && (int64_t)64 * (p.k >> 1) < (int64_t(1) << 31);
+    return p.n <= INT32_MAX - 256 && fp4::slot_bound(p, 16) * ((p.n + 15) / 16) <= INT32_MAX && (int64_t)128 * (p.k >> 1) < (int64_t(1) << 31);
 }
 
 hipError_t launch_ragged_m_fp4(const Fp4Params& p, int cus, hipStream_t s) {
+    // By the mean number of rows of a group (all a host knows), times in us, of (g, k, n), at rows a group:
+    //   stream / block: (128, 2880, 5760) at 1 142 / 151, at 4 211 / 218, at 8 234 / 234, at 16 271 / 250;
+    //     (32, 2880, 1447) at 1 13.6 / 18.9, at 4 21.1 / 21.6, at 16 26 / 23.  Rows of k = 7168 leave a stream
+    //     workgroup a CU to itself: (128, 7168, 2048) at 4 183 / 163, whence the limit on their bytes.
+    //   block / tile: (32, 2880, 2880) at 48 45 / 54, at 64 51 / 58, at 112 66 / 61; (8, 4096, 14336) at 48
+    //     53 / 63, at 112 86 / 68; (128, 7168, 2048) at 32 179 / 184, at 56 205 / 193, at 80 310 / 203.
     const int64_t per = p.m / p.g;
-    if (per > 48 && fp4::tile_ok(p)) return fp4::launch_tile(p, cus, s);
-    if (per <= 24 && p.k > 0 && fp4::stream::row_bytes(p) <= fp4::stream::kMaxRowBytes) return fp4::stream::launch(p, cus, s);
-    return fp4::launch_split<2, 2, 2>(p, s);
+    if (per > 56 && fp4::tile_ok(p)) return fp4::launch_tile(p, cus, s);
+    if (per <= 4 && p.k > 0 && fp4::stream::row_bytes(p) <= fp4::stream::kMaxRowBytes) return fp4::stream::launch(p, cus, s);
+    return fp4::block::launch(p, cus, s);
 }
 
 }  // namespace gg
