@@ -13,5 +13,6 @@ _API = ("ragged_dot_m", "ragged_dot_m_noalloc", "ragged_dot_m_gated", "ragged_do
 def __getattr__(name):
     if name in _API:
         from . import _binding
-        return getattr(_binding, name)
+        globals()[name] = value = getattr(_binding, name)
+        return value
     raise AttributeError(name)

@@ -254,21 +254,27 @@ __global__ __launch_bounds__(256) void scatter_panels(const uint64_t* __restrict
 }
 
 // out[t, :] = sum_j w[t, j] * y[copy_to_sorted[t * top_k + j], :], fp32 sum in j order;
-// entries outside [0, rows) contribute nothing.  WPR waves per token; VEC: 8 consecutive
-// columns per lane with 16-byte (bf16) or 2 x 16-byte (fp32) accesses.
+// entries outside [0, rows) contribute nothing.  WPR waves per token; VEC (n >= 8): 8 consecutive
+// columns per lane with 16-byte (bf16) or 2 x 16-byte (fp32) accesses.  Bound by memory: 4096 tokens
+// of 7168 bf16 columns at top_k = 1 / 2 / 8 take 24 / 32 / 98 us (4.9 to 5.4 TB/s), 2048 of 7165
+// at top_k = 6 43 us.  Batches of eight for every top_k took 47 / 48 us, element accesses for
+// widths that 16 bytes do not divide 124.
 // (streaming accesses: each expert-output row is read once and each token row written once,
 // so they bypass the caches' retention with nontemporal hints)
+// (rows begin where the width puts them: the accesses are aligned to an element only)
+typedef i32x4 __attribute__((aligned(2))) i32x4_any;
+typedef f32x4 __attribute__((aligned(4))) f32x4_any;
 template <typename InT>
 __device__ inline void load8(const InT* p, float (&v)[8]) {
     if constexpr (sizeof(InT) == 2) {
-        const i32x4 q = __builtin_nontemporal_load((const i32x4*)p);
+        const i32x4 q = __builtin_nontemporal_load((const i32x4_any*)p);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             v[2 * e] = __uint_as_float((uint32_t)q[e] << 16);
             v[2 * e + 1] = __uint_as_float((uint32_t)q[e] & 0xffff0000u);
         }
     } else {
-        const f32x4 a = __builtin_nontemporal_load((const f32x4*)p), b = __builtin_nontemporal_load((const f32x4*)(p + 4));
+        const f32x4 a = __builtin_nontemporal_load((const f32x4_any*)p), b = __builtin_nontemporal_load((const f32x4_any*)(p + 4));
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             v[e] = a[e];
@@ -282,10 +288,10 @@ __device__ inline void store8(OutT* p, const float (&v)[8]) {
         i32x4 q;
 #pragma unroll
         for (int e = 0; e < 4; ++e) q[e] = (int)(f32_to_bf16(v[2 * e]) | ((uint32_t)f32_to_bf16(v[2 * e + 1]) << 16));
-        __builtin_nontemporal_store(q, (i32x4*)p);
+        __builtin_nontemporal_store(q, (i32x4_any*)p);
     } else {
-        __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, (f32x4*)p);
-        __builtin_nontemporal_store(f32x4{v[4], v[5], v[6], v[7]}, (f32x4*)(p + 4));
+        __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, (f32x4_any*)p);
+        __builtin_nontemporal_store(f32x4{v[4], v[5], v[6], v[7]}, (f32x4_any*)(p + 4));
     }
 }
 __device__ inline float ld1(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
@@ -295,21 +301,21 @@ __device__ inline void st1(float* p, float v) { *p = v; }
 
 // WEIGHTED = false: every weight is 1 (the gradient of the permute: a token's row is the plain sum
 // of its copies' gradients).
-template <typename InT, typename OutT, bool VEC, bool WEIGHTED>
+template <typename InT, typename OutT, bool VEC, bool WEIGHTED, int WPR>
 __global__ __launch_bounds__(256) void combine(const InT* __restrict__ y, int rows, const int32_t* __restrict__ c2s,
                                                const float* __restrict__ w, int T, int top_k, int n,
                                                OutT* __restrict__ out) {
     // wave-uniform token: positions and weights come in through scalar loads
     const int wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = threadIdx.x & 63;
-    const int t = blockIdx.x * TPB + wv / WPR, h = wv % WPR;
+    const int t = blockIdx.x * (4 / WPR) + wv / WPR, h = wv % WPR;
     if (t >= T) return;
     const int32_t* pos = c2s + (size_t)t * top_k;
     const float* wt = WEIGHTED ? w + (size_t)t * top_k : nullptr;
     OutT* orow = out + (size_t)t * n;
     if constexpr (VEC) {
-        // eight copies at a time.  Copies without a sorted row (and slots past top_k) read
-        // row 0 and are replaced by zeros with a select, so the eight loads issue back to
-        // back with no branch between them.
+        // up to eight copies at a time.  Copies without a sorted row (and slots past top_k) read
+        // row 0 and are replaced by zeros with a select, so a batch's loads issue back to back
+        // with no branch between them.  The batch is no larger than top_k needs.
         struct Eight { int p[8]; bool ok[8]; float w[8]; };
         auto fetch = [&](int j0, Eight& q) {
 #pragma unroll
@@ -321,27 +327,36 @@ __global__ __launch_bounds__(256) void combine(const InT* __restrict__ y, int ro
                 q.w[jj] = q.ok[jj] ? (WEIGHTED ? wt[j] : 1.f) : 0.f;
             }
         };
-        auto accumulate = [&](const Eight& q, int c0, float (&acc)[8]) {
-            float v[8][8];
+        auto accumulate = [&](auto k_c, const Eight& q, int c0, float (&acc)[8]) {
+            constexpr int K = decltype(k_c)::value;
+            float v[K][8];
 #pragma unroll
-            for (int jj = 0; jj < 8; ++jj) load8(y + (size_t)q.p[jj] * n + c0, v[jj]);
+            for (int jj = 0; jj < K; ++jj) load8(y + (size_t)q.p[jj] * n + c0, v[jj]);
 #pragma unroll
-            for (int jj = 0; jj < 8; ++jj)
+            for (int jj = 0; jj < K; ++jj)
 #pragma unroll
                 for (int e = 0; e < 8; ++e) acc[e] = __builtin_fmaf(q.w[jj], q.ok[jj] ? v[jj][e] : 0.f, acc[e]);
         };
         Eight first;
         fetch(0, first);
-        for (int c0 = 512 * h + 8 * l; c0 < n; c0 += WPR * 512) {
-            float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-            accumulate(first, c0, acc);
-            for (int j0 = 8; j0 < top_k; j0 += 8) {
-                Eight more;
-                fetch(j0, more);
-                accumulate(more, c0, acc);
+        // (a row's last eight elements may overlap the eight before and are then written twice, the same)
+        auto columns = [&](auto k_c) {
+            for (int c1 = 512 * h + 8 * l; c1 < n; c1 += WPR * 512) {
+                const int c0 = min(c1, n - 8);
+                float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                accumulate(k_c, first, c0, acc);
+                for (int j0 = 8; j0 < top_k; j0 += 8) {
+                    Eight more;
+                    fetch(j0, more);
+                    accumulate(std::integral_constant<int, 8>{}, more, c0, acc);
+                }
+                store8(orow + c0, acc);
             }
-            store8(orow + c0, acc);
-        }
+        };
+        if (top_k > 4) columns(std::integral_constant<int, 8>{});
+        else if (top_k > 2) columns(std::integral_constant<int, 4>{});
+        else if (top_k > 1) columns(std::integral_constant<int, 2>{});
+        else columns(std::integral_constant<int, 1>{});
     } else {
         for (int c = 64 * h + l; c < n; c += WPR * 64) {
             float acc = 0.f;
@@ -355,21 +370,23 @@ __global__ __launch_bounds__(256) void combine(const InT* __restrict__ y, int ro
     }
 }
 
-template <typename InT, typename OutT, bool WEIGHTED>
-hipError_t launch_combine_w(const void* y, int rows, const int32_t* c2s, const float* w, int T, int top_k, int n,
-                            void* out, bool vec, hipStream_t s) {
-    const dim3 grid((T + TPB - 1) / TPB), block(256);
-    if (vec)
-        hipLaunchKernelGGL((combine<InT, OutT, true, WEIGHTED>), grid, block, 0, s, (const InT*)y, rows, c2s, w, T, top_k, n, (OutT*)out);
+template <typename InT, typename OutT, bool WEIGHTED, int W>
+void launch_combine_w(const void* y, int rows, const int32_t* c2s, const float* w, int T, int top_k, int n, void* out, hipStream_t s) {
+    const dim3 grid((T + 4 / W - 1) / (4 / W)), block(256);
+    if (n >= 8)
+        hipLaunchKernelGGL((combine<InT, OutT, true, WEIGHTED, W>), grid, block, 0, s, (const InT*)y, rows, c2s, w, T, top_k, n, (OutT*)out);
     else
-        hipLaunchKernelGGL((combine<InT, OutT, false, WEIGHTED>), grid, block, 0, s, (const InT*)y, rows, c2s, w, T, top_k, n, (OutT*)out);
-    return hipGetLastError();
+        hipLaunchKernelGGL((combine<InT, OutT, false, WEIGHTED, W>), grid, block, 0, s, (const InT*)y, rows, c2s, w, T, top_k, n, (OutT*)out);
 }
 template <typename InT, typename OutT>
 hipError_t launch_combine_t(const void* y, int rows, const int32_t* c2s, const float* w, int T, int top_k, int n,
-                            void* out, bool vec, hipStream_t s) {
-    return w ? launch_combine_w<InT, OutT, true>(y, rows, c2s, w, T, top_k, n, out, vec, s)
-             : launch_combine_w<InT, OutT, false>(y, rows, c2s, w, T, top_k, n, out, vec, s);
+                            void* out, hipStream_t s) {
+    // (of at most 512 columns a second wave would have none)
+    if (n <= 512) w ? launch_combine_w<InT, OutT, true, 1>(y, rows, c2s, w, T, top_k, n, out, s)
+                    : launch_combine_w<InT, OutT, false, 1>(y, rows, c2s, w, T, top_k, n, out, s);
+    else w ? launch_combine_w<InT, OutT, true, 2>(y, rows, c2s, w, T, top_k, n, out, s)
+           : launch_combine_w<InT, OutT, false, 2>(y, rows, c2s, w, T, top_k, n, out, s);
+    return hipGetLastError();
 }
 
 }  // namespace perm
@@ -420,14 +437,11 @@ hipError_t launch_permute(const PermuteArgs& a, hipStream_t s) {
 hipError_t launch_combine(const void* y, bool y_bf16, int rows, const int32_t* c2s, const float* w, int T, int top_k,
                           int n, void* out, bool out_bf16, hipStream_t s) {
     if (T == 0 || n == 0) return hipSuccess;
-    const size_t ey = y_bf16 ? 2 : 4, eo = out_bf16 ? 2 : 4;
-    const bool vec = n % 8 == 0 && (uintptr_t)y % 16 == 0 && (uintptr_t)out % 16 == 0 && (n * ey) % 16 == 0 &&
-                     (n * eo) % 16 == 0;
     if (y_bf16)
-        return out_bf16 ? perm::launch_combine_t<uint16_t, uint16_t>(y, rows, c2s, w, T, top_k, n, out, vec, s)
-                        : perm::launch_combine_t<uint16_t, float>(y, rows, c2s, w, T, top_k, n, out, vec, s);
-    return out_bf16 ? perm::launch_combine_t<float, uint16_t>(y, rows, c2s, w, T, top_k, n, out, vec, s)
-                    : perm::launch_combine_t<float, float>(y, rows, c2s, w, T, top_k, n, out, vec, s);
+        return out_bf16 ? perm::launch_combine_t<uint16_t, uint16_t>(y, rows, c2s, w, T, top_k, n, out, s)
+                        : perm::launch_combine_t<uint16_t, float>(y, rows, c2s, w, T, top_k, n, out, s);
+    return out_bf16 ? perm::launch_combine_t<float, uint16_t>(y, rows, c2s, w, T, top_k, n, out, s)
+                    : perm::launch_combine_t<float, float>(y, rows, c2s, w, T, top_k, n, out, s);
 }
 
 }  // namespace gg

@@ -3,7 +3,10 @@
 // One pass: the waves of token t read its dout row once, and for each of its copies read the copy's y row
 // and write its dy row, so every row of dout, y and dy moves once (3 row widths a copy at top_k = 1, tending
 // to 2): bound by memory.  dw's partial sums stay in fp32 registers, are added over the wave's lanes by
-// exchanges and over the token's waves in LDS, in a fixed order.
+// exchanges and over the token's waves in LDS, in a fixed order.  4096 tokens of 7168 bf16 columns at
+// top_k = 1 / 2 / 8: 38 / 59 / 201 us (4.7 to 5.0 TB/s); 2048 of 7165 at top_k = 6 92 us.  Batches of eight
+// for every top_k took 53 / 67 us, element accesses for widths that 16 bytes do not divide 234, and two waves
+// for widths of which one wave takes all 126 against 69 us (65536 tokens of 512).
 //
 // A dy row is written by the one copy that sorted_to_copy names for it (and that points back to it), so the
 // result does not depend on the order of waves even for index arrays that no permute wrote; rows that no
@@ -19,9 +22,12 @@ constexpr int KB = 8;   // copies handled at a time
 
 __device__ inline float up(uint32_t u) { return __uint_as_float(u); }
 
-// eight consecutive elements as floats
+// eight consecutive elements as floats; rows begin where the width puts them, so the 16-byte accesses are
+// aligned to an element only (the target's global memory takes that)
+typedef i32x4 __attribute__((aligned(2))) i32x4_any;
+typedef f32x4 __attribute__((aligned(4))) f32x4_any;
 __device__ inline void load8(const uint16_t* p, float (&v)[8]) {
-    const i32x4 q = __builtin_nontemporal_load((const i32x4*)p);
+    const i32x4 q = __builtin_nontemporal_load((const i32x4_any*)p);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         v[2 * e] = up((uint32_t)q[e] << 16);
@@ -29,7 +35,7 @@ __device__ inline void load8(const uint16_t* p, float (&v)[8]) {
     }
 }
 __device__ inline void load8(const float* p, float (&v)[8]) {
-    const f32x4 a = __builtin_nontemporal_load((const f32x4*)p), b = __builtin_nontemporal_load((const f32x4*)(p + 4));
+    const f32x4 a = __builtin_nontemporal_load((const f32x4_any*)p), b = __builtin_nontemporal_load((const f32x4_any*)(p + 4));
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         v[e] = a[e];
@@ -39,11 +45,11 @@ __device__ inline void load8(const float* p, float (&v)[8]) {
 __device__ inline void store8(uint16_t* p, const float (&v)[8]) {
     const i32x4 q = {(int)ring::pack_bf16(v[0], v[1]), (int)ring::pack_bf16(v[2], v[3]), (int)ring::pack_bf16(v[4], v[5]),
                      (int)ring::pack_bf16(v[6], v[7])};
-    __builtin_nontemporal_store(q, (i32x4*)p);
+    __builtin_nontemporal_store(q, (i32x4_any*)p);
 }
 __device__ inline void store8(float* p, const float (&v)[8]) {
-    __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, (f32x4*)p);
-    __builtin_nontemporal_store(f32x4{v[4], v[5], v[6], v[7]}, (f32x4*)(p + 4));
+    __builtin_nontemporal_store(f32x4{v[0], v[1], v[2], v[3]}, (f32x4_any*)p);
+    __builtin_nontemporal_store(f32x4{v[4], v[5], v[6], v[7]}, (f32x4_any*)(p + 4));
 }
 __device__ inline float ld1(const uint16_t* p) { return up((uint32_t)*p << 16); }
 __device__ inline float ld1(const float* p) { return *p; }
@@ -97,23 +103,35 @@ __global__ __launch_bounds__(256) void kernel(UnpermuteGradArgs a, int tok_block
         }
         if (on) {
             if constexpr (VEC) {
-                for (int c = 512 * h + 8 * l; c < n; c += 512 * WPT) {
-                    float d[8];
-                    load8(drow + c, d);
-                    float y[KB][8];
+                // (a row's last eight elements may overlap the eight before: their dy is written twice, the same,
+                // and their products are left out of the second sum)
+                auto columns = [&](auto k_c) {
+                    constexpr int K = decltype(k_c)::value;   // copies whose rows are read: absent ones among them read row 0
+                    for (int c0 = 512 * h + 8 * l; c0 < n; c0 += 512 * WPT) {
+                        const int c = min(c0, n - 8), done = c0 - c;
+                        float d[8];
+                        load8(drow + c, d);
+                        float y[K][8];
 #pragma unroll
-                    for (int j = 0; j < KB; ++j) load8((const T*)a.y + (size_t)(pos[j] < 0 ? 0 : pos[j]) * n + c, y[j]);
+                        for (int j = 0; j < K; ++j) load8((const T*)a.y + (size_t)(pos[j] < 0 ? 0 : pos[j]) * n + c, y[j]);
 #pragma unroll
-                    for (int j = 0; j < KB; ++j) {
-                        float o[8];
+                        for (int j = 0; j < K; ++j) {
+                            float o[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            acc[j] = __builtin_fmaf(d[e], pos[j] < 0 ? 0.f : y[j][e], acc[j]);
-                            o[e] = w[j] * d[e];
+                            for (int e = 0; e < 8; ++e) {
+                                acc[j] = __builtin_fmaf(e < done ? 0.f : d[e], pos[j] < 0 || e < done ? 0.f : y[j][e], acc[j]);
+                                o[e] = w[j] * d[e];
+                            }
+                            if (claim[j]) store8(dy + (size_t)pos[j] * n + c, o);
                         }
-                        if (claim[j]) store8(dy + (size_t)pos[j] * n + c, o);
                     }
-                }
+                };
+                // (loads behind a branch each would wait for one another; a batch of eight where there are two
+                // copies costs half the speed)
+                if (a.top_k - j0 > 4) columns(std::integral_constant<int, 8>{});
+                else if (a.top_k - j0 > 2) columns(std::integral_constant<int, 4>{});
+                else if (a.top_k - j0 > 1) columns(std::integral_constant<int, 2>{});
+                else columns(std::integral_constant<int, 1>{});
             } else {
                 for (int c = 64 * h + l; c < n; c += 64 * WPT) {
                     const float d = ld1(drow + c);
@@ -151,18 +169,18 @@ __global__ __launch_bounds__(256) void kernel(UnpermuteGradArgs a, int tok_block
 }
 
 template <typename T, int WPT>
-void launch_w(const UnpermuteGradArgs& a, bool vec, hipStream_t s) {
+void launch_w(const UnpermuteGradArgs& a, hipStream_t s) {
     const int tpb = 4 / WPT, tok_blocks = (a.tokens + tpb - 1) / tpb;
     const int64_t M = (int64_t)a.tokens * a.top_k;
     const int clear = (int)((M + 255) / 256 < 256 ? (M + 255) / 256 : 256);
-    if (vec) hipLaunchKernelGGL((kernel<T, true, WPT>), dim3(tok_blocks + clear), dim3(256), 0, s, a, tok_blocks);
+    if (a.n >= 8) hipLaunchKernelGGL((kernel<T, true, WPT>), dim3(tok_blocks + clear), dim3(256), 0, s, a, tok_blocks);
     else hipLaunchKernelGGL((kernel<T, false, WPT>), dim3(tok_blocks + clear), dim3(256), 0, s, a, tok_blocks);
 }
 
 template <typename T>
 hipError_t launch_t(const UnpermuteGradArgs& a, hipStream_t s) {
-    const bool vec = a.n % 8 == 0 && (uintptr_t)a.dout % 16 == 0 && (uintptr_t)a.y % 16 == 0 && (uintptr_t)a.dy % 16 == 0;
-    launch_w<T, 2>(a, vec, s);
+    if (a.n <= 512) launch_w<T, 1>(a, s);   // (a second wave would have no columns)
+    else launch_w<T, 2>(a, s);
     return hipGetLastError();
 }
 
