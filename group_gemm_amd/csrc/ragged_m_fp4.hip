@@ -1,6 +1,8 @@
 // ragged_m_fp4.hip -- the MXFP4 non-contracting ragged dot on gfx950: out[r, :] = lhs[r, :] . rhs[h]^T for
 // the rows r of group h, both operands e2m1 codes with k contiguous and E8M0 scales in panels
 // [ceil(k/256), rows, 8], fp32 accumulation in v_mfma_scale_f32_*_f8f6f4.
+#include <cmath>
+
 #include "common.hpp"
 #include "launch.hpp"
 #include "ring.hpp"
@@ -115,12 +117,16 @@ __device__ inline uint32_t keep_bytes(uint32_t w, int valid) { return valid >= 4
 __device__ inline void store1(uint16_t* p, float v) { *p = (uint16_t)pack_bf16(v, 0.f); }
 __device__ inline void store1(float* p, float v) { *p = v; }
 
-// Four consecutive columns of one row; `left` = columns of the row from here on.
+// Four consecutive columns of one row; `left` = columns of the row from here on.  A row begins where n puts it,
+// so the stores are aligned to an element only (the target's global memory takes that).
+typedef i32x2 __attribute__((aligned(2))) i32x2_any;
+typedef i32x4 __attribute__((aligned(2))) i32x4_any;
+typedef f32x4 __attribute__((aligned(4))) f32x4_any;
 template <typename OutT>
-__device__ inline void store4(OutT* o, f32x4 v, int left, bool vec) {
-    if (vec && left >= 4) {
-        if constexpr (sizeof(OutT) == 2) *(i32x2*)o = i32x2{(int)pack_bf16(v[0], v[1]), (int)pack_bf16(v[2], v[3])};
-        else *(f32x4*)o = v;
+__device__ inline void store4(OutT* o, f32x4 v, int left) {
+    if (left >= 4) {
+        if constexpr (sizeof(OutT) == 2) *(i32x2_any*)o = i32x2{(int)pack_bf16(v[0], v[1]), (int)pack_bf16(v[2], v[3])};
+        else *(f32x4_any*)o = v;
     } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -145,9 +151,7 @@ __global__ __launch_bounds__(64 * WAVES) void kernel(Fp4Params p, int splits, in
     // that are not there (their results are not stored) read on
     __shared__ __attribute__((aligned(16))) uint8_t smem[WAVES * D * SLOT + kMaxRowBytes + 1024];
     const int t = threadIdx.x, l = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
-    // split c of every row tile runs on XCD c % 8 (a group's row tiles share their weights in its L2)
-    const int idx = blockIdx.x >> 3, per = splits >> 3;
-    const int slot = idx / per, split = (idx % per) * 8 + (blockIdx.x & 7);
+    const int slot = blockIdx.x / splits, split = blockIdx.x % splits;
     uint32_t flags;
     const RowTile rt = find_row_tile<PER>(p.group_sizes, p.g, p.m, 16, slot, &flags);
     if (blockIdx.x == 0 && t == 0) *p.status = flags;
@@ -209,7 +213,6 @@ __global__ __launch_bounds__(64 * WAVES) void kernel(Fp4Params p, int splits, in
 
     const int r = l & 15, q = l >> 4;
     const uint32_t c0 = (uint32_t)(((2 * q) ^ swizzle(r)) << 4), c1 = c0 ^ 16u;   // chunks 2 q and 2 q + 1 of row r
-    const bool vec = (p.n & 3) == 0 && ((uintptr_t)p.out & (4 * sizeof(OutT) - 1)) == 0;
     int s = 0;
     for (int c = 0; c < tiles; ++c) {
         f32x4 acc0 = {0.f, 0.f, 0.f, 0.f}, acc1 = {0.f, 0.f, 0.f, 0.f};
@@ -234,7 +237,7 @@ __global__ __launch_bounds__(64 * WAVES) void kernel(Fp4Params p, int splits, in
             f32x4 v;
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = acc0[e] + acc1[e];
-            store4(out + (size_t)(rt.row0 + r) * p.n + col, v, p.n - col, vec);
+            store4(out + (size_t)(rt.row0 + r) * p.n + col, v, p.n - col);
         }
     }
     wait_vm<0>();   // no load may still be writing LDS when the workgroup ends
@@ -254,10 +257,10 @@ hipError_t launch_per(const Fp4Params& p, int64_t grid, int splits, int xrows, h
 inline hipError_t launch(const Fp4Params& p, int cus, hipStream_t s) {
     const int nct = (p.n + 15) / 16;
     const int64_t slots = slot_bound(p, 16);
-    // about eight workgroups a CU, none with fewer than a column tile a wave; a multiple of 8 (XCDs)
+    // about eight workgroups a CU, none with fewer than a column tile a wave
     int64_t splits = (8 * (int64_t)cus + slots - 1) / slots;
     if (splits > nct / WAVES) splits = nct / WAVES;
-    splits = splits < 8 ? 8 : (splits + 7) / 8 * 8;
+    if (splits < 1) splits = 1;
     const int64_t grid = slots * splits;
     const int xrows = p.m <= 8 ? 8 : 16;
     if (p.g <= 64) return launch_per<1>(p, grid, (int)splits, xrows, s);
@@ -278,14 +281,16 @@ constexpr int ROWS = 64, COLS = 128, NT = 256, D = 3, SUB = 4, MI = ROWS / 32;
 constexpr int W = COLS * kRowBytes, X = ROWS * kRowBytes, WS = COLS * 8, XS = ROWS * 8, SLOT = W + X + WS + XS;
 constexpr int LOADS = 8;   // a wave's loads of a panel: 4 of weights, 2 of rows, 1 of each one's scales
 
-// VEC: four consecutive columns of a row are one aligned store
-template <int PER, typename OutT, bool VEC>
-__global__ __launch_bounds__(NT, 2) void kernel(Fp4Params p, int splits, int run) {
+template <int PER, typename OutT>
+__global__ __launch_bounds__(NT, 2) void kernel(Fp4Params p, int splits, int run, int together) {
     __shared__ __attribute__((aligned(16))) uint8_t smem[D * SLOT];
     const int t = threadIdx.x, l = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
-    // split c of every row tile runs on XCD c % 8 (a group's row tiles share their weights in its L2)
-    const int idx = blockIdx.x >> 3, per = splits >> 3;
-    const int slot = idx / per, split = (idx % per) * 8 + (blockIdx.x & 7);
+    int slot = blockIdx.x / splits, split = blockIdx.x % splits;
+    if (together) {   // a group's row tiles at the same columns run side by side on one XCD and share the weights in its L2
+        const int slots = gridDim.x / splits, v = xcd_virtual_id(blockIdx.x, gridDim.x);
+        slot = v % slots;
+        split = v / slots;
+    }
     uint32_t flags;
     const RowTile rt = find_row_tile<PER>(p.group_sizes, p.g, p.m, ROWS, slot, &flags);
     if (blockIdx.x == 0 && t == 0) *p.status = flags;
@@ -364,73 +369,51 @@ __global__ __launch_bounds__(NT, 2) void kernel(Fp4Params p, int splits, int run
 #pragma unroll
                 for (int e = 0; e < SUB; ++e) fx[i][e] = *(const i32x4*)(at + (ax ^ (uint32_t)(e << 4)) + 32 * i * kRowBytes);
             }
-            // (without aligned rows of the output a lane holds rows of one column, and the lanes of a store are
-            // neighbours of one row)
+            // (the weights first, so that a lane holds four columns of one row)
             static_for<0, MI>([&](auto i_c) {
                 constexpr int i = decltype(i_c)::value;
                 if (i > 0 && i >= blocks) return;
                 static_for<0, SUB>([&](auto e_c) {
                     constexpr int e = decltype(e_c)::value;
-                    if constexpr (VEC) acc[i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(widen(fw[e]), widen(fx[i][e]), acc[i], kFp4, kFp4, e, sw, e, sx[i]);
-                    else acc[i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(widen(fx[i][e]), widen(fw[e]), acc[i], kFp4, kFp4, e, sx[i], e, sw);
+                    acc[i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(widen(fw[e]), widen(fx[i][e]), acc[i], kFp4, kFp4, e, sw, e, sx[i]);
                 });
             });
         }
-        // element 4 q + u of a block: its first operand's row 8 q + 4 h + u, its second's row l % 32
-        const int col0 = COLS * (ct0 + c) + 32 * wave;
-        const int col = VEC ? col0 + 4 * h : col0 + r;
-        int row = VEC ? r : 4 * h;
-        size_t o = (size_t)(rt.row0 + row) * p.n + col;
+        // element 4 q + u of block i: row 32 i + l % 32, column 8 q + 4 h + u of the wave's
+        const int col = COLS * (ct0 + c) + 32 * wave + 4 * h;
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
-            if constexpr (VEC) {
+            const int row = 32 * i + r;
+            OutT* const o = out + (size_t)(rt.row0 + row) * p.n + col;
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    if (row < rows && col + 8 * q < p.n) store4(out + o + 8 * q, f32x4{acc[i][4 * q], acc[i][4 * q + 1], acc[i][4 * q + 2], acc[i][4 * q + 3]}, 4, true);
-                row += 32;
-                o += (size_t)32 * p.n;
-            } else {
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    asm volatile("" : "+v"(o), "+v"(row));   // (or every store's address is computed ahead and held)
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        if (row + u < rows && col < p.n) store1(out + o + (size_t)u * p.n, acc[i][4 * q + u]);
-                    row += 8;
-                    o += (size_t)8 * p.n;
-                }
-            }
+            for (int q = 0; q < 4; ++q)
+                if (row < rows && col + 8 * q < p.n) store4(o + 8 * q, f32x4{acc[i][4 * q], acc[i][4 * q + 1], acc[i][4 * q + 2], acc[i][4 * q + 3]}, p.n - col - 8 * q);
         }
     }
     wait_vm<0>();   // no load may still be writing LDS when the workgroup ends
 }
 
 template <int PER>
-hipError_t launch_per(const Fp4Params& p, int64_t grid, int splits, int run, hipStream_t s) {
-    const bool vec = (p.n & 3) == 0 && ((uintptr_t)p.out & (p.out_f32 ? 15 : 7)) == 0;
-    const dim3 gr((uint32_t)grid), bl(NT);
-    if (p.out_f32) {
-        if (vec) hipLaunchKernelGGL((kernel<PER, float, true>), gr, bl, 0, s, p, splits, run);
-        else hipLaunchKernelGGL((kernel<PER, float, false>), gr, bl, 0, s, p, splits, run);
-    } else {
-        if (vec) hipLaunchKernelGGL((kernel<PER, uint16_t, true>), gr, bl, 0, s, p, splits, run);
-        else hipLaunchKernelGGL((kernel<PER, uint16_t, false>), gr, bl, 0, s, p, splits, run);
-    }
+hipError_t launch_per(const Fp4Params& p, int64_t grid, int splits, int run, int together, hipStream_t s) {
+    if (p.out_f32) hipLaunchKernelGGL((kernel<PER, float>), dim3((uint32_t)grid), dim3(NT), 0, s, p, splits, run, together);
+    else hipLaunchKernelGGL((kernel<PER, uint16_t>), dim3((uint32_t)grid), dim3(NT), 0, s, p, splits, run, together);
     return hipGetLastError();
 }
 
 inline hipError_t launch(const Fp4Params& p, int cus, hipStream_t s) {
     const int nct = (p.n + COLS - 1) / COLS;
     const int64_t slots = slot_bound(p, ROWS);
-    // about eight workgroups a CU, none without a column tile but for the multiple of 8 (XCDs)
-    int64_t splits = (8 * (int64_t)cus + slots - 1) / slots;
-    if (splits > nct) splits = nct;
-    splits = splits < 8 ? 8 : (splits + 7) / 8 * 8;
-    const int run = (int)((nct + splits - 1) / splits);
-    const int64_t grid = slots * splits;
-    if (p.g <= 64) return launch_per<1>(p, grid, (int)splits, run, s);
-    if (p.g <= 256) return launch_per<4>(p, grid, (int)splits, run, s);
-    return launch_per<16>(p, grid, (int)splits, run, s);
+    // about eight workgroups a CU, or one for every column tile of every row tile
+    int64_t run = slots * nct / (8 * (int64_t)cus);
+    run = run > nct ? nct : run;
+    run = run < 1 ? 1 : run;
+    int64_t splits = (nct + run - 1) / run;
+    splits = splits < 1 ? 1 : splits;   // (n = 0: the status word alone)
+    const int together = p.m / p.g > ROWS && splits >= 8;   // (else an XCD's share could be mostly empty row tiles)
+    const int64_t grid = together ? (slots * splits + 7) / 8 * 8 : slots * splits;   // (past the last split: nothing)
+    if (p.g <= 64) return launch_per<1>(p, grid, (int)splits, (int)run, together, s);
+    if (p.g <= 256) return launch_per<4>(p, grid, (int)splits, (int)run, together, s);
+    return launch_per<16>(p, grid, (int)splits, (int)run, together, s);
 }
 }  // namespace block
 
@@ -640,7 +623,7 @@ __global__ __launch_bounds__(NT, 1) void kernel(Fp4Params p) {
         with_nb<2>((blocks + 1) >> 1, [&](auto nb_c) {
             constexpr int NB = 2 * decltype(nb_c)::value;
             f32x16 acc[NB > 0 ? NB : 1][NJ];
-            constexpr int STORES = MI * (NJ / JS) * 8 * (WHOLE ? 1 : PIECE);   // a wave's of a whole tile
+            constexpr int STORES = MI * (NJ / JS) * 8;   // a wave's of a whole tile
             // One panel: 16 steps a sub-slice, each at most one MFMA and the reads and loads that go with it.
             // FIRST: the tile's first panel, whose turn and loads are done already.  follow: the panel after it,
             // lp: the panel to load.
@@ -761,12 +744,17 @@ __global__ __launch_bounds__(NT, 1) void kernel(Fp4Params p) {
                 const i32x4 v = *(const __attribute__((address_space(3))) i32x4*)(uintptr_t)(take + 256u * r + (turned ^ (srow + ((r & 15) << 4))));
                 if constexpr (WHOLE) {
                     bstore(ro, col < p.n ? off : kOOB, v);
-                } else {
+                } else if (r0w + 32 * i + r + (int)(srow >> 4) < cur.rows) {
+                    uint8_t* const o = (uint8_t*)out + (size_t)cur.row0 * row_bytes + off;
+                    if (col + PIECE <= p.n) {
+                        *(i32x4_any*)o = v;
+                    } else {
 #pragma unroll
-                    for (int e = 0; e < PIECE; ++e) {
-                        const uint32_t at = col + e < p.n ? off + (uint32_t)(e * OSZ) : kOOB;
-                        if constexpr (OSZ == 2) __builtin_amdgcn_raw_buffer_store_b16((uint16_t)((uint32_t)v[e >> 1] >> (16 * (e & 1))), ro, at, 0, 0);
-                        else __builtin_amdgcn_raw_buffer_store_b32((uint32_t)v[e & 3], ro, at, 0, 0);
+                        for (int e = 0; e < PIECE; ++e) {
+                            if (col + e >= p.n) break;
+                            if constexpr (OSZ == 2) *(uint16_t*)(o + 2 * e) = (uint16_t)((uint32_t)v[e >> 1] >> (16 * (e & 1)));
+                            else *(int*)(o + 4 * e) = v[e & 3];
+                        }
                     }
                 }
                 off += 4 * row_bytes;
@@ -776,7 +764,7 @@ __global__ __launch_bounds__(NT, 1) void kernel(Fp4Params p) {
         __builtin_amdgcn_sched_barrier(0);
         issue_some(std::integral_constant<int, 8>{}, std::integral_constant<int, 16>{}, lp2);
         lslot ^= 1;
-        stored = NB == MI;
+        stored = WHOLE && NB == MI;
         });
         cur.row0 = scalar(next.row0); cur.rows = scalar(next.rows); cur.col0 = scalar(next.col0); cur.turn0 = scalar(next.turn0);
     }
@@ -810,6 +798,20 @@ inline hipError_t launch_tile(const Fp4Params& p, int cus, hipStream_t s) {
     return hipGetLastError();
 }
 
+// Tile or block kernel, by the times that their tiles' numbers and panels give (a host knows the groups' mean
+// size only: a group of mean size has a half-filled tile more than it fills, and at least one).  In us on 256
+// CUs: the tile kernel's CUs take ceil(tiles / CUs) tiles each, 6 and 1.4 to 2.1 a panel with the tile's rows,
+// the block kernel's 1.6 and 0.7 a panel for each of its tiles / CUs.  Measured, block / tile, at (groups, k, n) x
+// rows a group: (32, 2880, 2880) x 48 45 / 54, x 64 51 / 58, x 112 66 / 61; (8, 4096, 14336) x 48 53 / 63,
+// x 112 86 / 68; (128, 7168, 2048) x 32 179 / 184, x 48 204 / 192, x 80 310 / 203; few long groups, which are few
+// tiles, (1, 6688, 2752) x 783 32 / 56, (8, 6400, 1344) x 272 26 / 47; (16, 1184, 1600) x 927 60 / 35.
+inline bool tile_faster(const Fp4Params& p, int cus) {
+    const double used = p.g < p.m ? p.g : p.m, per = p.m / used, panels = (p.k + kPanel - 1) / kPanel;
+    const double t = used * fmax(1., per / tile::BM + .5) * ((p.n + tile::BN - 1) / tile::BN);
+    const double b = used * fmax(1., per / block::ROWS + .5) * ((p.n + block::COLS - 1) / block::COLS);
+    return ceil(t / cus) * (6. + (1.4 + .7 * fmin(1., per / tile::BM)) * panels) < b / cus * (1.6 + .7 * panels);
+}
+
 }  // namespace fp4
 
 bool ragged_m_fp4_grid_ok(const Fp4Params& p) {
@@ -818,15 +820,11 @@ bool ragged_m_fp4_grid_ok(const Fp4Params& p) {
 }
 
 hipError_t launch_ragged_m_fp4(const Fp4Params& p, int cus, hipStream_t s) {
-    // By the mean number of rows of a group (all a host knows), times in us, of (g, k, n), at rows a group:
-    //   stream / block: (128, 2880, 5760) at 1 142 / 151, at 4 211 / 218, at 8 234 / 234, at 16 271 / 250;
-    //     (32, 2880, 1447) at 1 13.6 / 18.9, at 4 21.1 / 21.6, at 16 26 / 23.  Rows of k = 7168 leave a stream
-    //     workgroup a CU to itself: (128, 7168, 2048) at 4 183 / 163, whence the limit on their bytes.
-    //   block / tile: (32, 2880, 2880) at 48 45 / 54, at 64 51 / 58, at 112 66 / 61; (8, 4096, 14336) at 48
-    //     53 / 63, at 112 86 / 68; (128, 7168, 2048) at 32 179 / 184, at 56 205 / 193, at 80 310 / 203.
-    const int64_t per = p.m / p.g;
-    if (per > 56 && fp4::tile_ok(p)) return fp4::launch_tile(p, cus, s);
-    if (per <= 4 && p.k > 0 && fp4::stream::row_bytes(p) <= fp4::stream::kMaxRowBytes) return fp4::stream::launch(p, cus, s);
+    // Stream or block kernel, in us, at (groups, k, n) x rows a group: (128, 1440, 6344) x 2 115 / 124, (64, 992,
+    // 6244) x 2 43 / 49, (128, 2880, 5760) x 1 142 / 151, x 4 211 / 218, x 8 234 / 234, x 16 271 / 250.  With
+    // rows of more than 28 KiB a stream workgroup has a CU to itself: (128, 7168, 2048) x 4 183 / 163.
+    if (p.m / p.g <= 4 && p.k > 0 && fp4::stream::row_bytes(p) <= fp4::stream::kMaxRowBytes) return fp4::stream::launch(p, cus, s);
+    if (p.m > 0 && fp4::tile_ok(p) && fp4::tile_faster(p, cus)) return fp4::launch_tile(p, cus, s);
     return fp4::block::launch(p, cus, s);
 }
 
