@@ -229,3 +229,83 @@ def test_backward_of_a_layer_over_mxfp4_weights():
         torch.cuda.synchronize()
         ex, ew = backward()
         assert torch.equal(cx, ex) and torch.equal(cw, ew), seed
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n", [1, 7, 8, 9, 15, 511, 512, 513, 521, 1031])
+@pytest.mark.parametrize("top_k", [1, 2, 3, 5, 9])
+def test_widths_of_any_alignment(n, top_k, dtype):
+    """Rows that begin at any element, a last piece that overlaps the one before, every batch of copies: the
+    un-permute and both gradients, with every output behind an odd element."""
+    say("widths", n, top_k, dtype)
+    tokens = 37
+    r = np.random.default_rng(n + top_k)
+    s2c, c2s = routing(r, tokens, top_k, 5, 0.2)
+    c2s_d, s2c_d = dev(c2s), dev(s2c)
+    M = tokens * top_k
+
+    def odd(shape):
+        b = torch.full((int(np.prod(shape)) + 66,), float("nan"), dtype=dtype, device=DEV)
+        return b[33:33 + int(np.prod(shape))].view(shape), lambda: torch.isnan(torch.cat([b[:33], b[-33:]])).all()
+
+    y, _ = odd((M, n))
+    y.copy_(dev(r.standard_normal((M, n)).astype(np.float32)))
+    dout, _ = odd((tokens, n))
+    dout.copy_(dev(r.standard_normal((tokens, n)).astype(np.float32)))
+    w = dev(r.standard_normal((tokens, top_k)).astype(np.float32))
+    routed = (c2s >= 0)[:, None]
+    rows = np.where(routed, val(y)[np.maximum(c2s, 0)], 0.0).reshape(tokens, top_k, n)
+    step = 2.0 ** -8 if dtype == BF else 0.0
+
+    for weights, call in ((val(w), lambda o: B.moe_unpermute(y, c2s_d, w, out=o)), (np.ones((tokens, top_k)), lambda o: B.moe_permute_grad(y, c2s_d, top_k, out=o))):
+        out, ok = odd((tokens, n))
+        call(out)
+        want, mag = (rows * weights[..., None]).sum(1), (np.abs(rows * weights[..., None])).sum(1)
+        # top_k products and additions, each rounded once to fp32, and the result's own rounding
+        bound = (top_k + 1) * 2.0 ** -23 * mag
+        assert (np.abs(val(out) - want) <= bound + step * (np.abs(want) + bound)).all() and ok()
+
+    dy, ok = odd((M, n))
+    dw = torch.empty(tokens, top_k, device=DEV)
+    B.moe_unpermute_grad(dout, y, c2s_d, s2c_d, w, out=(dy, dw))
+    want = np.zeros((M, n))
+    at = np.nonzero(c2s >= 0)[0]
+    want[c2s[at]] = val(w).reshape(-1)[at, None] * val(dout)[at // top_k]
+    assert (np.abs(val(dy) - want) <= (2.0 ** -24 + step * 1.01) * np.abs(want)).all() and ok()
+    terms = rows * val(dout)[:, None]
+    assert (np.abs(val(dw) - terms.sum(-1)) <= (n / 64 + 34) * 2.0 ** -24 * np.abs(terms).sum(-1)).all()
+
+
+def test_gradients_past_32_bits():
+    """More than 2^32 elements: a few tokens far apart, their copies in the last rows."""
+    say("large rows")
+    tokens, top_k, n = 41003, 2, 57345
+    M = tokens * top_k
+    assert M * n > 2 ** 32
+    c2s = torch.arange(M - 1, -1, -1, dtype=torch.int32, device=DEV)   # copy i in row M - 1 - i
+    s2c = c2s.clone()
+    y = torch.zeros(M, n, dtype=BF, device=DEV)
+    some = torch.tensor([0, 1, tokens // 2, tokens - 2, tokens - 1], device=DEV)
+    for t in some.tolist():
+        y[M - 2 - 2 * t:M - 2 * t] = torch.randn(2, n, device=DEV).to(BF)
+    dout = torch.zeros(tokens, n, dtype=BF, device=DEV)
+    dout[some] = torch.randn(5, n, device=DEV).to(BF)
+    w = torch.rand(tokens, top_k, device=DEV)
+    dx = B.moe_permute_grad(y, c2s, top_k)
+    dy, dw = B.moe_unpermute_grad(dout, y, c2s, s2c, w)
+    for t in some.tolist():
+        a, b = y[M - 1 - 2 * t], y[M - 2 - 2 * t]   # copies 2 t and 2 t + 1
+        assert torch.equal(dx[t], (a.float() + b.float()).to(BF))
+        for j, row in ((0, M - 1 - 2 * t), (1, M - 2 - 2 * t)):
+            assert torch.equal(dy[row], (w[t, j] * dout[t].float()).to(BF))
+            p = dout[t].double() * y[row].double()
+            assert abs(dw[t, j].double() - p.sum()) <= (n / 64 + 34) * 2.0 ** -24 * p.abs().sum()
+    assert not dx[3].any() and not dy[5].any() and not dy[M - 9].any()
+
+
+def test_no_tokens():
+    say("no tokens")
+    i = torch.zeros(0, dtype=torch.int32, device=DEV)
+    assert B.moe_permute_grad(torch.zeros(0, 24, device=DEV), i, 3).shape == (0, 24)
+    dy, dw = B.moe_unpermute_grad(torch.zeros(0, 24, device=DEV), torch.zeros(0, 24, device=DEV), i, i, torch.zeros(0, 3, device=DEV))
+    assert dy.shape == (0, 24) and dw.shape == (0, 3)

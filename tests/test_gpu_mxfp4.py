@@ -396,3 +396,139 @@ def test_layer_on_another_stream_and_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(captured, step()), seed
+
+
+LONG = [
+    # some thousands of rows in long groups and wide enough for the 256 x 256 tiles: widths that whole stores divide and
+    # widths that they do not (a last piece of one to seven elements), k with and without a part panel, odd row counts
+    (1701, 544, 4997, [1000, 0, 640, 20], BF),
+    (1701, 544, 4997, [1000, 0, 640, 20], F32),
+    (1700, 800, 5000, [801, 799, 100], BF),
+    (1703, 608, 5004, [1, 1702], F32),
+    (1703, 1056, 5003, [1100, 602], F32),
+    (5000, 800, 4103, [1, 1024, 77, 1500, 0, 33, 300, 2000], BF),
+    (2304, 1312, 4098, [256, 512, 768, 700], BF),
+]
+
+
+@pytest.mark.parametrize("case", range(len(LONG)))
+def test_product_long_groups(case):
+    m, k, n, gs, out_dtype = LONG[case]
+    say("long groups", LONG[case])
+    check_product(*operands(np.random.default_rng(90 + case), m, k, n, len(gs)), gs, out_dtype)
+
+
+def test_product_long_groups_bad_sizes_and_nan_scales():
+    say("long groups: bad sizes, nan scales")
+    m, k, n = 1700, 800, 5000
+    lc, lp, rc, rp = operands(np.random.default_rng(100), m, k, n, 3, pad=255)
+    for gs, flags in (([900, -2, 700], B.DEV_NEGATIVE_SIZE), ([m, 7, m], B.DEV_SUM_EXCEEDS_M), ([0, 0, 0], 0)):
+        ws = torch.full((B.workspace_bytes("ragged_m", m, k, n, 3, 0, B.FP4),), 0xAB, dtype=torch.uint8, device=DEV)
+        check_product(lc, lp, rc, rp, gs, ws=ws)
+        assert B.read_device_status(ws) == flags
+    gs = [900, 0, 790]
+    lp[1, 3, 5] = 255        # row 3 (group 0)
+    rp[2, 3, 17, 0] = 255    # column 17 of group 2, in the part panel
+    out = host(B.ragged_dot_m_mxfp4(dev(lc), dev(rc), dev(np.asarray(gs, np.int32)), dev(lp), dev(rp)))
+    nan = np.zeros((m, n), bool)
+    nan[3] = True
+    nan[900:1690, 17] = True
+    assert np.array_equal(np.isnan(out), nan)
+
+
+@pytest.mark.parametrize("n", [1, 5, 115, 129, 1025])
+@pytest.mark.parametrize("out_dtype", [BF, F32])
+def test_product_narrow_and_ragged_widths(n, out_dtype):
+    """One column tile or a few, many row tiles of many groups; some tens of rows and several row tiles a group."""
+    say("narrow", n, out_dtype)
+    r = np.random.default_rng(n)
+    for g, most in ((40, 60), (5, 300), (3, 5)):
+        gs = r.integers(0, most, g)
+        m = int(gs.sum()) + 9
+        check_product(*operands(r, m, 352, n, g), gs, out_dtype)
+
+
+def test_empty_quantisation():
+    say("empty")
+    for rows, k in ((0, 64), (3, 0)):
+        c, s = B.mxfp4_quantize(torch.zeros(rows, k, device=DEV))
+        assert c.shape == (rows, k // 2) and s.shape == (-(-k // 256), rows, 8)
+        assert B.mxfp4_dequantize(c, s).shape == (rows, k)
+    for g, k, n in ((2, 0, 5), (2, 64, 0)):
+        c, s = B.mxfp4_quantize_weights(torch.zeros(g, k, n, device=DEV))
+        assert c.shape == (g, n, k // 2) and s.shape == (g, -(-k // 256), n, 8)
+        assert B.mxfp4_dequantize(c, s).shape == (g, n, k)
+
+
+@pytest.mark.parametrize("m,k,n,g", [(3, 2880, 1000001, 4), (3, 65536, 50000, 4), (40, 65536, 50000, 4), (1700, 65536, 50000, 4)])
+def test_product_of_weights_past_32_bits(m, k, n, g):
+    """The last group's codes begin past 4 GiB; eight rows and some columns against 64 bits."""
+    say("large weights", m, k, n, g)
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    w = torch.randint(0, 256, (g, n, k // 2), dtype=torch.uint8, device=DEV, generator=gen)
+    ws = torch.randint(116, 124, (g, -(-k // 256), n, 8), dtype=torch.uint8, device=DEV, generator=gen)
+    assert (g - 1) * n * (k // 2) > 2 ** 32
+    x = torch.randint(0, 256, (m, k // 2), dtype=torch.uint8, device=DEV, generator=gen)
+    xs = torch.randint(116, 124, (-(-k // 256), m, 8), dtype=torch.uint8, device=DEV, generator=gen)
+    if k % 256:
+        ws[:, -1, :, k % 256 // 32:] = 0
+        xs[-1, :, k % 256 // 32:] = 0
+    gs = torch.tensor([0] * (g - 1) + [m], dtype=torch.int32, device=DEV)
+    out = B.ragged_dot_m_mxfp4(x, w, gs, xs, ws, out_dtype=F32)
+    rows = torch.tensor(sorted({0, 1, 2, m // 2, m - 3, m - 2, m - 1}), device=DEV)
+    cols = torch.tensor([0, 1, 17, n // 2, n - 300, n - 2, n - 1], device=DEV)
+    a = oracle.mxfp4_values(host(x[rows]), host(xs[:, rows]))
+    b = oracle.mxfp4_values(host(w[-1, cols]), host(ws[-1][:, cols]))
+    want, mag = a @ b.T, np.abs(a) @ np.abs(b).T
+    assert (np.abs(host(out[rows][:, cols]) - want) <= (k / 8 + 32) * 2.0 ** -23 * mag).all()
+
+
+def test_quantisation_past_32_bits():
+    """More than 2^32 elements: the last rows are quantised and put back as they are alone."""
+    say("large rows")
+    rows, k = 70001, 65536
+    x = torch.empty(rows, k, dtype=BF, device=DEV)
+    x[:-3] = 0
+    tail = torch.randn(3, k, device=DEV).to(BF)
+    x[-3:] = tail
+    c, s = B.mxfp4_quantize(x)
+    c3, s3 = B.mxfp4_quantize(tail)
+    assert torch.equal(c[-3:].view(torch.uint8), c3.view(torch.uint8)) and torch.equal(s[:, -3:], s3)
+    assert not c[:-3].view(torch.uint8).any()
+    del x
+    assert torch.equal(B.mxfp4_dequantize(c, s)[-3:], B.mxfp4_dequantize(c3, s3))
+
+
+def test_two_streams_and_one_workspace():
+    """The workspace holds a status word only: calls on two streams may share it, and so may captured graphs."""
+    say("two streams, one workspace")
+    r = np.random.default_rng(20)
+    ws = torch.zeros(B.workspace_bytes("ragged_m", 600, 544, 700, 3, 0, B.FP4), dtype=torch.uint8, device=DEV)
+    calls, wants = [], []
+    for m, gs in ((600, [300, 0, 290]), (9, [3, 3, 3])):
+        lc, lp, rc, rp = (dev(a) for a in operands(r, m, 544, 700, 3))
+        sizes = dev(np.asarray(gs, np.int32))
+        calls.append(lambda lc=lc, lp=lp, rc=rc, rp=rp, sizes=sizes: B.ragged_dot_m_mxfp4(lc, rc, sizes, lp, rp, workspace=ws))
+        wants.append(calls[-1]())
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [[], []]
+    for _ in range(10):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                outs[i].append(calls[i]())
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(o, wants[i]) for o in outs[i])
+    graphs = []
+    for i in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=streams[i]):
+            o = calls[i]()
+        graphs.append((g, o))
+    for _ in range(3):
+        for (g, o), want in zip(graphs, wants):
+            o.zero_()
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(o, want) and torch.equal(calls[0](), wants[0])
