@@ -9,7 +9,9 @@
 // as NaN in both directions (checked on the GPU for every code at scale bytes 0-3, 100, 127, 128, 200 and
 // 252-255), so one conversion is exact to the definition and the scale is one shift.
 //
-// All three kernels move each byte once and compute little: they are bound by memory.
+// All three kernels move each byte once and compute little: they are bound by memory.  Measured: rows
+// [4096, 7168] bf16 12.5 us and back 11.6 us (5.9 and 6.4 TB/s, part of it out of the last-level cache), weights
+// [8, 4096, 14336] bf16 and back 448 us (5.3 TB/s).
 #include "common.hpp"
 #include "launch.hpp"
 
@@ -45,19 +47,18 @@ __device__ inline uint32_t encode8(const float (&v)[8], float scale) {
     return (uint32_t)q;
 }
 
-// Eight consecutive values of a row, and the exponent of their largest magnitude.  VEC: 16-byte loads.
+// 16 bytes of a row, which may begin at any element (the target's global memory takes that)
+typedef i32x4 __attribute__((aligned(2))) i32x4_any;
+typedef f32x4 __attribute__((aligned(4))) f32x4_any;
+
+// Eight consecutive values of a row, and the exponent of their largest magnitude.
 template <typename T> struct Eight;
 template <> struct Eight<uint16_t> {
     uint32_t v[4];
-    template <bool VEC> __device__ void load(const uint16_t* p) {
-        if constexpr (VEC) {
-            const i32x4 q = *(const i32x4*)p;
+    __device__ void load(const uint16_t* p) {
+        const i32x4 q = *(const i32x4_any*)p;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = (uint32_t)q[i];
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = (uint32_t)p[2 * i] | ((uint32_t)p[2 * i + 1] << 16);
-        }
+        for (int i = 0; i < 4; ++i) v[i] = (uint32_t)q[i];
     }
     __device__ void zero() { v[0] = v[1] = v[2] = v[3] = 0; }
     __device__ uint32_t top() const {   // magnitudes order as integers, NaN above infinity
@@ -69,15 +70,10 @@ template <> struct Eight<uint16_t> {
 };
 template <> struct Eight<float> {
     float v[8];
-    template <bool VEC> __device__ void load(const float* p) {
-        if constexpr (VEC) {
-            const f32x4 a = *(const f32x4*)p, b = *(const f32x4*)(p + 4);
+    __device__ void load(const float* p) {
+        const f32x4 a = *(const f32x4_any*)p, b = *(const f32x4_any*)(p + 4);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) { v[i] = a[i]; v[4 + i] = b[i]; }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = p[i];
-        }
+        for (int i = 0; i < 4; ++i) { v[i] = a[i]; v[4 + i] = b[i]; }
     }
     __device__ void zero() {
 #pragma unroll
@@ -94,7 +90,7 @@ template <> struct Eight<float> {
 // Rows.  A half wave holds one panel of one row, eight elements a lane, so a block is four lanes and its
 // maximum two lane exchanges.  A workgroup takes 8 U rows of one panel, so the panel's scale bytes of its
 // rows leave as one contiguous run and U loads a lane are in flight.
-template <typename T, bool VEC, int U>
+template <typename T, int U>
 __global__ __launch_bounds__(256) void quantize_rows(const T* __restrict__ x, int64_t rows, int64_t k, int64_t stride,
                                                      uint8_t* __restrict__ codes, uint8_t* __restrict__ scale, int panels) {
     const int t = threadIdx.x, c = t & 31, sub = t >> 5;
@@ -105,7 +101,7 @@ __global__ __launch_bounds__(256) void quantize_rows(const T* __restrict__ x, in
 #pragma unroll
     for (int u = 0; u < U; ++u) {
         const int64_t r = r0 + 8 * u;
-        if (r < rows && col < k) e[u].template load<VEC>(x + r * stride + col);
+        if (r < rows && col < k) e[u].load(x + r * stride + col);
         else e[u].zero();
     }
 #pragma unroll
@@ -131,40 +127,41 @@ __global__ __launch_bounds__(256) void quantize_rows(const T* __restrict__ x, in
 // rows of one block, so a column's maximum and its 32 codes need no exchange; a workgroup holds one panel
 // (8 blocks) of 32 threads' columns.  The codes turn in LDS and leave as the panel's 128 bytes of every
 // column, whole cache lines.
-template <typename T, bool VEC>
+template <typename T>
 __global__ __launch_bounds__(256) void quantize_weights(const T* __restrict__ w, int64_t k, int64_t n, int panels, int ntiles,
                                                         uint8_t* __restrict__ codes, uint8_t* __restrict__ scale) {
     constexpr int C = 16 / sizeof(T), COLS = 32 * C;
     __shared__ i32x4 turn[COLS * 8];
-    __shared__ uint8_t sbytes[COLS * 8];
+    __shared__ __attribute__((aligned(8))) uint8_t sbytes[COLS * 8];
     const int t = threadIdx.x, cg = t & 31, blk = t >> 5;
     const int nt = blockIdx.x % ntiles;
     const int p = (blockIdx.x / ntiles) % panels;
     const int64_t h = blockIdx.x / ntiles / panels;
-    const int64_t col0 = (int64_t)nt * COLS, col = col0 + C * cg;
+    // (a row's last 16 bytes may begin before their place: the columns that two threads hold come out the same)
+    const int64_t col0 = (int64_t)nt * COLS, col = n < C ? C * cg : min(col0 + C * cg, n - C);
     const int64_t k0 = (int64_t)p * kPanel + 32 * blk;
     const T* src = w + (h * k + k0) * n + col;
     uint32_t v[32][4];   // row i of the block: the thread's C columns
+    if (k0 < k && n >= C) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
+        for (int i = 0; i < 32; ++i) {
+            const i32x4 q = __builtin_nontemporal_load((const i32x4_any*)(src + (int64_t)i * n));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[i][j] = 0;
-        if (k0 < k) {
-            if constexpr (VEC) {
-                if (col < n) {
-                    const i32x4 q = __builtin_nontemporal_load((const i32x4*)(src + (int64_t)i * n));
+            for (int j = 0; j < 4; ++j) v[i][j] = (uint32_t)q[j];
+        }
+    } else {   // fewer columns than that, and blocks past k
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) v[i][j] = (uint32_t)q[j];
+        for (int i = 0; i < 32; ++i) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[i][j] = 0;
+            if (k0 >= k) continue;
+#pragma unroll
+            for (int j = 0; j < C; ++j)
+                if (col + j < n) {
+                    const T a = src[(int64_t)i * n + j];
+                    if constexpr (sizeof(T) == 2) v[i][j >> 1] |= (uint32_t)a << (16 * (j & 1));
+                    else v[i][j] = __float_as_uint((float)a);
                 }
-            } else {
-#pragma unroll
-                for (int j = 0; j < C; ++j)
-                    if (col + j < n) {
-                        const T a = src[(int64_t)i * n + j];
-                        if constexpr (sizeof(T) == 2) v[i][j >> 1] |= (uint32_t)a << (16 * (j & 1));
-                        else v[i][j] = __float_as_uint((float)a);
-                    }
-            }
         }
     }
 #pragma unroll
@@ -200,8 +197,9 @@ __global__ __launch_bounds__(256) void quantize_weights(const T* __restrict__ w,
                 q[d] = (int)encode8(x, s);
             }
         }
-        const int cl = C * cg + j;
-        turn[cl * 8 + (blk ^ (cg & 7))] = q;   // 16-byte chunk of the column, spread over the banks
+        const int cl = (int)(col - col0) + j;
+        if (cl < 0) continue;
+        turn[cl * 8 + (blk ^ ((cl / C) & 7))] = q;   // 16-byte chunk of the column, spread over the banks
         sbytes[cl * 8 + blk] = (uint8_t)(k0 < k ? b : 0);
     }
     __syncthreads();
@@ -218,7 +216,7 @@ __global__ __launch_bounds__(256) void quantize_weights(const T* __restrict__ w,
 }
 
 // Back to values, the geometry of quantize_rows: a lane turns one dword of codes into eight values.
-template <typename OutT, bool VEC, int U>
+template <typename OutT, int U>
 __global__ __launch_bounds__(256) void dequantize(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scale, int64_t n,
                                                   int64_t k, int panels, int rtiles, OutT* __restrict__ out) {
     const int t = threadIdx.x, c = t & 31, sub = t >> 5;
@@ -251,23 +249,12 @@ __global__ __launch_bounds__(256) void dequantize(const uint8_t* __restrict__ co
             v[1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q[u], s, 1));
             v[2] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q[u], s, 2));
             v[3] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q[u], s, 3));
-            if constexpr (VEC) {
-                *(i32x4*)o = v;
-            } else {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = (OutT)((uint32_t)v[i >> 1] >> (16 * (i & 1)));
-            }
+            *(i32x4_any*)o = v;
         } else {
             const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[u], s, 0), e = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[u], s, 1);
             const f32x2 f = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[u], s, 2), d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[u], s, 3);
-            if constexpr (VEC) {
-                *(f32x4*)o = f32x4{a[0], a[1], e[0], e[1]};
-                *(f32x4*)(o + 4) = f32x4{f[0], f[1], d[0], d[1]};
-            } else {
-                const float y[8] = {a[0], a[1], e[0], e[1], f[0], f[1], d[0], d[1]};
-#pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = y[i];
-            }
+            *(f32x4_any*)o = f32x4{a[0], a[1], e[0], e[1]};
+            *(f32x4_any*)(o + 4) = f32x4{f[0], f[1], d[0], d[1]};
         }
     }
 }
@@ -277,12 +264,10 @@ constexpr int64_t kMaxGrid = INT32_MAX;
 template <typename T>
 hipError_t quantize_t(const void* x, int64_t rows, int64_t k, int64_t stride, uint8_t* codes, uint8_t* scale, hipStream_t s) {
     const int panels = (int)((k + kPanel - 1) / kPanel);
-    const bool vec = (uintptr_t)x % 16 == 0 && (stride * (int64_t)sizeof(T)) % 16 == 0;
     constexpr int U = 4;
     const int64_t grid = (rows + 8 * U - 1) / (8 * U) * panels;
     if (grid > kMaxGrid) return hipErrorInvalidValue;
-    if (vec) hipLaunchKernelGGL((quantize_rows<T, true, U>), dim3((uint32_t)grid), dim3(256), 0, s, (const T*)x, rows, k, stride, codes, scale, panels);
-    else hipLaunchKernelGGL((quantize_rows<T, false, U>), dim3((uint32_t)grid), dim3(256), 0, s, (const T*)x, rows, k, stride, codes, scale, panels);
+    hipLaunchKernelGGL((quantize_rows<T, U>), dim3((uint32_t)grid), dim3(256), 0, s, (const T*)x, rows, k, stride, codes, scale, panels);
     return hipGetLastError();
 }
 
@@ -293,9 +278,7 @@ hipError_t quantize_weights_t(const void* w, int g, int64_t k, int64_t n, uint8_
     const int64_t ntiles = (n + COLS - 1) / COLS;
     const int64_t grid = ntiles * panels * g;
     if (grid > kMaxGrid) return hipErrorInvalidValue;
-    const bool vec = (uintptr_t)w % 16 == 0 && (n * (int64_t)sizeof(T)) % 16 == 0;
-    if (vec) hipLaunchKernelGGL((quantize_weights<T, true>), dim3((uint32_t)grid), dim3(256), 0, s, (const T*)w, k, n, panels, (int)ntiles, codes, scale);
-    else hipLaunchKernelGGL((quantize_weights<T, false>), dim3((uint32_t)grid), dim3(256), 0, s, (const T*)w, k, n, panels, (int)ntiles, codes, scale);
+    hipLaunchKernelGGL((quantize_weights<T>), dim3((uint32_t)grid), dim3(256), 0, s, (const T*)w, k, n, panels, (int)ntiles, codes, scale);
     return hipGetLastError();
 }
 
@@ -306,9 +289,7 @@ hipError_t dequantize_t(const uint8_t* codes, const uint8_t* scale, int g, int64
     const int64_t rtiles = (n + 8 * U - 1) / (8 * U);
     const int64_t grid = rtiles * panels * g;
     if (grid > kMaxGrid) return hipErrorInvalidValue;
-    // a row of out is k elements, k % 32 == 0: its rows are 16-byte aligned when out is
-    if ((uintptr_t)out % 16 == 0) hipLaunchKernelGGL((dequantize<OutT, true, U>), dim3((uint32_t)grid), dim3(256), 0, s, codes, scale, n, k, panels, (int)rtiles, (OutT*)out);
-    else hipLaunchKernelGGL((dequantize<OutT, false, U>), dim3((uint32_t)grid), dim3(256), 0, s, codes, scale, n, k, panels, (int)rtiles, (OutT*)out);
+    hipLaunchKernelGGL((dequantize<OutT, U>), dim3((uint32_t)grid), dim3(256), 0, s, codes, scale, n, k, panels, (int)rtiles, (OutT*)out);
     return hipGetLastError();
 }
 
