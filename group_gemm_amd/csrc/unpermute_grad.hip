@@ -18,7 +18,8 @@
 namespace gg {
 namespace upg {
 
-constexpr int KB = 8;   // copies handled at a time
+constexpr int KB = 8;       // copies handled at a time
+constexpr int CLEAR = 16;   // rows that a clearing wave looks over at a time (64: 22 us, not 12, where 46 of 183 rows of 1030 are lost)
 
 __device__ inline float up(uint32_t u) { return __uint_as_float(u); }
 
@@ -65,16 +66,21 @@ __global__ __launch_bounds__(256) void kernel(UnpermuteGradArgs a, int tok_block
     T* dy = (T*)a.dy;
     if ((int)blockIdx.x >= tok_blocks) {   // clear the rows that no copy claims
         const int nw = ((int)gridDim.x - tok_blocks) * 4;
-        for (int p0 = (((int)blockIdx.x - tok_blocks) * 4 + wv) * 64; p0 < M; p0 += nw * 64) {
-            const int p = p0 + l;
+        for (int64_t p0 = (int64_t)(((int)blockIdx.x - tok_blocks) * 4 + wv) * CLEAR; p0 < M; p0 += (int64_t)nw * CLEAR) {
+            const int64_t p = p0 + l;
             bool lost = false;
-            if (p < M) {
+            if (l < CLEAR && p < M) {
                 const int i = a.sorted_to_copy[p];
                 lost = i < 0 || i >= M || a.copy_to_sorted[i] != p;
             }
             for (uint64_t rows = __ballot(lost); rows; rows &= rows - 1) {
                 T* o = dy + (size_t)(p0 + __ffsll((unsigned long long)rows) - 1) * n;
-                for (int c = l; c < n; c += 64) st1(o + c, 0.f);
+                if constexpr (VEC) {
+                    const float zero[8] = {};
+                    for (int c = 8 * l; c < n; c += 512) store8(o + min(c, n - 8), zero);
+                } else {
+                    for (int c = l; c < n; c += 64) st1(o + c, 0.f);
+                }
             }
         }
         return;
@@ -172,7 +178,7 @@ template <typename T, int WPT>
 void launch_w(const UnpermuteGradArgs& a, hipStream_t s) {
     const int tpb = 4 / WPT, tok_blocks = (a.tokens + tpb - 1) / tpb;
     const int64_t M = (int64_t)a.tokens * a.top_k;
-    const int clear = (int)((M + 255) / 256 < 256 ? (M + 255) / 256 : 256);
+    const int clear = (int)((M + 4 * CLEAR - 1) / (4 * CLEAR) < 512 ? (M + 4 * CLEAR - 1) / (4 * CLEAR) : 512);
     if (a.n >= 8) hipLaunchKernelGGL((kernel<T, true, WPT>), dim3(tok_blocks + clear), dim3(256), 0, s, a, tok_blocks);
     else hipLaunchKernelGGL((kernel<T, false, WPT>), dim3(tok_blocks + clear), dim3(256), 0, s, a, tok_blocks);
 }

@@ -186,9 +186,11 @@ gg_status mxfp4_dequantize(const uint8_t* codes, const uint8_t* scale, void* out
  *   out[r, :] = lhs[r, :] . rhs[h]^T   for every row r of group h;   rows r >= sum(sizes) = 0.
  *   lhs [m, k/2], lhs_scale [ceil(k/256), m, 8]; rhs [g, n, k/2], rhs_scale [g, ceil(k/256), n, 8]
  *   out [m, n]  bf16 or fp32; every element written
- * k % 32 == 0 (GG_ERR_UNSUPPORTED otherwise); any m and n.  Few rows per group (single tokens,
- * decoding batches) and many (prompts) take different kernels.  Workspace, status and errors as
- * ragged_dot_m: gg_workspace_bytes(GG_OP_RAGGED_M, m, k, n, g, 0, GG_DT_E2M1). */
+ * k % 32 == 0 (GG_ERR_UNSUPPORTED otherwise) and k < 2^25; any m and n.  Few rows per group (single
+ * tokens, decoding batches), some tens and many (prompts) take different kernels, which add in
+ * different orders; one kernel's result does not depend on the launch.  Workspace, status and
+ * errors as ragged_dot_m: gg_workspace_bytes(GG_OP_RAGGED_M, m, k, n, g, 0, GG_DT_E2M1); the
+ * workspace holds the status word only, so calls on several streams may share it. */
 gg_status ragged_dot_m_mxfp4(const void* lhs, const void* rhs, const int32_t* group_sizes, void* out,
                              int64_t m, int64_t k, int64_t n, int32_t g, gg_dtype out_dtype,
                              const uint8_t* lhs_scale, const uint8_t* rhs_scale, void* workspace,
