@@ -430,7 +430,7 @@ constexpr int BM = 256, BN = 256, NT = 256, MI = 4, NJ = 4, SUB = 4;   // SUB: i
 constexpr int OPER = 256 * kRowBytes;     // one operand's slot
 constexpr int SC = 256 * 8;               // one operand's scales of a panel
 constexpr int ROT = 2;                    // panels between the starts of neighbouring column tiles
-constexpr int LOADS = 17;                 // a wave's loads of a panel: 8 + 8 of eight rows, 1 KiB of scales
+constexpr int LOADS = 17;                 // a wave's loads of a panel: 1 KiB of scales, 8 + 8 of eight rows
 constexpr int READ = 15;                  // MFMA of a panel after which the next panel's reads begin
 constexpr int load_step(int d) { return d * 31 / LOADS; }   // MFMA after which load d goes out
 constexpr int loads_before(int step) {
@@ -516,8 +516,10 @@ __global__ __launch_bounds__(NT, 1) void kernel(Fp4Params p) {
         return i;
     };
 
-    // Load number d of the stream's panel lp: d < 8 rows 64 wave + 8 d .. + 7, d < 16 the same of the weights,
-    // then the scales.  Lane l brings row l / 8 of the eight, chunk (l % 8) ^ swizzle(row); the swizzle of row
+    // Load number d of the stream's panel lp: the scales, then (counting on from 0) d < 8 rows 64 wave + 8 d .. + 7,
+    // d < 16 the same of the weights.  The scales come first, before a panel's instructions: their load is behind a
+    // branch, and the compiler moves what instructions it can past a branch, away from the loads that they were
+    // to be spread among.  Lane l brings row l / 8 of the eight, chunk (l % 8) ^ swizzle(row); the swizzle of row
     // 64 wave + 8 d + l / 8 is (4 d + l / 16) % 8.  v: lane offsets for even and odd d; in a last panel that k
     // does not fill, the chunks past k are out of range and read as zeros.
     const int lc = (l & 7) ^ (l >> 4);
@@ -528,8 +530,8 @@ __global__ __launch_bounds__(NT, 1) void kernel(Fp4Params p) {
     const uint32_t srows = (uint32_t)(wave < 2 ? p.m : p.n) * 8u;
     uint32_t lslot = 0, past = 0;   // past: set once the stream has no more tiles, its loads then read nothing
     auto issue = [&](auto d_c, int lp) {
-        constexpr int d = decltype(d_c)::value;
-        if constexpr (d < 16) {
+        constexpr int d = decltype(d_c)::value - 1;
+        if constexpr (d >= 0) {
             const bool last = lp == panels - 1;
             const uint32_t v = d & 1 ? (last ? vt1 : v1) : (last ? vt0 : v0);
             const uint32_t s = (uint32_t)(64 * wave + 8 * (d & 7)) * (uint32_t)rb + (uint32_t)lp * kRowBytes + past;
@@ -629,6 +631,8 @@ __global__ __launch_bounds__(NT, 1) void kernel(Fp4Params p) {
             // lp: the panel to load.
             auto panel = [&](auto first_c, int follow, int lp) {
                 constexpr bool FIRST = decltype(first_c)::value;
+                if constexpr (!FIRST) issue(std::integral_constant<int, 0>{}, lp);
+                __builtin_amdgcn_sched_barrier(0);
                 static_for<0, SUB>([&](auto s_c) {
                     constexpr int S = decltype(s_c)::value;
                     static_for<0, 16>([&](auto m_c) {
@@ -645,7 +649,7 @@ __global__ __launch_bounds__(NT, 1) void kernel(Fp4Params p) {
                         constexpr int G = 16 * S + M;
                         // the loads, spread over the first half (a load takes a compute unit's address path 16
                         // clocks, so the four waves' go out no faster than one each in 64)
-                        if constexpr (!FIRST) static_for<0, LOADS>([&](auto d_c) { if constexpr (load_step(decltype(d_c)::value) == G) issue(d_c, lp); });
+                        if constexpr (!FIRST) static_for<1, LOADS>([&](auto d_c) { if constexpr (load_step(decltype(d_c)::value) == G) issue(d_c, lp); });
                         // the next panel's reads, spread over the rest: its loads have had a panel and a quarter to
                         // arrive, and are older than those just begun
                         if constexpr (G == READ) {
@@ -711,8 +715,7 @@ __global__ __launch_bounds__(NT, 1) void kernel(Fp4Params p) {
         // The slot that has just been emptied takes the panel after the next: its rows and scales at once, its
         // weights once the results have passed through their place (8 KiB a wave, the part that its own loads fill).
         const int lp2 = around(next.turn0 + 2);
-        issue_some(std::integral_constant<int, 0>{}, std::integral_constant<int, 8>{}, lp2);
-        issue_some(std::integral_constant<int, 16>{}, std::integral_constant<int, LOADS>{}, lp2);
+        issue_some(std::integral_constant<int, 0>{}, std::integral_constant<int, 9>{}, lp2);
         // Results: element 4 q + u of block (i, j) is row 32 i + l % 32, column 32 j + 8 q + 4 h + u.  They turn in
         // LDS, 256 bytes of 32 rows at a time (16-byte pieces XORed by the row), and leave as whole lines.
         uint8_t* const strip = &sm.b[0][0] + lslot * OPER + (uint32_t)wave * 8192u;
@@ -762,7 +765,7 @@ __global__ __launch_bounds__(NT, 1) void kernel(Fp4Params p) {
         });
         __builtin_amdgcn_s_waitcnt(0xc07f);   // the strip has been read (lgkmcnt(0))
         __builtin_amdgcn_sched_barrier(0);
-        issue_some(std::integral_constant<int, 8>{}, std::integral_constant<int, 16>{}, lp2);
+        issue_some(std::integral_constant<int, 9>{}, std::integral_constant<int, LOADS>{}, lp2);
         lslot ^= 1;
         stored = WHOLE && NB == MI;
         });
