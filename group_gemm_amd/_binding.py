@@ -494,6 +494,10 @@ def moe_unpermute_grad(dout, y, copy_to_sorted, sorted_to_copy, weights, out=Non
         dy = torch.empty_like(y)
     else:
         _tensor(dy, "dy", dev, (M, n), y.dtype)
+        span = dy.numel() * dy.element_size()
+        for t, name in ((y, "y"), (dout, "dout")):
+            if dy.data_ptr() < t.data_ptr() + t.numel() * t.element_size() and t.data_ptr() < dy.data_ptr() + span:
+                raise ValueError(f"dy overlaps {name}")
     if dweights is None:
         dweights = torch.empty((tokens, top_k), dtype=torch.float32, device=dev)
     else:

@@ -341,8 +341,8 @@ __global__ __launch_bounds__(256) void combine(const InT* __restrict__ y, int ro
         fetch(0, first);
         // (a row's last eight elements may overlap the eight before and are then written twice, the same)
         auto columns = [&](auto k_c) {
-            for (int c1 = 512 * h + 8 * l; c1 < n; c1 += WPR * 512) {
-                const int c0 = min(c1, n - 8);
+            for (uint32_t c1 = 512 * h + 8 * l; c1 < (uint32_t)n; c1 += WPR * 512) {   // (may pass 2^31)
+                const int c0 = min((int)c1, n - 8);
                 float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
                 accumulate(k_c, first, c0, acc);
                 for (int j0 = 8; j0 < top_k; j0 += 8) {

@@ -77,7 +77,7 @@ __global__ __launch_bounds__(256) void kernel(UnpermuteGradArgs a, int tok_block
                 T* o = dy + (size_t)(p0 + __ffsll((unsigned long long)rows) - 1) * n;
                 if constexpr (VEC) {
                     const float zero[8] = {};
-                    for (int c = 8 * l; c < n; c += 512) store8(o + min(c, n - 8), zero);
+                    for (uint32_t c = 8 * l; c < (uint32_t)n; c += 512) store8(o + min((int)c, n - 8), zero);
                 } else {
                     for (int c = l; c < n; c += 64) st1(o + c, 0.f);
                 }
@@ -113,8 +113,8 @@ __global__ __launch_bounds__(256) void kernel(UnpermuteGradArgs a, int tok_block
                 // and their products are left out of the second sum)
                 auto columns = [&](auto k_c) {
                     constexpr int K = decltype(k_c)::value;   // copies whose rows are read: absent ones among them read row 0
-                    for (int c0 = 512 * h + 8 * l; c0 < n; c0 += 512 * WPT) {
-                        const int c = min(c0, n - 8), done = c0 - c;
+                    for (uint32_t c0 = 512 * h + 8 * l; c0 < (uint32_t)n; c0 += 512 * WPT) {   // (may pass 2^31)
+                        const int c = min((int)c0, n - 8), done = (int)c0 - c;
                         float d[8];
                         load8(drow + c, d);
                         float y[K][8];

@@ -338,7 +338,8 @@ gg_status moe_permute_grad(const void* dsorted, const int32_t* copy_to_sorted, v
  *   dweights       [tokens, top_k]      fp32: dweights[i] = dout[i / top_k, :] . y[copy_to_sorted[i], :],
  *     summed in fp32 in an order that depends on n alone; 0 where the entry is outside
  *     [0, tokens * top_k)
- * Every element of dy and dweights is written; no atomics.  No workspace. */
+ * Every element of dy and dweights is written; no atomics.  No workspace.  dy may not overlap y or dout
+ * (not checked here). */
 gg_status moe_unpermute_grad(const void* dout, const void* y, const int32_t* copy_to_sorted,
                              const int32_t* sorted_to_copy, const float* weights, void* dy,
                              float* dweights, int64_t tokens, int32_t top_k, int64_t n, gg_dtype dtype,

@@ -303,6 +303,16 @@ def test_gradients_past_32_bits():
     assert not dx[3].any() and not dy[5].any() and not dy[M - 9].any()
 
 
+def test_gradients_in_place_are_refused():
+    say("in place")
+    b = torch.zeros(20, 16, device=DEV)
+    y, dout, i, w = b[:12], torch.zeros(6, 16, device=DEV), torch.arange(12, dtype=torch.int32, device=DEV), torch.ones(6, 2, device=DEV)
+    for dy in (y, b[8:20]):
+        with pytest.raises(ValueError):
+            B.moe_unpermute_grad(dout, y, i, i, w, out=(dy, None))
+    B.moe_unpermute_grad(dout, y, i, i, w, out=(torch.empty_like(y), None))
+
+
 def test_no_tokens():
     say("no tokens")
     i = torch.zeros(0, dtype=torch.int32, device=DEV)
