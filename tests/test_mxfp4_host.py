@@ -71,6 +71,12 @@ def test_product():
     assert product(wsb=16) == WS_SMALL
 
 
+def test_product_offsets_stay_in_32_bits():
+    # 128 rows of codes have to stay below 2^31 bytes, column indices past n in 32 bits
+    assert product(k=1 << 25) == product(k=(1 << 30)) == BAD_SHAPE
+    assert product(m=1, n=(1 << 31) - 200) == BAD_SHAPE
+
+
 def test_workspace_bytes():
     assert B.workspace_bytes("ragged_m", 8, 64, 16, 2, 0, B.FP4) > 0
     assert B.workspace_bytes("permute", 8, 64, 0, 2, 0, B.FP4) > 0
