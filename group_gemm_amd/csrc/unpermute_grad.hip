@@ -151,9 +151,11 @@ __global__ __launch_bounds__(256) void kernel(UnpermuteGradArgs a, int tok_block
             }
         }
 #pragma unroll
-        for (int j = 0; j < KB; ++j)
+        for (int j = 0; j < KB; ++j) {
+            if (pos[j] < 0) acc[j] = 0.f;   // (its terms were dout times 0, and dout need not be finite)
 #pragma unroll
             for (int s = 32; s > 0; s >>= 1) acc[j] += __shfl_xor(acc[j], s, 64);
+        }
         if constexpr (WPT > 1) {
             __syncthreads();
             if (l == 0)
