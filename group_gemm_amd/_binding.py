@@ -178,6 +178,14 @@ def _out(out, name, device, shape, out_dtype):
     return torch.empty(shape, dtype=out_dtype, device=device)
 
 
+def _apart(out, name, **inputs):
+    """Refuse an output that shares memory with an input that the call still reads."""
+    a, end = out.data_ptr(), out.data_ptr() + out.numel() * out.element_size()
+    for tname, t in inputs.items():
+        if t.numel() and a < t.data_ptr() + t.numel() * t.element_size() and t.data_ptr() < end:
+            raise ValueError(f"{name} overlaps {tname}")
+
+
 def _bias(b, name, g, n, device):
     if b is None:
         return 0
@@ -457,7 +465,8 @@ def moe_unpermute(y, copy_to_sorted, weights, out=None, out_dtype=None):
 def moe_permute_grad(dsorted, copy_to_sorted, top_k, out=None, out_dtype=None):
     """The gradient of moe_permute with respect to x: dx[t, :] = sum_j
     dsorted[copy_to_sorted[t * top_k + j], :] for dsorted [tokens * top_k, k] (fp32 or bf16);
-    copies that were not routed add nothing.  out_dtype defaults to dsorted's."""
+    copies that were not routed add nothing.  out_dtype defaults to dsorted's; out may not overlap
+    dsorted."""
     dev = dsorted.device
     _tensor(dsorted, "dsorted", None, dtypes=_FLOATS)
     if dsorted.dim() != 2 or top_k < 1 or dsorted.shape[0] % top_k:
@@ -466,7 +475,10 @@ def moe_permute_grad(dsorted, copy_to_sorted, top_k, out=None, out_dtype=None):
     _tensor(copy_to_sorted, "copy_to_sorted", dev, (M,), torch.int32)
     if out_dtype is None:
         out_dtype = out.dtype if out is not None else dsorted.dtype
+    given = out is not None
     out = _out(out, "out", dev, (M // top_k, k), out_dtype)
+    if given:
+        _apart(out, "out", dsorted=dsorted, copy_to_sorted=copy_to_sorted)
     _call("moe_permute_grad", dev, dsorted.data_ptr(), copy_to_sorted.data_ptr(), out.data_ptr(), M // top_k, top_k, k,
           GG_DT[dsorted.dtype], GG_DT[out.dtype])
     return out
@@ -476,7 +488,8 @@ def moe_unpermute_grad(dout, y, copy_to_sorted, sorted_to_copy, weights, out=Non
     """The gradients of moe_unpermute(y, copy_to_sorted, weights): for dout [tokens, n] and y
     [tokens * top_k, n] of one type (fp32 or bf16) and the index arrays of moe_permute, returns
     (dy like y, dweights fp32 [tokens, top_k]).  Rows of dy that no copy was sorted to are 0.
-    `out` may supply the pair of outputs (an entry None is allocated)."""
+    `out` may supply the pair of outputs (an entry None is allocated); they may not overlap an input,
+    but dweights may be `weights` itself."""
     dev = y.device
     _tensor(y, "y", None, dtypes=_FLOATS)
     if y.dim() != 2 or weights.dim() != 2:
@@ -494,14 +507,14 @@ def moe_unpermute_grad(dout, y, copy_to_sorted, sorted_to_copy, weights, out=Non
         dy = torch.empty_like(y)
     else:
         _tensor(dy, "dy", dev, (M, n), y.dtype)
-        span = dy.numel() * dy.element_size()
-        for t, name in ((y, "y"), (dout, "dout")):
-            if dy.data_ptr() < t.data_ptr() + t.numel() * t.element_size() and t.data_ptr() < dy.data_ptr() + span:
-                raise ValueError(f"dy overlaps {name}")
+        _apart(dy, "dy", y=y, dout=dout, weights=weights, copy_to_sorted=copy_to_sorted, sorted_to_copy=sorted_to_copy)
     if dweights is None:
         dweights = torch.empty((tokens, top_k), dtype=torch.float32, device=dev)
     else:
         _tensor(dweights, "dweights", dev, (tokens, top_k), torch.float32)
+        _apart(dweights, "dweights", y=y, dout=dout, dy=dy, copy_to_sorted=copy_to_sorted, sorted_to_copy=sorted_to_copy)
+        if dweights.data_ptr() != weights.data_ptr():
+            _apart(dweights, "dweights", weights=weights)
     _call("moe_unpermute_grad", dev, dout.data_ptr(), y.data_ptr(), copy_to_sorted.data_ptr(), sorted_to_copy.data_ptr(),
           weights.data_ptr(), dy.data_ptr(), dweights.data_ptr(), tokens, top_k, n, GG_DT[y.dtype])
     return dy, dweights

@@ -31,6 +31,12 @@ bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// whether two arrays share a byte (sizes are at most 2^63 and addresses below 2^48: no sum wraps)
+bool overlap(const void* a, uint64_t an, const void* b, uint64_t bn) {
+    const uint64_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
+    return an > 0 && bn > 0 && a0 < b0 + bn && b0 < a0 + an;
+}
+
 // Compute units of the current device, cached per device.
 int device_cus(int* cus) {
     static int cache[64] = {0};
@@ -498,6 +504,9 @@ gg_status moe_permute_grad(const void* dsorted, const int32_t* copy_to_sorted, v
     if (tokens * k > 0 && (!copy_to_sorted || !dsorted || !dx)) return GG_ERR_NULL_PTR;
     if (!aligned(dsorted, elem_bytes(in_dtype)) || !aligned(dx, elem_bytes(out_dtype)) || !aligned(copy_to_sorted, 4))
         return GG_ERR_MISALIGNED;
+    const uint64_t copies = (uint64_t)tokens * top_k, dx_bytes = (uint64_t)tokens * k * elem_bytes(out_dtype);
+    if (overlap(dx, dx_bytes, dsorted, copies * k * elem_bytes(in_dtype)) || overlap(dx, dx_bytes, copy_to_sorted, copies * 4))
+        return GG_ERR_UNSUPPORTED;
     return gg::launch_combine(dsorted, in_dtype == GG_DT_BF16, (int)(tokens * top_k), copy_to_sorted, nullptr, (int)tokens,
                               top_k, (int)k, dx, out_dtype == GG_DT_BF16, (hipStream_t)stream) == hipSuccess
                ? GG_OK
@@ -516,6 +525,14 @@ gg_status moe_unpermute_grad(const void* dout, const void* y, const int32_t* cop
     if (!aligned(dout, es) || !aligned(y, es) || !aligned(dy, es) || !aligned(copy_to_sorted, 4) ||
         !aligned(sorted_to_copy, 4) || !aligned(weights, 4) || !aligned(dweights, 4))
         return GG_ERR_MISALIGNED;
+    const uint64_t copies = (uint64_t)tokens * top_k, dout_bytes = (uint64_t)tokens * n * es, rows_bytes = copies * n * es;
+    auto on_inputs = [&](const void* p, uint64_t bytes) {
+        return overlap(p, bytes, dout, dout_bytes) || overlap(p, bytes, y, rows_bytes) ||
+               overlap(p, bytes, copy_to_sorted, copies * 4) || overlap(p, bytes, sorted_to_copy, copies * 4);
+    };
+    if (on_inputs(dy, rows_bytes) || overlap(dy, rows_bytes, weights, copies * 4) || overlap(dy, rows_bytes, dweights, copies * 4) ||
+        on_inputs(dweights, copies * 4) || (dweights != weights && overlap(dweights, copies * 4, weights, copies * 4)))
+        return GG_ERR_UNSUPPORTED;
     gg::UnpermuteGradArgs a{};
     a.dout = dout; a.y = y; a.copy_to_sorted = copy_to_sorted; a.sorted_to_copy = sorted_to_copy; a.weights = weights;
     a.dy = dy; a.dweights = dweights; a.tokens = (int)tokens; a.top_k = top_k; a.n = (int)n;

@@ -323,7 +323,8 @@ gg_status moe_unpermute(const void* y, const int32_t* copy_to_sorted, const floa
  *                                       [0, tokens * top_k) (-1: not routed) adds nothing
  *   dx             [tokens, k]          out_dtype (fp32 or bf16):
  *     dx[t, :] = sum_j dsorted[copy_to_sorted[t * top_k + j], :]
- * fp32 accumulation in j order, one rounding; every element of dx is written.  No workspace. */
+ * fp32 accumulation in j order, one rounding; every element of dx is written.  No workspace.  dx may not
+ * lie in dsorted or copy_to_sorted (GG_ERR_UNSUPPORTED): other rows' copies are still read there. */
 gg_status moe_permute_grad(const void* dsorted, const int32_t* copy_to_sorted, void* dx, int64_t tokens,
                            int32_t top_k, int64_t k, gg_dtype in_dtype, gg_dtype out_dtype, void* stream);
 
@@ -338,8 +339,8 @@ gg_status moe_permute_grad(const void* dsorted, const int32_t* copy_to_sorted, v
  *   dweights       [tokens, top_k]      fp32: dweights[i] = dout[i / top_k, :] . y[copy_to_sorted[i], :],
  *     summed in fp32 in an order that depends on n alone; 0 where the entry is outside
  *     [0, tokens * top_k)
- * Every element of dy and dweights is written; no atomics.  No workspace.  dy may not overlap y or dout
- * (not checked here). */
+ * Every element of dy and dweights is written; no atomics.  No workspace.  dy and dweights may not lie in
+ * an input or in each other (GG_ERR_UNSUPPORTED), but dweights may be the array of weights itself. */
 gg_status moe_unpermute_grad(const void* dout, const void* y, const int32_t* copy_to_sorted,
                              const int32_t* sorted_to_copy, const float* weights, void* dy,
                              float* dweights, int64_t tokens, int32_t top_k, int64_t n, gg_dtype dtype,

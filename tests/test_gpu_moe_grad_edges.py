@@ -58,3 +58,42 @@ def test_nonfinite_dout_of_tokens_with_unrouted_copies(n, top_k, dtype):
     assert not got[absent].any(), "a copy without a sorted row has a weight gradient"
     assert same(got, want_w)
     assert same(dy.double().cpu().numpy(), want_y)   # products of whole numbers of at most 4 bits: exact in bf16
+
+
+def test_outputs_in_an_input_are_refused():
+    """Only where rows are still read is the call refused: beside an input, and weights' own array, stay allowed."""
+    say("in place")
+    tokens, top_k, n = 6, 2, 16
+    M = tokens * top_k
+    buf = torch.arange(2 * M * n, device=DEV, dtype=F32).view(2 * M, n)
+    d = buf[:M]
+    i = torch.arange(M, dtype=torch.int32, device=DEV)
+    w = torch.rand(tokens, top_k, device=DEV)
+    before = buf.clone()
+    for out in (d[:tokens], d[tokens:], buf[M - 1:M + 5]):
+        with pytest.raises(ValueError, match="overlaps dsorted"):
+            B.moe_permute_grad(d, i, top_k, out=out)
+    with pytest.raises(ValueError, match="dweights overlaps y"):
+        B.moe_unpermute_grad(d[:tokens].clone(), d, i, i, w, out=(None, d.view(-1)[:M].view(tokens, top_k)))
+    wide = torch.rand(M + 1, device=DEV)
+    with pytest.raises(ValueError, match="dweights overlaps weights"):
+        B.moe_unpermute_grad(d[:tokens].clone(), d, i, i, wide[:M].view(tokens, top_k), out=(None, wide[1:].view(tokens, top_k)))
+    assert torch.equal(buf, before)
+    want = B.moe_permute_grad(d, i, top_k)
+    assert torch.equal(B.moe_permute_grad(d, i, top_k, out=buf[M:M + tokens]), want) and torch.equal(d, before[:M])
+
+
+@pytest.mark.parametrize("top_k", [2, 19])
+@pytest.mark.parametrize("n", [24, 1030])
+def test_weight_gradients_into_the_weights(n, top_k):
+    say("dweights over weights", n, top_k)
+    tokens = 21
+    r = np.random.default_rng(n + top_k)
+    e = r.integers(-1, 5, (tokens, top_k))
+    _, _, _, s2c, c2s = oracle.moe_permute(np.zeros((tokens, 1), np.float32), e, 5)
+    dout, y = (dev(r.standard_normal((m, n)).astype(np.float32)) for m in (tokens, tokens * top_k))
+    w = dev(r.random((tokens, top_k)).astype(np.float32))
+    want = B.moe_unpermute_grad(dout, y, dev(c2s), dev(s2c), w)
+    got = B.moe_unpermute_grad(dout, y, dev(c2s), dev(s2c), w, out=(None, w))
+    assert got[1].data_ptr() == w.data_ptr()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
