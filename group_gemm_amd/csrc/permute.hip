@@ -339,7 +339,8 @@ __global__ __launch_bounds__(256) void combine(const InT* __restrict__ y, int ro
         };
         Eight first;
         fetch(0, first);
-        // (a row's last eight elements may overlap the eight before and are then written twice, the same)
+        // (a row's last eight elements may overlap the eight before; each is stored by one lane alone, as where
+        // out is y itself, one copy a token and every row in its place, the other lane may read it already weighted)
         auto columns = [&](auto k_c) {
             for (uint32_t c1 = 512 * h + 8 * l; c1 < (uint32_t)n; c1 += WPR * 512) {   // (may pass 2^31)
                 const int c0 = min((int)c1, n - 8);
@@ -350,7 +351,13 @@ __global__ __launch_bounds__(256) void combine(const InT* __restrict__ y, int ro
                     fetch(j0, more);
                     accumulate(std::integral_constant<int, 8>{}, more, c0, acc);
                 }
-                store8(orow + c0, acc);
+                if ((int)c1 == c0) {
+                    store8(orow + c0, acc);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (c0 + e >= (int)c1) st1(orow + c0 + e, acc[e]);
+                }
             }
         };
         if (top_k > 4) columns(std::integral_constant<int, 8>{});
