@@ -59,6 +59,11 @@ int persistent_grid(int64_t tile_bound, int per_cu, int cus) {
     return (int)g;
 }
 
+// Launchers return hipErrorInvalidConfiguration for more workgroups than a launch holds.
+gg_status launched(hipError_t e) {
+    return e == hipSuccess ? GG_OK : e == hipErrorInvalidConfiguration ? GG_ERR_BAD_SHAPE : GG_ERR_HIP;
+}
+
 bool fits_i32(int64_t x) { return x >= 0 && x <= INT32_MAX; }
 
 // Shape and group-size checks shared by every entry point.
@@ -475,7 +480,7 @@ gg_status moe_permute(const void* x, const uint8_t* x_scale, const int32_t* expe
     a.row_bytes = fp4 ? k / 2 : k * (int64_t)es;
     a.scale_row_bytes = mx && !fp4 ? k / 32 : 0;
     a.scale_panels = fp4 ? (int)cdiv64(k, 256) : 0;
-    return gg::launch_permute(a, (hipStream_t)stream) == hipSuccess ? GG_OK : GG_ERR_HIP;
+    return launched(gg::launch_permute(a, (hipStream_t)stream));
 }
 
 gg_status moe_unpermute(const void* y, const int32_t* copy_to_sorted, const float* weights, void* out, int64_t tokens,
@@ -489,10 +494,8 @@ gg_status moe_unpermute(const void* y, const int32_t* copy_to_sorted, const floa
     if (!aligned(y, elem_bytes(in_dtype)) || !aligned(out, elem_bytes(out_dtype)) || !aligned(copy_to_sorted, 4) ||
         !aligned(weights, 4))
         return GG_ERR_MISALIGNED;
-    return gg::launch_combine(y, in_dtype == GG_DT_BF16, (int)(tokens * top_k), copy_to_sorted, weights, (int)tokens,
-                              top_k, (int)n, out, out_dtype == GG_DT_BF16, (hipStream_t)stream) == hipSuccess
-               ? GG_OK
-               : GG_ERR_HIP;
+    return launched(gg::launch_combine(y, in_dtype == GG_DT_BF16, (int)(tokens * top_k), copy_to_sorted, weights, (int)tokens,
+                              top_k, (int)n, out, out_dtype == GG_DT_BF16, (hipStream_t)stream));
 }
 
 gg_status moe_permute_grad(const void* dsorted, const int32_t* copy_to_sorted, void* dx, int64_t tokens, int32_t top_k,
@@ -507,10 +510,8 @@ gg_status moe_permute_grad(const void* dsorted, const int32_t* copy_to_sorted, v
     const uint64_t copies = (uint64_t)tokens * top_k, dx_bytes = (uint64_t)tokens * k * elem_bytes(out_dtype);
     if (overlap(dx, dx_bytes, dsorted, copies * k * elem_bytes(in_dtype)) || overlap(dx, dx_bytes, copy_to_sorted, copies * 4))
         return GG_ERR_UNSUPPORTED;
-    return gg::launch_combine(dsorted, in_dtype == GG_DT_BF16, (int)(tokens * top_k), copy_to_sorted, nullptr, (int)tokens,
-                              top_k, (int)k, dx, out_dtype == GG_DT_BF16, (hipStream_t)stream) == hipSuccess
-               ? GG_OK
-               : GG_ERR_HIP;
+    return launched(gg::launch_combine(dsorted, in_dtype == GG_DT_BF16, (int)(tokens * top_k), copy_to_sorted, nullptr, (int)tokens,
+                              top_k, (int)k, dx, out_dtype == GG_DT_BF16, (hipStream_t)stream));
 }
 
 gg_status moe_unpermute_grad(const void* dout, const void* y, const int32_t* copy_to_sorted, const int32_t* sorted_to_copy,
@@ -536,7 +537,7 @@ gg_status moe_unpermute_grad(const void* dout, const void* y, const int32_t* cop
     gg::UnpermuteGradArgs a{};
     a.dout = dout; a.y = y; a.copy_to_sorted = copy_to_sorted; a.sorted_to_copy = sorted_to_copy; a.weights = weights;
     a.dy = dy; a.dweights = dweights; a.tokens = (int)tokens; a.top_k = top_k; a.n = (int)n;
-    return gg::launch_unpermute_grad(a, dtype == GG_DT_BF16, (hipStream_t)stream) == hipSuccess ? GG_OK : GG_ERR_HIP;
+    return launched(gg::launch_unpermute_grad(a, dtype == GG_DT_BF16, (hipStream_t)stream));
 }
 
 gg_status mxfp4_quantize(const void* x, uint8_t* codes, uint8_t* scale, int64_t rows, int64_t k, int64_t x_stride,
@@ -549,9 +550,7 @@ gg_status mxfp4_quantize(const void* x, uint8_t* codes, uint8_t* scale, int64_t 
     if (k % 32 != 0) return GG_ERR_UNSUPPORTED;
     if (rows * k > 0 && (!x || !codes || !scale)) return GG_ERR_NULL_PTR;
     if (!aligned(x, elem_bytes(in_dtype)) || !aligned(codes, 16) || !aligned(scale, 8)) return GG_ERR_MISALIGNED;
-    return gg::launch_fp4_quantize(x, in_dtype == GG_DT_BF16, rows, k, x_stride, codes, scale, (hipStream_t)stream) == hipSuccess
-               ? GG_OK
-               : GG_ERR_HIP;
+    return launched(gg::launch_fp4_quantize(x, in_dtype == GG_DT_BF16, rows, k, x_stride, codes, scale, (hipStream_t)stream));
 }
 
 gg_status mxfp4_quantize_weights(const void* w, uint8_t* codes, uint8_t* scale, int32_t g, int64_t k, int64_t n,
@@ -563,9 +562,7 @@ gg_status mxfp4_quantize_weights(const void* w, uint8_t* codes, uint8_t* scale, 
     if (k % 32 != 0) return GG_ERR_UNSUPPORTED;
     if (k * n > 0 && (!w || !codes || !scale)) return GG_ERR_NULL_PTR;
     if (!aligned(w, elem_bytes(in_dtype)) || !aligned(codes, 16) || !aligned(scale, 8)) return GG_ERR_MISALIGNED;
-    return gg::launch_fp4_quantize_weights(w, in_dtype == GG_DT_BF16, g, k, n, codes, scale, (hipStream_t)stream) == hipSuccess
-               ? GG_OK
-               : GG_ERR_HIP;
+    return launched(gg::launch_fp4_quantize_weights(w, in_dtype == GG_DT_BF16, g, k, n, codes, scale, (hipStream_t)stream));
 }
 
 gg_status mxfp4_dequantize(const uint8_t* codes, const uint8_t* scale, void* out, int32_t g, int64_t n, int64_t k,
@@ -577,9 +574,7 @@ gg_status mxfp4_dequantize(const uint8_t* codes, const uint8_t* scale, void* out
     if (k % 32 != 0) return GG_ERR_UNSUPPORTED;
     if (k * n > 0 && (!codes || !scale || !out)) return GG_ERR_NULL_PTR;
     if (!aligned(out, elem_bytes(out_dtype)) || !aligned(codes, 16) || !aligned(scale, 8)) return GG_ERR_MISALIGNED;
-    return gg::launch_fp4_dequantize(codes, scale, g, n, k, out, out_dtype == GG_DT_BF16, (hipStream_t)stream) == hipSuccess
-               ? GG_OK
-               : GG_ERR_HIP;
+    return launched(gg::launch_fp4_dequantize(codes, scale, g, n, k, out, out_dtype == GG_DT_BF16, (hipStream_t)stream));
 }
 
 gg_status ragged_dot_m_mxfp4(const void* lhs, const void* rhs, const int32_t* group_sizes, void* out, int64_t m, int64_t k,

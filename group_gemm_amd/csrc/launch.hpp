@@ -86,6 +86,10 @@ bool ragged_k_bf16_fast_ok(const KParams& p);
 hipError_t launch_ragged_k_bf16_fast(const KParams& p, int grid, hipStream_t s);
 hipError_t launch_ragged_k_f32(const KParams& p, int grid, hipStream_t s);
 
+// A launch holds fewer than 2^32 threads along x: the most workgroups of 256.  The launchers of one workgroup per
+// some rows below return hipErrorInvalidConfiguration, before they launch anything, where a call needs more.
+constexpr int64_t kMaxBlocks = (int64_t(1) << 24) - 1;
+
 // MXFP4 (e2m1 codes, E8M0 scale panels [ceil(k/256), rows, 8]).
 struct Fp4Params {              // ragged_dot_m_mxfp4
     const uint8_t* lhs;         // [m, k/2]
@@ -98,7 +102,7 @@ struct Fp4Params {              // ragged_dot_m_mxfp4
     int m, k, n, g;
     int out_f32;
 };
-bool ragged_m_fp4_grid_ok(const Fp4Params& p);   // the launch fits 2^31 - 1 workgroups
+bool ragged_m_fp4_grid_ok(const Fp4Params& p);   // the launch and its 32-bit indices hold the shape
 hipError_t launch_ragged_m_fp4(const Fp4Params& p, int cus, hipStream_t s);
 hipError_t launch_fp4_quantize(const void* x, bool bf16, int64_t rows, int64_t k, int64_t stride, uint8_t* codes,
                                uint8_t* scale, hipStream_t s);

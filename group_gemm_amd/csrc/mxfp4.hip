@@ -259,14 +259,12 @@ __global__ __launch_bounds__(256) void dequantize(const uint8_t* __restrict__ co
     }
 }
 
-constexpr int64_t kMaxGrid = INT32_MAX;
-
 template <typename T>
 hipError_t quantize_t(const void* x, int64_t rows, int64_t k, int64_t stride, uint8_t* codes, uint8_t* scale, hipStream_t s) {
     const int panels = (int)((k + kPanel - 1) / kPanel);
     constexpr int U = 4;
     const int64_t grid = (rows + 8 * U - 1) / (8 * U) * panels;
-    if (grid > kMaxGrid) return hipErrorInvalidValue;
+    if (grid > kMaxBlocks) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((quantize_rows<T, U>), dim3((uint32_t)grid), dim3(256), 0, s, (const T*)x, rows, k, stride, codes, scale, panels);
     return hipGetLastError();
 }
@@ -277,7 +275,7 @@ hipError_t quantize_weights_t(const void* w, int g, int64_t k, int64_t n, uint8_
     constexpr int COLS = 32 * 16 / sizeof(T);
     const int64_t ntiles = (n + COLS - 1) / COLS;
     const int64_t grid = ntiles * panels * g;
-    if (grid > kMaxGrid) return hipErrorInvalidValue;
+    if (grid > kMaxBlocks) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((quantize_weights<T>), dim3((uint32_t)grid), dim3(256), 0, s, (const T*)w, k, n, panels, (int)ntiles, codes, scale);
     return hipGetLastError();
 }
@@ -288,7 +286,7 @@ hipError_t dequantize_t(const uint8_t* codes, const uint8_t* scale, int g, int64
     constexpr int U = 4;
     const int64_t rtiles = (n + 8 * U - 1) / (8 * U);
     const int64_t grid = rtiles * panels * g;
-    if (grid > kMaxGrid) return hipErrorInvalidValue;
+    if (grid > kMaxBlocks) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((dequantize<OutT, U>), dim3((uint32_t)grid), dim3(256), 0, s, codes, scale, n, k, panels, (int)rtiles, (OutT*)out);
     return hipGetLastError();
 }

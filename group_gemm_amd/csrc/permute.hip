@@ -377,9 +377,13 @@ __global__ __launch_bounds__(256) void combine(const InT* __restrict__ y, int ro
     }
 }
 
+// waves a token: of at most 512 columns a second wave would have none
+inline int combine_waves(int n) { return n <= 512 ? 1 : 2; }
+inline int64_t combine_blocks(int T, int waves) { return ((int64_t)T + 4 / waves - 1) / (4 / waves); }
+
 template <typename InT, typename OutT, bool WEIGHTED, int W>
 void launch_combine_w(const void* y, int rows, const int32_t* c2s, const float* w, int T, int top_k, int n, void* out, hipStream_t s) {
-    const dim3 grid((T + 4 / W - 1) / (4 / W)), block(256);
+    const dim3 grid((uint32_t)combine_blocks(T, W)), block(256);
     if (n >= 8)
         hipLaunchKernelGGL((combine<InT, OutT, true, WEIGHTED, W>), grid, block, 0, s, (const InT*)y, rows, c2s, w, T, top_k, n, (OutT*)out);
     else
@@ -388,8 +392,7 @@ void launch_combine_w(const void* y, int rows, const int32_t* c2s, const float* 
 template <typename InT, typename OutT>
 hipError_t launch_combine_t(const void* y, int rows, const int32_t* c2s, const float* w, int T, int top_k, int n,
                             void* out, hipStream_t s) {
-    // (of at most 512 columns a second wave would have none)
-    if (n <= 512) w ? launch_combine_w<InT, OutT, true, 1>(y, rows, c2s, w, T, top_k, n, out, s)
+    if (combine_waves(n) == 1) w ? launch_combine_w<InT, OutT, true, 1>(y, rows, c2s, w, T, top_k, n, out, s)
                     : launch_combine_w<InT, OutT, false, 1>(y, rows, c2s, w, T, top_k, n, out, s);
     else w ? launch_combine_w<InT, OutT, true, 2>(y, rows, c2s, w, T, top_k, n, out, s)
            : launch_combine_w<InT, OutT, false, 2>(y, rows, c2s, w, T, top_k, n, out, s);
@@ -410,6 +413,9 @@ PermuteGeometry permute_geometry(int64_t M) {
 hipError_t launch_permute(const PermuteArgs& a, hipStream_t s) {
     const int M = a.tokens * a.top_k;
     const PermuteGeometry pg = permute_geometry(M);
+    const int tok_blocks = (a.tokens + perm::TPB - 1) / perm::TPB;
+    const int zero_blocks = min((M + 3) / 4, 256);
+    if ((int64_t)tok_blocks + zero_blocks > kMaxBlocks) return hipErrorInvalidConfiguration;
     if (pg.nblk > 0)
         hipLaunchKernelGGL(perm::histogram, dim3(pg.nblk), dim3(perm::NT), 0, s, a.experts, M, a.g, pg.chunk, a.counts,
                            a.bad);
@@ -421,8 +427,6 @@ hipError_t launch_permute(const PermuteArgs& a, hipStream_t s) {
     const bool vec = (uintptr_t)a.x % 16 == 0 && (uintptr_t)a.sorted_x % 16 == 0 && a.row_bytes % 16 == 0 &&
                      (!a.x_scale || a.scale_panels > 0 || ((uintptr_t)a.x_scale % 16 == 0 && (uintptr_t)a.sorted_scale % 16 == 0 &&
                                      a.scale_row_bytes % 16 == 0));
-    const int tok_blocks = (a.tokens + perm::TPB - 1) / perm::TPB;
-    const int zero_blocks = min((M + 3) / 4, 256);
     const dim3 grid(tok_blocks + zero_blocks), block(256);
     const uint8_t* xs = a.x_scale && a.scale_row_bytes > 0 ? (const uint8_t*)a.x_scale : nullptr;
     uint8_t* ss = xs ? (uint8_t*)a.sorted_scale : nullptr;
@@ -444,6 +448,7 @@ hipError_t launch_permute(const PermuteArgs& a, hipStream_t s) {
 hipError_t launch_combine(const void* y, bool y_bf16, int rows, const int32_t* c2s, const float* w, int T, int top_k,
                           int n, void* out, bool out_bf16, hipStream_t s) {
     if (T == 0 || n == 0) return hipSuccess;
+    if (perm::combine_blocks(T, perm::combine_waves(n)) > kMaxBlocks) return hipErrorInvalidConfiguration;
     if (y_bf16)
         return out_bf16 ? perm::launch_combine_t<uint16_t, uint16_t>(y, rows, c2s, w, T, top_k, n, out, s)
                         : perm::launch_combine_t<uint16_t, float>(y, rows, c2s, w, T, top_k, n, out, s);

@@ -830,8 +830,11 @@ inline bool tile_faster(const Fp4Params& p, int cus) {
 }  // namespace fp4
 
 bool ragged_m_fp4_grid_ok(const Fp4Params& p) {
-    // (column indices past n must not leave 32 bits either)
-    return p.n <= INT32_MAX - 256 && fp4::slot_bound(p, 16) * ((p.n + 15) / 16) <= INT32_MAX && (int64_t)128 * (p.k >> 1) < (int64_t(1) << 31);
+    // Column indices past n must not leave 32 bits either.  The block kernel's workgroups are at most its row tiles
+    // and 16 more a compute unit (up to 1024 of them); that many keep m below 2^30, so that rounding a group's rows
+    // up to whole tiles stays in 32 bits too.
+    return p.n <= INT32_MAX - 256 && fp4::slot_bound(p, 16) * ((p.n + 15) / 16) <= INT32_MAX && (int64_t)128 * (p.k >> 1) < (int64_t(1) << 31) &&
+           fp4::slot_bound(p, fp4::block::ROWS) + 16 * 1024 + 8 <= kMaxBlocks;
 }
 
 hipError_t launch_ragged_m_fp4(const Fp4Params& p, int cus, hipStream_t s) {

@@ -177,19 +177,19 @@ __global__ __launch_bounds__(256) void kernel(UnpermuteGradArgs a, int tok_block
 }
 
 template <typename T, int WPT>
-void launch_w(const UnpermuteGradArgs& a, hipStream_t s) {
-    const int tpb = 4 / WPT, tok_blocks = (a.tokens + tpb - 1) / tpb;
+hipError_t launch_w(const UnpermuteGradArgs& a, hipStream_t s) {
+    const int tpb = 4 / WPT, tok_blocks = (int)(((int64_t)a.tokens + tpb - 1) / tpb);
     const int64_t M = (int64_t)a.tokens * a.top_k;
     const int clear = (int)((M + 4 * CLEAR - 1) / (4 * CLEAR) < 512 ? (M + 4 * CLEAR - 1) / (4 * CLEAR) : 512);
+    if ((int64_t)tok_blocks + clear > kMaxBlocks) return hipErrorInvalidConfiguration;
     if (a.n >= 8) hipLaunchKernelGGL((kernel<T, true, WPT>), dim3(tok_blocks + clear), dim3(256), 0, s, a, tok_blocks);
     else hipLaunchKernelGGL((kernel<T, false, WPT>), dim3(tok_blocks + clear), dim3(256), 0, s, a, tok_blocks);
+    return hipGetLastError();
 }
 
 template <typename T>
 hipError_t launch_t(const UnpermuteGradArgs& a, hipStream_t s) {
-    if (a.n <= 512) launch_w<T, 1>(a, s);   // (a second wave would have no columns)
-    else launch_w<T, 2>(a, s);
-    return hipGetLastError();
+    return a.n <= 512 ? launch_w<T, 1>(a, s) : launch_w<T, 2>(a, s);   // (a second wave would have no columns)
 }
 
 }  // namespace upg

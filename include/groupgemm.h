@@ -158,6 +158,8 @@ gg_status ragged_dot_m_nk(const void* lhs, const void* rhs_nk, const int32_t* gr
  *     rows needs are contiguous, which a row-major [rows, k/32] array is not.
  *   Weights [g, k, n] become codes [g, n, k/2] and scales [g, ceil(k/256), n, 8].
  *   Code arrays are 16-byte aligned, scale arrays 8-byte aligned.
+ *   The conversions take up to 2^24 - 1 workgroups (GG_ERR_BAD_SHAPE past that): one for 32 rows of a
+ *   panel, and of weights for 256 (bf16) or 128 (fp32) columns of a panel.
  *
  * mxfp4_quantize -- rows to MXFP4 (the blocked form that ragged_dot_m_mxfp4 multiplies).
  * ("[Triton/Gluon] Merge MoE MXFP8 GEMM into existing _moe_gemm_a8w8 kernel": one E8M0 scale per 32
@@ -186,7 +188,8 @@ gg_status mxfp4_dequantize(const uint8_t* codes, const uint8_t* scale, void* out
  *   out[r, :] = lhs[r, :] . rhs[h]^T   for every row r of group h;   rows r >= sum(sizes) = 0.
  *   lhs [m, k/2], lhs_scale [ceil(k/256), m, 8]; rhs [g, n, k/2], rhs_scale [g, ceil(k/256), n, 8]
  *   out [m, n]  bf16 or fp32; every element written
- * k % 32 == 0 (GG_ERR_UNSUPPORTED otherwise) and k < 2^25; any m and n.  Few rows per group (single
+ * k % 32 == 0 (GG_ERR_UNSUPPORTED otherwise) and k < 2^25, m up to 2^30 - 2^21, n up to 2^31 - 257 and
+ * an out of up to about 2^39 elements (GG_ERR_BAD_SHAPE past that).  Few rows per group (single
  * tokens, decoding batches), some tens and many (prompts) take different kernels, which add in
  * different orders; one kernel's result does not depend on the launch.  Workspace, status and
  * errors as ragged_dot_m: gg_workspace_bytes(GG_OP_RAGGED_M, m, k, n, g, 0, GG_DT_E2M1); the
@@ -293,7 +296,7 @@ gg_status padded_dot(gg_op mode, const void* a, const void* b, const int32_t* gr
  *                                   copy was not routed
  * Every output element is written on every call; with tokens == 0 only group_sizes (zeros)
  * is written and the other pointers may be NULL.  All computed on the device (histogram,
- * scan, rank, gather); nothing is read back.  tokens * top_k <= 2^30.  Workspace:
+ * scan, rank, gather); nothing is read back.  tokens * top_k <= 2^30 and tokens <= 2^25 - 514.  Workspace:
  * gg_workspace_bytes(GG_OP_PERMUTE, tokens * top_k, k, 0, g, 0, dtype) bytes, 16-byte
  * aligned; its status word is rewritten by every call. */
 gg_status moe_permute(const void* x, const uint8_t* x_scale, const int32_t* experts, void* sorted_x,
@@ -311,7 +314,9 @@ gg_status moe_permute(const void* x, const uint8_t* x_scale, const int32_t* expe
  *   weights        [tokens, top_k]      fp32 router weights
  *   out            [tokens, n]          out_dtype (fp32 or bf16):
  *     out[t, :] = sum_j weights[t, j] * y[copy_to_sorted[t * top_k + j], :]
- * fp32 accumulation in j order, one rounding.  No workspace. */
+ * fp32 accumulation in j order, one rounding.  No workspace.  tokens * top_k <= 2^30 and tokens <=
+ * 2^25 - 2 (2^26 - 4 for n <= 512).  out may be y itself where top_k = 1, the types are the same and every
+ * row stays in its place; other overlaps race, and are not checked. */
 gg_status moe_unpermute(const void* y, const int32_t* copy_to_sorted, const float* weights, void* out,
                         int64_t tokens, int32_t top_k, int64_t n, gg_dtype in_dtype,
                         gg_dtype out_dtype, void* stream);
@@ -323,7 +328,8 @@ gg_status moe_unpermute(const void* y, const int32_t* copy_to_sorted, const floa
  *                                       [0, tokens * top_k) (-1: not routed) adds nothing
  *   dx             [tokens, k]          out_dtype (fp32 or bf16):
  *     dx[t, :] = sum_j dsorted[copy_to_sorted[t * top_k + j], :]
- * fp32 accumulation in j order, one rounding; every element of dx is written.  No workspace.  dx may not
+ * fp32 accumulation in j order, one rounding; every element of dx is written.  No workspace.  Tokens as in
+ * moe_unpermute.  dx may not
  * lie in dsorted or copy_to_sorted (GG_ERR_UNSUPPORTED): other rows' copies are still read there. */
 gg_status moe_permute_grad(const void* dsorted, const int32_t* copy_to_sorted, void* dx, int64_t tokens,
                            int32_t top_k, int64_t k, gg_dtype in_dtype, gg_dtype out_dtype, void* stream);
@@ -339,7 +345,8 @@ gg_status moe_permute_grad(const void* dsorted, const int32_t* copy_to_sorted, v
  *   dweights       [tokens, top_k]      fp32: dweights[i] = dout[i / top_k, :] . y[copy_to_sorted[i], :],
  *     summed in fp32 in an order that depends on n alone; 0 where the entry is outside
  *     [0, tokens * top_k)
- * Every element of dy and dweights is written; no atomics.  No workspace.  dy and dweights may not lie in
+ * Every element of dy and dweights is written; no atomics.  No workspace.  tokens * top_k <= 2^30 and
+ * tokens <= 2^25 - 1026 (2^26 - 2052 for n <= 512).  dy and dweights may not lie in
  * an input or in each other (GG_ERR_UNSUPPORTED), but dweights may be the array of weights itself. */
 gg_status moe_unpermute_grad(const void* dout, const void* y, const int32_t* copy_to_sorted,
                              const int32_t* sorted_to_copy, const float* weights, void* dy,
