@@ -58,6 +58,8 @@ def lib():
         L.mxfp4_quantize_weights.argtypes = [vp, vp, vp, i32, i64, i64, ctypes.c_int, vp]
         L.mxfp4_dequantize.argtypes = [vp, vp, vp, i32, i64, i64, ctypes.c_int, vp]
         L.ragged_dot_m_mxfp4.argtypes = [vp, vp, vp, vp, i64, i64, i64, i32, ctypes.c_int, vp, vp, vp, sz, vp]
+        L.gg_mxfp4_kernel.argtypes = [i64, i64, i64, i32, i32]
+        L.gg_mxfp4_kernel.restype = i32
         L.gg_schedule.argtypes = [vp, i64, i64, i32, i32, i32, vp, vp, vp, vp]
         L.gg_read_device_status.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32), vp]
         L.gg_status_string.argtypes = [ctypes.c_int]

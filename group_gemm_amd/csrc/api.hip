@@ -598,6 +598,13 @@ gg_status ragged_dot_m_mxfp4(const void* lhs, const void* rhs, const int32_t* gr
     return gg::launch_ragged_m_fp4(p, cus, (hipStream_t)stream) == hipSuccess ? GG_OK : GG_ERR_HIP;
 }
 
+int32_t gg_mxfp4_kernel(int64_t m, int64_t k, int64_t n, int32_t g, int32_t cus) {
+    if (g < 1 || g > GG_MAX_GROUPS || cus < 1 || !fits_i32(m) || !fits_i32(k) || !fits_i32(n) || k % 32 != 0) return -1;
+    gg::Fp4Params p{};
+    p.m = (int)m; p.k = (int)k; p.n = (int)n; p.g = g;
+    return gg::ragged_m_fp4_grid_ok(p) ? (int32_t)gg::ragged_m_fp4_kernel(p, cus) : -1;
+}
+
 gg_status gg_schedule(const int32_t* group_sizes, int64_t m, int64_t n, int32_t g, int32_t block_m, int32_t block_n,
                       int32_t* row_off, int32_t* tile_off, uint32_t* status, void* stream) {
     if (!group_sizes || !row_off || !tile_off || !status) return GG_ERR_NULL_PTR;

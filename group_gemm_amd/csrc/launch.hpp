@@ -103,6 +103,7 @@ struct Fp4Params {              // ragged_dot_m_mxfp4
     int out_f32;
 };
 bool ragged_m_fp4_grid_ok(const Fp4Params& p);   // the launch and its 32-bit indices hold the shape
+gg_fp4_kernel ragged_m_fp4_kernel(const Fp4Params& p, int cus);   // which kernel the launch takes
 hipError_t launch_ragged_m_fp4(const Fp4Params& p, int cus, hipStream_t s);
 hipError_t launch_fp4_quantize(const void* x, bool bf16, int64_t rows, int64_t k, int64_t stride, uint8_t* codes,
                                uint8_t* scale, hipStream_t s);

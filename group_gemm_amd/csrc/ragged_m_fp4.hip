@@ -837,13 +837,20 @@ bool ragged_m_fp4_grid_ok(const Fp4Params& p) {
            fp4::slot_bound(p, fp4::block::ROWS) + 16 * 1024 + 8 <= kMaxBlocks;
 }
 
-hipError_t launch_ragged_m_fp4(const Fp4Params& p, int cus, hipStream_t s) {
+gg_fp4_kernel ragged_m_fp4_kernel(const Fp4Params& p, int cus) {
     // Stream or block kernel, in us, at (groups, k, n) x rows a group: (128, 1440, 6344) x 2 115 / 124, (64, 992,
     // 6244) x 2 43 / 49, (128, 2880, 5760) x 1 142 / 151, x 4 211 / 218, x 8 234 / 234, x 16 271 / 250.  With
     // rows of more than 28 KiB a stream workgroup has a CU to itself: (128, 7168, 2048) x 4 183 / 163.
-    if (p.m / p.g <= 4 && p.k > 0 && fp4::stream::row_bytes(p) <= fp4::stream::kMaxRowBytes) return fp4::stream::launch(p, cus, s);
-    if (p.m > 0 && fp4::tile_ok(p) && fp4::tile_faster(p, cus)) return fp4::launch_tile(p, cus, s);
-    return fp4::block::launch(p, cus, s);
+    if (p.m / p.g <= 4 && p.k > 0 && fp4::stream::row_bytes(p) <= fp4::stream::kMaxRowBytes) return GG_FP4_STREAM;
+    return p.m > 0 && fp4::tile_ok(p) && fp4::tile_faster(p, cus) ? GG_FP4_TILE : GG_FP4_BLOCK;
+}
+
+hipError_t launch_ragged_m_fp4(const Fp4Params& p, int cus, hipStream_t s) {
+    switch (ragged_m_fp4_kernel(p, cus)) {
+        case GG_FP4_STREAM: return fp4::stream::launch(p, cus, s);
+        case GG_FP4_TILE: return fp4::launch_tile(p, cus, s);
+        default: return fp4::block::launch(p, cus, s);
+    }
 }
 
 }  // namespace gg

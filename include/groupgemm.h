@@ -199,6 +199,15 @@ gg_status ragged_dot_m_mxfp4(const void* lhs, const void* rhs, const int32_t* gr
                              const uint8_t* lhs_scale, const uint8_t* rhs_scale, void* workspace,
                              size_t workspace_bytes, void* stream);
 
+/* gg_mxfp4_kernel -- which of its kernels ragged_dot_m_mxfp4 takes for a shape on a GPU of `cus` compute
+ * units, or -1 for a shape that it refuses, so that the choice can be tested on its own.  Host only. */
+typedef enum {
+    GG_FP4_STREAM = 0,             /* up to four rows a group                               */
+    GG_FP4_BLOCK = 1,              /* some tens of rows a group, and what the others do not take */
+    GG_FP4_TILE = 2                /* long groups                                           */
+} gg_fp4_kernel;
+int32_t gg_mxfp4_kernel(int64_t m, int64_t k, int64_t n, int32_t g, int32_t cus);
+
 /* ragged_dot_m_epilogue -- ragged_dot_m with a fused epilogue, in place on out:
  *   out[r, :] = alpha * (lhs[r, :] . rhs[h]) + bias[h, :] + beta * out[r, :]
  * for every row r of group h; rows r >= sum(sizes) are 0 as in ragged_dot_m.
