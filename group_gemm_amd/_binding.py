@@ -86,22 +86,14 @@ def _p(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(device):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
-
-
 def _raw_stream(index):
     """The current stream's handle, without the Stream object around it (4 us of a call's 16)."""
     return torch._C._cuda_getCurrentRawStream(index)
 
 
-def _check(code, what):
-    if code != 0:
-        raise GGError(code, what)
-
-
 def _call(name, dev, *args):
-    """One call of the library on the current stream of `dev`, with `dev` the current device."""
+    """One call of the library on the current stream of `dev`, with `dev` the current device: kernels run on the
+    current device, and the default stream's handle is the same on all of them."""
     if torch.cuda.current_device() != dev.index:
         with torch.cuda.device(dev):
             code = getattr(lib(), name)(*args, _raw_stream(dev.index))
@@ -235,19 +227,16 @@ def ragged_dot_m(lhs, rhs, group_sizes, out=None, out_dtype=None, lhs_scale=None
     out = _out(out, "out", dev, (m, n), out_dtype)
     ws = _workspace("ragged_m", m, k, n, g, 0, lhs.dtype, dev, workspace)
     if epilogue:
-        code = lib().ragged_dot_m_epilogue(_p(lhs), _p(rhs), _p(group_sizes), _p(out), m, k, n, g, GG_DT[lhs.dtype],
-                                           GG_DT[out.dtype], _p(lhs_scale), _p(rhs_scale), _p(bias), stride,
-                                           float(alpha), float(beta), _p(ws), ws.numel(), _stream(dev))
-        _check(code, "ragged_dot_m_epilogue")
+        _call("ragged_dot_m_epilogue", dev, _p(lhs), _p(rhs), _p(group_sizes), _p(out), m, k, n, g, GG_DT[lhs.dtype],
+              GG_DT[out.dtype], _p(lhs_scale), _p(rhs_scale), _p(bias), stride, float(alpha), float(beta), _p(ws),
+              ws.numel())
         return out
     if rhs_layout == "nk":
-        code = lib().ragged_dot_m_nk(_p(lhs), _p(rhs), _p(group_sizes), _p(out), m, k, n, g, GG_DT[lhs.dtype],
-                                     GG_DT[out.dtype], _p(ws), ws.numel(), _stream(dev))
-        _check(code, "ragged_dot_m_nk")
+        _call("ragged_dot_m_nk", dev, _p(lhs), _p(rhs), _p(group_sizes), _p(out), m, k, n, g, GG_DT[lhs.dtype],
+              GG_DT[out.dtype], _p(ws), ws.numel())
         return out
-    code = lib().ragged_dot_m(_p(lhs), _p(rhs), _p(group_sizes), _p(out), m, k, n, g, GG_DT[lhs.dtype],
-                              GG_DT[out.dtype], _p(lhs_scale), _p(rhs_scale), _p(ws), ws.numel(), _stream(dev))
-    _check(code, "ragged_dot_m")
+    _call("ragged_dot_m", dev, _p(lhs), _p(rhs), _p(group_sizes), _p(out), m, k, n, g, GG_DT[lhs.dtype],
+          GG_DT[out.dtype], _p(lhs_scale), _p(rhs_scale), _p(ws), ws.numel())
     return out
 
 
@@ -271,9 +260,8 @@ def ragged_dot_m_noalloc(lhs, rhs, group_sizes, out, lhs_scale=None, rhs_scale=N
     _out(out, "out", dev, (m, n), None)
     if status is not None:
         _tensor(status, "status", dev, (1,), dtypes=(torch.int32, torch.uint32))
-    code = lib().ragged_dot_m_noalloc(_p(lhs), _p(rhs), _p(group_sizes), _p(out), m, k, n, g, GG_DT[lhs.dtype],
-                                      GG_DT[out.dtype], _p(lhs_scale), _p(rhs_scale), _p(status), _stream(dev))
-    _check(code, "ragged_dot_m_noalloc")
+    _call("ragged_dot_m_noalloc", dev, _p(lhs), _p(rhs), _p(group_sizes), _p(out), m, k, n, g, GG_DT[lhs.dtype],
+          GG_DT[out.dtype], _p(lhs_scale), _p(rhs_scale), _p(status))
     return out
 
 
@@ -306,10 +294,8 @@ def ragged_dot_m_gated(lhs, w0, w1, group_sizes, act="silu", out=None, out_dtype
         out_dtype = out.dtype if out is not None else torch.bfloat16
     out = _out(out, "out", dev, (m, n), out_dtype)
     ws = _workspace("ragged_m", m, k, n, g, 0, lhs.dtype, dev, workspace)
-    code = lib().ragged_dot_m_gated(_p(lhs), _p(w0), _p(w1), _p(group_sizes), _p(out), m, k, n, g, GG_DT[lhs.dtype],
-                                    GG_DT[out.dtype], ACT[act], _p(bias0), _p(bias1), stride, _p(ws), ws.numel(),
-                                    _stream(dev))
-    _check(code, "ragged_dot_m_gated")
+    _call("ragged_dot_m_gated", dev, _p(lhs), _p(w0), _p(w1), _p(group_sizes), _p(out), m, k, n, g, GG_DT[lhs.dtype],
+          GG_DT[out.dtype], ACT[act], _p(bias0), _p(bias1), stride, _p(ws), ws.numel())
     return out
 
 
@@ -335,14 +321,11 @@ def ragged_dot_k(lhs, dout, group_sizes, out=None, out_dtype=None, workspace=Non
     out = _out(out, "out", dev, (g, k, n), out_dtype)
     ws = _workspace("ragged_k", m, k, n, g, 0, lhs.dtype, dev, workspace)
     if alpha != 1.0 or beta != 0.0:
-        code = lib().ragged_dot_k_epilogue(_p(lhs), _p(dout), _p(group_sizes), _p(out), m, k, n, g, GG_DT[lhs.dtype],
-                                           GG_DT[out.dtype], float(alpha), float(beta), _p(ws), ws.numel(),
-                                           _stream(dev))
-        _check(code, "ragged_dot_k_epilogue")
+        _call("ragged_dot_k_epilogue", dev, _p(lhs), _p(dout), _p(group_sizes), _p(out), m, k, n, g, GG_DT[lhs.dtype],
+              GG_DT[out.dtype], float(alpha), float(beta), _p(ws), ws.numel())
         return out
-    code = lib().ragged_dot_k(_p(lhs), _p(dout), _p(group_sizes), _p(out), m, k, n, g, GG_DT[lhs.dtype],
-                              GG_DT[out.dtype], _p(ws), ws.numel(), _stream(dev))
-    _check(code, "ragged_dot_k")
+    _call("ragged_dot_k", dev, _p(lhs), _p(dout), _p(group_sizes), _p(out), m, k, n, g, GG_DT[lhs.dtype],
+          GG_DT[out.dtype], _p(ws), ws.numel())
     return out
 
 
@@ -380,9 +363,8 @@ def padded_dot(mode, a, b, group_sizes, capacity, out=None, out_dtype=None, a_sc
     out = _out(out, "out", dev, shape, out_dtype)
     op = "padded_" + mode
     ws = _workspace(op, m, k, n, g, capacity, a.dtype, dev, workspace)
-    code = lib().padded_dot(OP[op], _p(a), _p(b), _p(group_sizes), _p(out), m, k, n, g, capacity, GG_DT[a.dtype],
-                            GG_DT[out.dtype], _p(a_scale), _p(b_scale), _p(ws), ws.numel(), _stream(dev))
-    _check(code, "padded_dot")
+    _call("padded_dot", dev, OP[op], _p(a), _p(b), _p(group_sizes), _p(out), m, k, n, g, capacity, GG_DT[a.dtype],
+          GG_DT[out.dtype], _p(a_scale), _p(b_scale), _p(ws), ws.numel())
     return out
 
 
@@ -437,9 +419,8 @@ def moe_permute(x, experts, g, x_scale=None, workspace=None, out=None):
     _tensor(s2c, "sorted_to_copy", dev, (M,), torch.int32)
     _tensor(c2s, "copy_to_sorted", dev, (M,), torch.int32)
     ws = _workspace("permute", M, k, 0, g, 0, x.dtype, dev, workspace)
-    code = lib().moe_permute(_p(x), _p(x_scale), _p(experts), _p(sorted_x), _p(sorted_scale), _p(group_sizes), _p(s2c),
-                             _p(c2s), tokens, top_k, k, g, GG_DT[x.dtype], _p(ws), ws.numel(), _stream(dev))
-    _check(code, "moe_permute")
+    _call("moe_permute", dev, _p(x), _p(x_scale), _p(experts), _p(sorted_x), _p(sorted_scale), _p(group_sizes), _p(s2c),
+          _p(c2s), tokens, top_k, k, g, GG_DT[x.dtype], _p(ws), ws.numel())
     return sorted_x, sorted_scale, group_sizes, s2c, c2s
 
 
@@ -459,9 +440,8 @@ def moe_unpermute(y, copy_to_sorted, weights, out=None, out_dtype=None):
     if out_dtype is None:
         out_dtype = out.dtype if out is not None else torch.bfloat16
     out = _out(out, "out", dev, (tokens, n), out_dtype)
-    code = lib().moe_unpermute(_p(y), _p(copy_to_sorted), _p(weights), _p(out), tokens, top_k, n, GG_DT[y.dtype],
-                               GG_DT[out.dtype], _stream(dev))
-    _check(code, "moe_unpermute")
+    _call("moe_unpermute", dev, _p(y), _p(copy_to_sorted), _p(weights), _p(out), tokens, top_k, n, GG_DT[y.dtype],
+          GG_DT[out.dtype])
     return out
 
 def moe_permute_grad(dsorted, copy_to_sorted, top_k, out=None, out_dtype=None):
@@ -632,9 +612,7 @@ def build_schedule(group_sizes, m, n, block_m, block_n):
     row_off = torch.empty(g + 1, dtype=torch.int32, device=dev)
     tile_off = torch.empty(g + 1, dtype=torch.int32, device=dev)
     status = torch.empty(1, dtype=torch.int32, device=dev)
-    code = lib().gg_schedule(_p(group_sizes), m, n, g, block_m, block_n, _p(row_off), _p(tile_off), _p(status),
-                             _stream(dev))
-    _check(code, "gg_schedule")
+    _call("gg_schedule", dev, _p(group_sizes), m, n, g, block_m, block_n, _p(row_off), _p(tile_off), _p(status))
     return row_off, tile_off, status
 
 
@@ -643,6 +621,5 @@ def read_device_status(workspace):
     if workspace.numel() < 4:
         raise ValueError("workspace too small to hold the status word")
     flags = ctypes.c_uint32(0)
-    _check(lib().gg_read_device_status(_p(workspace), ctypes.byref(flags), _stream(workspace.device)),
-           "gg_read_device_status")
+    _call("gg_read_device_status", workspace.device, _p(workspace), ctypes.byref(flags))
     return flags.value
