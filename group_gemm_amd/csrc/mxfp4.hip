@@ -10,8 +10,9 @@
 // 252-255), so one conversion is exact to the definition and the scale is one shift.
 //
 // All three kernels move each byte once and compute little: they are bound by memory.  Measured: rows
-// [4096, 7168] bf16 12.5 us and back 11.6 us (5.9 and 6.4 TB/s, part of it out of the last-level cache), weights
-// [8, 4096, 14336] bf16 and back 448 us (5.3 TB/s).
+// [4096, 7168] bf16 12.8 us and back 12.0 us (5.8 and 6.2 TB/s, part of it out of the last-level cache), fp32 24.5
+// and 23.4; weights [8, 4096, 14336] bf16 198 us and back 232 us (6.0 and 5.1 TB/s), fp32 359 and 598 us (5.9 and
+// 3.6 TB/s: the way back to fp32 is 1.3 times a copy's time).
 #include "common.hpp"
 #include "launch.hpp"
 

@@ -431,17 +431,25 @@ inline hipError_t launch(const Fp4Params& p, int cus, hipStream_t s) {
 // c + 1 come out of their slot into the registers that panel c has done with, and panel c + 2 is loaded into
 // panel c's slot, which was emptied before panel c began: a load has all but the first MFMAs of a panel to
 // arrive.  The stream runs on into the workgroup's next tile, so a tile begins with its first panel in
-// registers and its second in LDS, and the results of the tile before leave meanwhile.
-// 8192 rows of 8 groups, k = 4096, n = 14336: 270 us, 3560 TFLOP/s; 32768 rows of 256 very unequal groups,
-// k = 7168, n = 2048: 502 us, 4.5 TB/s, bound by memory; 8192 rows, k = 16384, n = 8192: 4500 TFLOP/s.  A panel
-// takes 1.8 us and a tile 5 beside them.  Without its loads a panel takes 1.5: these instructions alone, on
-// random data, run at 6000 TFLOP/s and no more whatever feeds them, as the chip lowers its clock.  Loads spread
-// over the first 31, 45, 52 or 60 of a panel's 64 instructions measured within 2 %, all before the first 2.0 us.
+// registers and its second in LDS.  Between two tiles no matrix instruction runs: the results turn in LDS and go
+// out as stores, of which only the last are still under way while the next tile's first panel is computed.
+// 8192 rows of 8 groups, k = 4096, n = 14336: 266 us, 3600 TFLOP/s.  32768 rows of 256 very unequal groups,
+// k = 7168, n = 2048: 505 us among other calls; in a row of twelve 498 to 592, median 564, as the chip lowers its
+// clock: 4.5 and 4.0 TB/s, bound by memory.  8192 rows of 8 groups, n = 8192, which are four tiles a workgroup,
+// with 3 / 8 / 16 / 64 panels: 57 / 81 / 147 / 500 us (4400 TFLOP/s): 1.8 to 2.1 us a panel, and 7 to 9 us a tile
+// beside them, the launch among it.  Without its loads a panel takes 1.5: these instructions alone run at 6300
+// TFLOP/s on random data and 8700 on zeros, with the operands' reads from LDS at 5700 to 6200 and 8800.  Loads
+// spread over the first 31, 45, 52 or 60 of a panel's 64 instructions measured within 2 %, all before the first
+// 2.0 us.
 namespace tile {
 constexpr int BM = 256, BN = 256, NT = 256, MI = 4, NJ = 4, SUB = 4;   // SUB: instructions along k of a panel
 constexpr int OPER = 256 * kRowBytes;     // one operand's slot
 constexpr int SC = 256 * 8;               // one operand's scales of a panel
-constexpr int ROT = 2;                    // panels between the starts of neighbouring column tiles
+// panels between the starts of neighbouring column tiles.  2 / 0, in us, at 8192 rows of 8 groups, n = 8192: k = 768
+// 57.4 / 56.3, 1024 60.0 / 61.2, 2048 80.9 / 82.4, 2880 113.1 / 114.6, 4096 147.0 / 148.0, 7168 237.1 / 234.3, 8192
+// 266.9 / 264.7, 16384 499.5 / 500.8; (32, 2880, 5760) x 512 187.2 / 190.6; (256, 7168, 2048) x 128 439.9 / 443.0:
+// at most 2 % either way, and more of the shapes above faster with 2
+constexpr int ROT = 2;
 constexpr int LOADS = 17;                 // a wave's loads of a panel: 1 KiB of scales, 8 + 8 of eight rows
 constexpr int READ = 15;                  // MFMA of a panel after which the next panel's reads begin
 constexpr int load_step(int d) { return d * 31 / LOADS; }   // MFMA after which load d goes out
@@ -791,7 +799,9 @@ __global__ __launch_bounds__(NT, 1) void kernel(Fp4Params p) {
 }
 }  // namespace tile
 
-// 32-bit offsets of the tile kernel's descriptors, and at least three panels
+// 32-bit offsets of the tile kernel's descriptors, and at least three panels, as two are loaded ahead.  (Long groups
+// of one or two panels go to the block kernel, whose stores of 8 or 16 bytes a lane bound it there: 8192 rows of 8
+// groups, n = 7168, take 59 us at k = 256 and 72 at k = 512, 2.2 and 2.5 times what their bytes ask for.)
 inline bool tile_ok(const Fp4Params& p) {
     const int64_t panels = (p.k + kPanel - 1) / kPanel;
     const int64_t tiles = ((int64_t)p.m / tile::BM + p.g + 1) * ((p.n + tile::BN - 1) / tile::BN);
@@ -814,12 +824,16 @@ inline hipError_t launch_tile(const Fp4Params& p, int cus, hipStream_t s) {
 }
 
 // Tile or block kernel, by the times that their tiles' numbers and panels give (a host knows the groups' mean
-// size only: a group of mean size has a half-filled tile more than it fills, and at least one).  In us on 256
+// size only, rows past the last group among it: a group of mean size has a half-filled tile more than it fills, and
+// at least one).  In us on 256
 // CUs: the tile kernel's CUs take ceil(tiles / CUs) tiles each, 6 and 1.4 to 2.1 a panel with the tile's rows,
 // the block kernel's 1.6 and 0.7 a panel for each of its tiles / CUs.  Measured, block / tile, at (groups, k, n) x
 // rows a group: (32, 2880, 2880) x 48 45 / 54, x 64 51 / 58, x 112 66 / 61; (8, 4096, 14336) x 48 53 / 63,
 // x 112 86 / 68; (128, 7168, 2048) x 32 179 / 184, x 48 204 / 192, x 80 310 / 203; few long groups, which are few
 // tiles, (1, 6688, 2752) x 783 32 / 56, (8, 6400, 1344) x 272 26 / 47; (16, 1184, 1600) x 927 60 / 35.
+// Where the mean says little the choice can miss: 512 rows that are all at one of 256 groups, k = 2880, n = 5760,
+// take the stream kernel, 46 us against a floor of 3; 2048 rows at 8 of 64 groups of k = n = 4096 the block kernel,
+// 43 us against 20.
 inline bool tile_faster(const Fp4Params& p, int cus) {
     const double used = p.g < p.m ? p.g : p.m, per = p.m / used, panels = (p.k + kPanel - 1) / kPanel;
     const double t = used * fmax(1., per / tile::BM + .5) * ((p.n + tile::BN - 1) / tile::BN);

@@ -43,6 +43,9 @@
 extern "C" {
 #endif
 
+/* 5: the calls up to moe_unpermute.  The MXFP4 calls, GG_DT_E2M1, the gradients of permute and un-permute and
+ * gg_mxfp4_kernel were added under the same number: they change no earlier call, and a caller that has to know
+ * whether a library holds them looks for the symbols. */
 #define GG_ABI_VERSION 5
 
 /* Each enumeration below also names the ends of the int32 range, so that every int32 value a
