@@ -5,7 +5,8 @@ loading the GPU library.
 """
 _API = ("ragged_dot_m", "ragged_dot_m_noalloc", "ragged_dot_m_gated", "ragged_dot_k", "padded_dot", "moe_permute", "moe_unpermute",
         "moe_permute_grad", "moe_unpermute_grad", "mxfp4_quantize", "mxfp4_quantize_weights", "mxfp4_dequantize",
-        "ragged_dot_m_mxfp4",
+        "ragged_dot_m_mxfp4", "ragged_lora", "ragged_lora_grad", "mxfp8_quantize", "mxfp8_dequantize", "gated_act_mxfp8",
+        "gated_act_mxfp8_grad",
         "workspace_bytes", "read_device_status",
         "build_schedule", "abi_version", "status_string", "lib", "GGError")
 

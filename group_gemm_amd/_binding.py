@@ -14,7 +14,7 @@ LIB_PATH = os.path.join(HERE, "libgroupgemm.so")
 
 FP4 = torch.float4_e2m1fn_x2   # two 4-bit codes per element
 GG_DT = {torch.float32: 0, torch.bfloat16: 1, torch.uint8: 2, torch.float8_e4m3fn: 2, FP4: 3}
-OP = {"ragged_m": 0, "ragged_k": 1, "padded_m": 2, "padded_k": 3, "permute": 4}
+OP = {"ragged_m": 0, "ragged_k": 1, "padded_m": 2, "padded_k": 3, "permute": 4, "lora": 5, "lora_grad": 6}
 DEV_NEGATIVE_SIZE, DEV_SUM_EXCEEDS_M, DEV_OVER_CAPACITY, DEV_BAD_EXPERT = 0x1, 0x2, 0x4, 0x8
 
 _lib = None
@@ -58,6 +58,14 @@ def lib():
         L.mxfp4_quantize_weights.argtypes = [vp, vp, vp, i32, i64, i64, ctypes.c_int, vp]
         L.mxfp4_dequantize.argtypes = [vp, vp, vp, i32, i64, i64, ctypes.c_int, vp]
         L.ragged_dot_m_mxfp4.argtypes = [vp, vp, vp, vp, i64, i64, i64, i32, ctypes.c_int, vp, vp, vp, sz, vp]
+        ci = ctypes.c_int
+        L.mxfp8_quantize.argtypes = [vp, vp, vp, i64, i64, i64, ci, vp]
+        L.mxfp8_dequantize.argtypes = [vp, vp, vp, i64, i64, ci, vp]
+        L.gated_act_mxfp8.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, ci, ci, ci, vp]
+        L.gated_act_mxfp8_grad.argtypes = [vp, vp, vp, vp, vp, vp, i64, i64, i64, ci, ci, ci, vp]
+        L.ragged_dot_k_mxfp8.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, i32, ci, f32, f32, vp, sz, vp]
+        L.ragged_lora.argtypes = [vp] * 9 + [i64, i64, i64, i32, i32, i64, i64, i64, ci, ci, vp, sz, vp]
+        L.ragged_lora_grad.argtypes = [vp] * 12 + [i64, i64, i64, i32, i32, ci, ci, ci, vp, sz, vp]
         L.gg_mxfp4_kernel.argtypes = [i64, i64, i64, i32, i32]
         L.gg_mxfp4_kernel.restype = i32
         L.gg_schedule.argtypes = [vp, i64, i64, i32, i32, i32, vp, vp, vp, vp]
@@ -68,7 +76,8 @@ def lib():
         for f in ("ragged_dot_m", "ragged_dot_m_noalloc", "ragged_dot_m_nk", "ragged_dot_m_epilogue", "ragged_dot_m_gated", "ragged_dot_k",
                   "ragged_dot_k_epilogue",
                   "padded_dot", "moe_permute", "moe_unpermute", "moe_permute_grad", "moe_unpermute_grad", "mxfp4_quantize",
-                  "mxfp4_quantize_weights", "mxfp4_dequantize", "ragged_dot_m_mxfp4", "gg_schedule", "gg_read_device_status"):
+                  "mxfp4_quantize_weights", "mxfp4_dequantize", "ragged_dot_m_mxfp4", "mxfp8_quantize", "mxfp8_dequantize", "gated_act_mxfp8",
+                  "gated_act_mxfp8_grad", "ragged_dot_k_mxfp8", "ragged_lora", "ragged_lora_grad", "gg_schedule", "gg_read_device_status"):
             getattr(L, f).restype = ctypes.c_int
         _lib = L
     return _lib
@@ -299,27 +308,40 @@ def ragged_dot_m_gated(lhs, w0, w1, group_sizes, act="silu", out=None, out_dtype
     return out
 
 
-def ragged_dot_k(lhs, dout, group_sizes, out=None, out_dtype=None, workspace=None, alpha=1.0, beta=0.0):
+def ragged_dot_k(lhs, dout, group_sizes, out=None, out_dtype=None, workspace=None, alpha=1.0, beta=0.0, lhs_scale=None):
     """out[g,k,n]: out[h] = lhs[rows of h]^T . dout[rows of h]; empty groups give 0.
     alpha, beta: out[h] = alpha * (...) + beta * out[h], in place (ragged_dot_k_epilogue;
-    beta = 1 accumulates over micro-steps; beta != 0 needs `out`)."""
+    beta = 1 accumulates over micro-steps; beta != 0 needs `out`).  lhs may be e4m3 codes (float8_e4m3fn
+    or uint8, k % 32 == 0) with their E8M0 lhs_scale [m, k/32], as mxfp8_quantize gives them, and dout bf16
+    (ragged_dot_k_mxfp8)."""
     dev = lhs.device
-    _tensor(lhs, "lhs", None, dtypes=(torch.float32, torch.bfloat16))
+    _tensor(lhs, "lhs", None, dtypes=_IN_DTYPES)
     if lhs.dim() != 2 or dout.dim() != 2 or group_sizes.dim() != 1:
         raise ValueError("lhs must be [m,k], dout [m,n] and group_sizes [g]")
     m, k = lhs.shape
     m2, n = dout.shape
     g = group_sizes.shape[0]
-    _tensor(dout, "dout", dev, dtype=lhs.dtype)
+    mx = _is_e4m3(lhs)
+    _tensor(dout, "dout", dev, dtype=torch.bfloat16 if mx else lhs.dtype)
     _tensor(group_sizes, "group_sizes", dev, (g,), torch.int32)
     if m2 != m:
         raise ValueError(f"lhs has {m} rows, dout {m2}")
+    if mx:
+        if lhs_scale is None or k % 32:
+            raise ValueError("e4m3 rows need lhs_scale [m, k/32] (k % 32 == 0)")
+        _tensor(lhs_scale, "lhs_scale", dev, (m, k // 32), torch.uint8)
+    elif lhs_scale is not None:
+        raise ValueError("lhs_scale is taken only with e4m3 rows")
     if beta != 0.0 and out is None:
         raise ValueError("beta != 0 accumulates into `out`, which must be given")
     if out_dtype is None:
         out_dtype = out.dtype if out is not None else torch.float32
     out = _out(out, "out", dev, (g, k, n), out_dtype)
     ws = _workspace("ragged_k", m, k, n, g, 0, lhs.dtype, dev, workspace)
+    if mx:
+        _call("ragged_dot_k_mxfp8", dev, _p(lhs), _p(lhs_scale), _p(dout), _p(group_sizes), _p(out), m, k, n, g,
+              GG_DT[out.dtype], float(alpha), float(beta), _p(ws), ws.numel())
+        return out
     if alpha != 1.0 or beta != 0.0:
         _call("ragged_dot_k_epilogue", dev, _p(lhs), _p(dout), _p(group_sizes), _p(out), m, k, n, g, GG_DT[lhs.dtype],
               GG_DT[out.dtype], float(alpha), float(beta), _p(ws), ws.numel())
@@ -599,6 +621,229 @@ def ragged_dot_m_mxfp4(lhs, rhs, group_sizes, lhs_scale, rhs_scale, out=None, ou
     _call("ragged_dot_m_mxfp4", dev, lhs.data_ptr(), rhs.data_ptr(), group_sizes.data_ptr(), out.data_ptr(), m, k, n, g,
           GG_DT[out.dtype], lhs_scale.data_ptr(), rhs_scale.data_ptr(), ws.data_ptr(), ws.numel())
     return out
+
+
+# ---------------------------------------------------------------------------------------
+# 8-bit activation checkpoints: codes (torch.float8_e4m3fn, or uint8 bytes) and E8M0 scales (uint8 [rows, k/32])
+
+_E4M3 = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _rows(t, name, device, shape=None, dtype=None, dtypes=None):
+    """A matrix with unit column stride and rows that do not overlap; its row stride."""
+    _tensor(t, name, device, shape, dtype, dtypes, contiguous=False)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix")
+    rows, k = t.shape
+    stride = t.stride(0) if rows > 1 else k
+    if rows and k and ((k > 1 and t.stride(1) != 1) or stride < k):
+        raise ValueError(f"{name} must have unit column stride and rows that do not overlap")
+    return max(stride, k)
+
+
+def _codes8(out, rows, k, dev):
+    codes, scale = out
+    if codes is None:
+        codes = torch.empty((rows, k), dtype=torch.float8_e4m3fn, device=dev)
+    else:
+        _tensor(codes, "codes", dev, (rows, k), dtypes=_E4M3)
+    if scale is None:
+        scale = torch.empty((rows, k // 32), dtype=torch.uint8, device=dev)
+    else:
+        _tensor(scale, "scale", dev, (rows, k // 32), torch.uint8)
+    return codes, scale
+
+
+def mxfp8_quantize(x, out=None):
+    """Rows x [rows, k] (fp32 or bf16, k % 32 == 0, unit column stride, any row stride >= k) to MXFP8:
+    (codes torch.float8_e4m3fn [rows, k], scale uint8 [rows, k/32]), one power-of-two scale per 32 elements
+    along k, the smallest with which nothing is clipped.  `out` may supply the pair (an entry None is allocated)."""
+    dev = x.device
+    stride = _rows(x, "x", None, dtypes=_FLOATS)
+    rows, k = x.shape
+    if k % 32:
+        raise ValueError("x must be [rows, k] with k % 32 == 0")
+    codes, scale = _codes8(out if out is not None else (None, None), rows, k, dev)
+    _call("mxfp8_quantize", dev, x.data_ptr(), codes.data_ptr(), scale.data_ptr(), rows, k, stride, GG_DT[x.dtype])
+    return codes, scale
+
+
+def mxfp8_dequantize(codes, scale, out=None, out_dtype=None):
+    """The values of MXFP8 rows (codes [rows, k], scale [rows, k/32]) as [rows, k]: bf16 (default) or fp32."""
+    dev = codes.device
+    _tensor(codes, "codes", None, dtypes=_E4M3)
+    if codes.dim() != 2 or codes.shape[1] % 32:
+        raise ValueError("codes must be [rows, k] with k % 32 == 0")
+    rows, k = codes.shape
+    _tensor(scale, "scale", dev, (rows, k // 32), torch.uint8)
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else torch.bfloat16
+    out = _out(out, "out", dev, (rows, k), out_dtype)
+    _call("mxfp8_dequantize", dev, codes.data_ptr(), scale.data_ptr(), out.data_ptr(), rows, k, GG_DT[out.dtype])
+    return out
+
+
+def gated_act_mxfp8(gate, up, act="silu", out=None, out_dtype=None):
+    """h = act(gate) * up for gate, up [m, n] (fp32 or bf16, n % 32 == 0, one row stride: two matrices or two halves of
+    one), with the two kept in 8 bits for the backward pass: returns (h [m, n], codes float8_e4m3fn [m, 2n] and scale
+    uint8 [m, 2n/32] of gate | up).  `out` may supply the three (an entry None is allocated)."""
+    dev = gate.device
+    stride = _rows(gate, "gate", None, dtypes=_FLOATS)
+    m, n = gate.shape
+    if _rows(up, "up", dev, (m, n), gate.dtype) != stride:
+        raise ValueError("gate and up must have one row stride")
+    if n % 32:
+        raise ValueError("gate must be [m, n] with n % 32 == 0")
+    if act not in ACT:
+        raise ValueError(f"act must be one of {sorted(ACT)}")
+    h, codes, scale = out if out is not None else (None, None, None)
+    if out_dtype is None:
+        out_dtype = h.dtype if h is not None else gate.dtype
+    h = _out(h, "h", dev, (m, n), out_dtype)
+    codes, scale = _codes8((codes, scale), m, 2 * n, dev)
+    _call("gated_act_mxfp8", dev, gate.data_ptr(), up.data_ptr(), h.data_ptr(), codes.data_ptr(), scale.data_ptr(), m, n,
+          stride, ACT[act], GG_DT[gate.dtype], GG_DT[h.dtype])
+    return h, codes, scale
+
+
+def gated_act_mxfp8_grad(dh, codes, scale, act="silu", out=None, out_dtype=None):
+    """The backward pass of gated_act_mxfp8 from its checkpoint: for dh [m, n] (fp32 or bf16), codes [m, 2n] and scale
+    [m, 2n/32] returns (dgate, dup, h), all [m, n], with h = act(gate) * up recomputed.  `out` may supply the three (an
+    entry None is allocated); dgate and dup may be two halves of one matrix, and one of the three may be dh."""
+    dev = dh.device
+    _tensor(dh, "dh", None, dtypes=_FLOATS)
+    if dh.dim() != 2 or dh.shape[1] % 32:
+        raise ValueError("dh must be [m, n] with n % 32 == 0")
+    m, n = dh.shape
+    _tensor(codes, "codes", dev, (m, 2 * n), dtypes=_E4M3)
+    _tensor(scale, "scale", dev, (m, 2 * n // 32), torch.uint8)
+    if act not in ACT:
+        raise ValueError(f"act must be one of {sorted(ACT)}")
+    dgate, dup, h = out if out is not None else (None, None, None)
+    if out_dtype is None:
+        given = [t.dtype for t in (dgate, dup, h) if t is not None]
+        out_dtype = given[0] if given else dh.dtype
+    if out_dtype not in _FLOATS:
+        raise ValueError(f"out_dtype must be one of {_FLOATS}")
+    if dgate is None:
+        dgate = torch.empty((m, n), dtype=out_dtype, device=dev)
+    if dup is None:
+        dup = torch.empty((m, n), dtype=out_dtype, device=dev)
+    stride = _rows(dgate, "dgate", dev, (m, n), out_dtype)
+    if _rows(dup, "dup", dev, (m, n), out_dtype) != stride:
+        raise ValueError("dgate and dup must have one row stride")
+    h = _out(h, "h", dev, (m, n), out_dtype)
+    _call("gated_act_mxfp8_grad", dev, dh.data_ptr(), codes.data_ptr(), scale.data_ptr(), dgate.data_ptr(), dup.data_ptr(),
+          h.data_ptr(), m, n, stride, ACT[act], GG_DT[dh.dtype], GG_DT[out_dtype])
+    return dgate, dup, h
+
+
+# ---------------------------------------------------------------------------------------
+# low-rank adapters
+
+
+def _adapter_shapes(a, b, dtype, dev):
+    if a.dim() != 3 or b.dim() != 3:
+        raise ValueError("a must be [g, r, k] and b [g, n, r]")
+    g, r, k = a.shape
+    g2, n, r2 = b.shape
+    if g2 != g or r2 != r:
+        raise ValueError(f"a is {tuple(a.shape)}, b {tuple(b.shape)}: [g, r, k] and [g, n, r] are expected")
+    _tensor(a, "a", dev, dtype=dtype)
+    _tensor(b, "b", dev, dtype=dtype)
+    return g, r, k, n
+
+
+def ragged_lora(x, a, b, group_sizes=None, base=None, row_group=None, scaling=None, v=None, out=None, out_dtype=None,
+                workspace=None):
+    """Low-rank adapters beside a shared projection: out[i] = base[i] + scaling[h] * (x[i] . a[h]^T) . b[h]^T for x
+    [m, k], a [g, r, k] and b [g, n, r] of one type (fp32 or bf16), h being the adapter of row i: rows sorted by
+    adapter with group_sizes (int32 [g]; rows past them have none), or rows in any order with row_group (int32 [m],
+    outside [0, g): none).  Rows without an adapter are base's.  base [m, n] (fp32 or bf16) is the shared projection's
+    result, None for 0; out may be base (in place).  x, base and out may have any row stride.  scaling: fp32 [g].  v: fp32
+    [m, r] that receives x[i] . a[h]^T, which ragged_lora_grad takes."""
+    dev = x.device
+    x_stride = _rows(x, "x", None, dtypes=_FLOATS)
+    g, r, k, n = _adapter_shapes(a, b, x.dtype, dev)
+    m = x.shape[0]
+    if x.shape[1] != k:
+        raise ValueError(f"x has k = {x.shape[1]}, a has {k}")
+    if (group_sizes is None) == (row_group is None):
+        raise ValueError("exactly one of group_sizes and row_group must be given")
+    if group_sizes is not None:
+        _tensor(group_sizes, "group_sizes", dev, (g,), torch.int32)
+    else:
+        _tensor(row_group, "row_group", dev, (m,), torch.int32)
+    if scaling is not None:
+        _tensor(scaling, "scaling", dev, (g,), torch.float32)
+    if v is not None:
+        _tensor(v, "v", dev, (m, r), torch.float32)
+    base_stride = n
+    if base is not None:
+        base_stride = _rows(base, "base", dev, (m, n), dtypes=_FLOATS)
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else base.dtype if base is not None else x.dtype
+    if out_dtype not in _FLOATS or (base is not None and base.dtype != out_dtype):
+        raise ValueError(f"out_dtype must be fp32 or bf16 and base's, not {out_dtype}")
+    if out is None:
+        out = torch.empty((m, n), dtype=out_dtype, device=dev)
+    out_stride = _rows(out, "out", dev, (m, n), out_dtype)
+    ws = _workspace("lora", m, k, n, g, r, x.dtype, dev, workspace)
+    _call("ragged_lora", dev, x.data_ptr(), a.data_ptr(), b.data_ptr(), _p(group_sizes), _p(row_group), _p(scaling), _p(base),
+          out.data_ptr(), _p(v), m, k, n, r, g, x_stride, base_stride, out_stride, GG_DT[x.dtype], GG_DT[out_dtype],
+          ws.data_ptr(), ws.numel())
+    return out
+
+
+def ragged_lora_grad(x, v, dout, a, b, group_sizes, dbase=None, scaling=None, x_scale=None, need_dx=True, grad_dtype=None,
+                     out=None, workspace=None):
+    """The gradients of ragged_lora over rows sorted by adapter: (dx [m, k], da [g, r, k], db [g, n, r]) for dout [m, n],
+    the x and v of that call, and dbase [m, k], the shared projection's gradient of x that dx adds to (None: 0).  x may be
+    an 8-bit checkpoint (codes of mxfp8_quantize with x_scale).  need_dx=False: dx is None.  grad_dtype: da's and db's
+    (default fp32).  `out` may supply (dx, da, db) (an entry None is allocated); dx may be dbase (in place)."""
+    dev = dout.device
+    _tensor(dout, "dout", None, dtypes=_FLOATS)
+    if dout.dim() != 2 or x.dim() != 2:
+        raise ValueError("x must be [m, k] and dout [m, n]")
+    g, r, k, n = _adapter_shapes(a, b, dout.dtype, dev)
+    m = dout.shape[0]
+    if dout.shape[1] != n:
+        raise ValueError(f"dout has n = {dout.shape[1]}, b has {n}")
+    if torch.is_tensor(x) and _is_e4m3(x):
+        _tensor(x, "x", dev, (m, k), dtypes=_E4M3)
+        if dout.dtype != torch.bfloat16:
+            raise ValueError("e4m3 rows go with bf16 gradients and weights")
+        if x_scale is None or k % 32:
+            raise ValueError("e4m3 rows need x_scale [m, k/32] (k % 32 == 0)")
+        _tensor(x_scale, "x_scale", dev, (m, k // 32), torch.uint8)
+    else:
+        _tensor(x, "x", dev, (m, k), dout.dtype)
+        if x_scale is not None:
+            raise ValueError("x_scale is taken only with e4m3 rows")
+    _tensor(v, "v", dev, (m, r), torch.float32)
+    _tensor(group_sizes, "group_sizes", dev, (g,), torch.int32)
+    if scaling is not None:
+        _tensor(scaling, "scaling", dev, (g,), torch.float32)
+    dx, da, db = out if out is not None else (None, None, None)
+    if not need_dx and (dx is not None or dbase is not None):
+        raise ValueError("need_dx=False takes neither dbase nor dx")
+    if dbase is not None:
+        _tensor(dbase, "dbase", dev, (m, k), dout.dtype)
+    if need_dx:
+        if dx is None:
+            dx = torch.empty((m, k), dtype=dout.dtype, device=dev)
+        else:
+            _tensor(dx, "dx", dev, (m, k), dout.dtype)
+    if grad_dtype is None:
+        given = [t.dtype for t in (da, db) if t is not None]
+        grad_dtype = given[0] if given else torch.float32
+    da = _out(da, "da", dev, (g, r, k), grad_dtype)
+    db = _out(db, "db", dev, (g, n, r), grad_dtype)
+    ws = _workspace("lora_grad", m, k, n, g, r, dout.dtype, dev, workspace)
+    _call("ragged_lora_grad", dev, x.data_ptr(), _p(x_scale), v.data_ptr(), dout.data_ptr(), a.data_ptr(), b.data_ptr(),
+          group_sizes.data_ptr(), _p(scaling), _p(dbase), _p(dx), da.data_ptr(), db.data_ptr(), m, k, n, r, g, GG_DT[x.dtype],
+          GG_DT[dout.dtype], GG_DT[grad_dtype], ws.data_ptr(), ws.numel())
+    return dx, da, db
 
 
 def build_schedule(group_sizes, m, n, block_m, block_n):

@@ -66,6 +66,20 @@ gg_status launched(hipError_t e) {
 
 bool fits_i32(int64_t x) { return x >= 0 && x <= INT32_MAX; }
 
+// whether two matrices share a byte: rows of `width` bytes, `pitch` apart (rows of one pitch may interleave)
+struct Span { const void* p; uint64_t rows, width, pitch; };
+bool overlap(const Span& a, const Span& b) {
+    if (!a.p || !b.p || a.rows == 0 || b.rows == 0 || a.width == 0 || b.width == 0) return false;
+    if (!overlap(a.p, (a.rows - 1) * a.pitch + a.width, b.p, (b.rows - 1) * b.pitch + b.width)) return false;
+    if (a.pitch != b.pitch || a.rows == 1 || b.rows == 1) return true;
+    const uint64_t a0 = (uintptr_t)a.p, b0 = (uintptr_t)b.p;
+    const uint64_t d = b0 >= a0 ? (b0 - a0) % a.pitch : (a.pitch - (a0 - b0) % a.pitch) % a.pitch;   // columns that b begins after a
+    return d < a.width || d + b.width > a.pitch;
+}
+Span dense(const void* p, uint64_t bytes) { return {p, 1, bytes, bytes}; }
+// whether `out` shares a byte with any of `others`
+template <typename... S> bool meets(const Span& out, const S&... others) { return (overlap(out, others) || ...); }
+
 // Shape and group-size checks shared by every entry point.
 gg_status check_shape(int64_t m, int64_t k, int64_t n, int32_t g, const int32_t* gs) {
     if (!gs) return GG_ERR_NULL_PTR;
@@ -193,6 +207,29 @@ void* scratch_address() {
     return addr[dev];
 }
 
+// Workspace of ragged_lora_grad behind the header: offsets of its parts.
+struct LoraGradLayout { size_t bt, at, t, u, parts, bytes; };
+LoraGradLayout lora_grad_layout(int64_t m, int64_t k, int64_t n, int r, int32_t g, gg_dtype dtype) {
+    const size_t es = elem_bytes(dtype), rows = align_up((size_t)m * r * 4, 256);
+    const int splits = gg::lora_splits(m, n);
+    const int64_t chunk = gg::lora_chunk(m, k, n);
+    LoraGradLayout w{};
+    w.bt = 0;
+    w.at = w.bt + align_up((size_t)g * n * r * es, 256);
+    w.u = w.at + align_up((size_t)g * k * r * es, 256);
+    w.t = splits > 1 ? w.u + rows : w.u;
+    w.parts = w.t + (size_t)splits * rows;
+    w.bytes = w.parts + align_up(2 * (size_t)cdiv64(m, chunk) * (size_t)(k + n) * r * 4, 256);
+    return w;
+}
+
+// [rows, k] in eights of a row's elements, with k % 8 checked elsewhere
+bool eights_ok(int64_t rows, int64_t k) {
+    return fits_i32(rows) && fits_i32(k) && (k == 0 || rows <= ((int64_t(1) << 34) - 8) / k);
+}
+
+bool floats(gg_dtype d) { return d == GG_DT_F32 || d == GG_DT_BF16; }
+
 bool m_dtypes_ok(gg_dtype in, gg_dtype out) {
     if (in == GG_DT_F32) return out == GG_DT_F32;
     if (in == GG_DT_BF16 || in == GG_DT_E4M3) return out == GG_DT_BF16 || out == GG_DT_F32;
@@ -251,6 +288,14 @@ size_t gg_workspace_bytes(gg_op op, int64_t m, int64_t k, int64_t n, int32_t g, 
             if (m > kMaxCopies) return 0;
             const gg::PermuteGeometry pg = gg::permute_geometry(m);
             return kHeader + align_up((size_t)pg.nblk * (size_t)g * 4, 256) + align_up((size_t)pg.nblk * 4, 256);
+        }
+        case GG_OP_LORA: {   // capacity: r
+            if (capacity < 1 || capacity > GG_MAX_RANK || !fits_i32(m) || !fits_i32(k) || in == GG_DT_E4M3) return 0;
+            return kHeader + align_up((size_t)gg::lora_splits(m, k) * (size_t)m * (size_t)capacity * 4, 256);
+        }
+        case GG_OP_LORA_GRAD: {
+            if (capacity < 1 || capacity > GG_MAX_RANK || !fits_i32(m) || !fits_i32(k) || !fits_i32(n) || in == GG_DT_E4M3) return 0;
+            return kHeader + lora_grad_layout(m, k, n, (int)capacity, g, in).bytes;
         }
         default: break;
     }
@@ -603,6 +648,191 @@ int32_t gg_mxfp4_kernel(int64_t m, int64_t k, int64_t n, int32_t g, int32_t cus)
     gg::Fp4Params p{};
     p.m = (int)m; p.k = (int)k; p.n = (int)n; p.g = g;
     return gg::ragged_m_fp4_grid_ok(p) ? (int32_t)gg::ragged_m_fp4_kernel(p, cus) : -1;
+}
+
+gg_status mxfp8_quantize(const void* x, uint8_t* codes, uint8_t* scale, int64_t rows, int64_t k, int64_t x_stride,
+                         gg_dtype in_dtype, void* stream) {
+    if (!eights_ok(rows, k) || x_stride < k || x_stride > (int64_t(1) << 31)) return GG_ERR_BAD_SHAPE;
+    if (!floats(in_dtype)) return GG_ERR_BAD_DTYPE;
+    if (k % 32 != 0) return GG_ERR_UNSUPPORTED;
+    if (rows * k > 0 && (!x || !codes || !scale)) return GG_ERR_NULL_PTR;
+    const size_t es = elem_bytes(in_dtype);
+    if (!aligned(x, es) || !aligned(codes, 16)) return GG_ERR_MISALIGNED;
+    const Span xs{x, (uint64_t)rows, (uint64_t)k * es, (uint64_t)x_stride * es}, cs = dense(codes, (uint64_t)(rows * k)),
+               ss = dense(scale, (uint64_t)(rows * (k / 32)));
+    if (meets(cs, xs, ss) || meets(ss, xs)) return GG_ERR_UNSUPPORTED;
+    return launched(gg::launch_fp8_quantize(x, in_dtype == GG_DT_BF16, rows, k, x_stride, codes, scale, (hipStream_t)stream));
+}
+
+gg_status mxfp8_dequantize(const uint8_t* codes, const uint8_t* scale, void* out, int64_t rows, int64_t k, gg_dtype out_dtype,
+                           void* stream) {
+    if (!eights_ok(rows, k)) return GG_ERR_BAD_SHAPE;
+    if (!floats(out_dtype)) return GG_ERR_BAD_DTYPE;
+    if (k % 32 != 0) return GG_ERR_UNSUPPORTED;
+    if (rows * k > 0 && (!codes || !scale || !out)) return GG_ERR_NULL_PTR;
+    const size_t es = elem_bytes(out_dtype);
+    if (!aligned(codes, 16) || !aligned(out, es)) return GG_ERR_MISALIGNED;
+    if (meets(dense(out, (uint64_t)(rows * k) * es), dense(codes, (uint64_t)(rows * k)), dense(scale, (uint64_t)(rows * (k / 32)))))
+        return GG_ERR_UNSUPPORTED;
+    return launched(gg::launch_fp8_dequantize(codes, scale, rows, k, out, out_dtype == GG_DT_BF16, (hipStream_t)stream));
+}
+
+gg_status gated_act_mxfp8(const void* gate, const void* up, void* h, uint8_t* codes, uint8_t* scale, int64_t m, int64_t n,
+                          int64_t stride, gg_activation act, gg_dtype in_dtype, gg_dtype out_dtype, void* stream) {
+    if (!eights_ok(m, n) || !eights_ok(m, 2 * n) || stride < n || stride > (int64_t(1) << 31)) return GG_ERR_BAD_SHAPE;
+    if (!floats(in_dtype) || !floats(out_dtype)) return GG_ERR_BAD_DTYPE;
+    if (n % 32 != 0 || (act != GG_ACT_SILU && act != GG_ACT_GELU_TANH)) return GG_ERR_UNSUPPORTED;
+    if (m * n > 0 && (!gate || !up || !h || !codes || !scale)) return GG_ERR_NULL_PTR;
+    const uint64_t es = elem_bytes(in_dtype), os = elem_bytes(out_dtype), M = (uint64_t)m, N = (uint64_t)n;
+    if (!aligned(gate, es) || !aligned(up, es) || !aligned(h, os) || !aligned(codes, 16)) return GG_ERR_MISALIGNED;
+    const Span g{gate, M, N * es, (uint64_t)stride * es}, u{up, M, N * es, (uint64_t)stride * es};
+    const Span hs = dense(h, M * N * os), cs = dense(codes, 2 * M * N), ss = dense(scale, M * N / 16);
+    if (meets(hs, g, u, cs, ss) || meets(cs, g, u, ss) || meets(ss, g, u)) return GG_ERR_UNSUPPORTED;
+    gg::GatedActArgs a{};
+    a.gate = gate; a.up = up; a.h = h; a.codes = codes; a.scale = scale; a.m = m; a.n = n; a.stride = stride;
+    a.bf16 = in_dtype == GG_DT_BF16; a.out_bf16 = out_dtype == GG_DT_BF16; a.gelu = act == GG_ACT_GELU_TANH;
+    return launched(gg::launch_gated_act(a, (hipStream_t)stream));
+}
+
+gg_status gated_act_mxfp8_grad(const void* dh, const uint8_t* codes, const uint8_t* scale, void* dgate, void* dup, void* h,
+                               int64_t m, int64_t n, int64_t stride, gg_activation act, gg_dtype in_dtype, gg_dtype out_dtype,
+                               void* stream) {
+    if (!eights_ok(m, n) || !eights_ok(m, 2 * n) || stride < n || stride > (int64_t(1) << 31)) return GG_ERR_BAD_SHAPE;
+    if (!floats(in_dtype) || !floats(out_dtype)) return GG_ERR_BAD_DTYPE;
+    if (n % 32 != 0 || (act != GG_ACT_SILU && act != GG_ACT_GELU_TANH)) return GG_ERR_UNSUPPORTED;
+    if (m * n > 0 && (!dh || !dgate || !dup || !codes || !scale)) return GG_ERR_NULL_PTR;
+    const uint64_t es = elem_bytes(in_dtype), os = elem_bytes(out_dtype), M = (uint64_t)m, N = (uint64_t)n;
+    if (!aligned(dh, es) || !aligned(dgate, os) || !aligned(dup, os) || !aligned(h, os) || !aligned(codes, 16)) return GG_ERR_MISALIGNED;
+    const Span ds = dense(dh, M * N * es), cs = dense(codes, 2 * M * N), ss = dense(scale, M * N / 16);
+    const Span g{dgate, M, N * os, (uint64_t)stride * os}, u{dup, M, N * os, (uint64_t)stride * os}, hs = dense(h, M * N * os);
+    if (meets(g, cs, ss, u, hs) || meets(u, cs, ss, hs) || meets(hs, cs, ss)) return GG_ERR_UNSUPPORTED;
+    // an element of dh is read by the lane that writes its place
+    const bool same = in_dtype == out_dtype;
+    if ((overlap(g, ds) && !(same && dgate == dh && stride == n)) || (overlap(u, ds) && !(same && dup == dh && stride == n)) ||
+        (overlap(hs, ds) && !(same && h == dh)))
+        return GG_ERR_UNSUPPORTED;
+    gg::GatedActGradArgs a{};
+    a.dh = dh; a.codes = codes; a.scale = scale; a.dgate = dgate; a.dup = dup; a.h = h; a.m = m; a.n = n; a.stride = stride;
+    a.bf16 = in_dtype == GG_DT_BF16; a.out_bf16 = out_dtype == GG_DT_BF16; a.gelu = act == GG_ACT_GELU_TANH;
+    return launched(gg::launch_gated_act_grad(a, (hipStream_t)stream));
+}
+
+gg_status ragged_dot_k_mxfp8(const void* lhs, const uint8_t* lhs_scale, const void* dout, const int32_t* group_sizes, void* out,
+                             int64_t m, int64_t k, int64_t n, int32_t g, gg_dtype out_dtype, float alpha, float beta,
+                             void* workspace, size_t workspace_bytes, void* stream) {
+    gg_status st = check_common(m, k, n, g, group_sizes, workspace, workspace_bytes, kHeader);
+    if (st != GG_OK) return st;
+    if (!floats(out_dtype)) return GG_ERR_BAD_DTYPE;
+    if (k % 32 != 0) return GG_ERR_UNSUPPORTED;
+    if ((m * k > 0 && (!lhs || !lhs_scale)) || (m * n > 0 && !dout) || (k * n > 0 && !out)) return GG_ERR_NULL_PTR;
+    if (!aligned(lhs, 16) || !aligned(dout, 2) || !aligned(out, elem_bytes(out_dtype))) return GG_ERR_MISALIGNED;
+    int cus;
+    if (device_cus(&cus) != 0) return GG_ERR_HIP;
+    const int64_t bound = (int64_t)g * cdiv64(k, 256) * cdiv64(n, 256);
+    if (!fits_i32(bound)) return GG_ERR_BAD_SHAPE;
+    gg::KmxParams p{};
+    p.lhs = (const uint8_t*)lhs; p.lhs_scale = lhs_scale; p.dout = (const uint16_t*)dout; p.group_sizes = group_sizes; p.out = out;
+    p.status = (uint32_t*)workspace; p.m = (int)m; p.k = (int)k; p.n = (int)n; p.g = g; p.out_f32 = out_dtype == GG_DT_F32;
+    p.alpha = alpha; p.beta = beta;
+    return gg::launch_ragged_k_mx(p, persistent_grid(bound, 1, cus), (hipStream_t)stream) == hipSuccess ? GG_OK : GG_ERR_HIP;
+}
+
+gg_status ragged_lora(const void* x, const void* a, const void* b, const int32_t* group_sizes, const int32_t* row_group,
+                      const float* scaling, const void* base, void* out, float* v, int64_t m, int64_t k, int64_t n, int32_t r,
+                      int32_t g, int64_t x_stride, int64_t base_stride, int64_t out_stride, gg_dtype dtype, gg_dtype out_dtype,
+                      void* workspace, size_t workspace_bytes, void* stream) {
+    if (!group_sizes == !row_group && m > 0) return group_sizes ? GG_ERR_UNSUPPORTED : GG_ERR_NULL_PTR;
+    if (!workspace) return GG_ERR_NULL_PTR;
+    if (m < 0 || k < 0 || n < 0 || g < 1 || g > GG_MAX_GROUPS || !fits_i32(m) || !fits_i32(k) || !fits_i32(n) || r < 1 ||
+        r > GG_MAX_RANK || x_stride < k || (base && base_stride < n) || out_stride < n || x_stride > (int64_t(1) << 31) ||
+        base_stride > (int64_t(1) << 31) || out_stride > (int64_t(1) << 31))
+        return GG_ERR_BAD_SHAPE;
+    if (!floats(dtype) || !floats(out_dtype)) return GG_ERR_BAD_DTYPE;
+    if ((m * k > 0 && !x) || (m > 0 && k > 0 && !a) || (m > 0 && n > 0 && (!b || !out))) return GG_ERR_NULL_PTR;
+    const uint64_t es = elem_bytes(dtype), os = elem_bytes(out_dtype), M = (uint64_t)m;
+    if (!aligned(x, es) || !aligned(a, es) || !aligned(b, es) || !aligned(group_sizes, 4) || !aligned(row_group, 4) ||
+        !aligned(scaling, 4) || !aligned(base, os) || !aligned(out, os) || !aligned(v, 4) || !aligned(workspace, 16))
+        return GG_ERR_MISALIGNED;
+    const size_t need = gg_workspace_bytes(GG_OP_LORA, m, k, n, g, r, dtype);
+    if (workspace_bytes < need) return GG_ERR_WORKSPACE_TOO_SMALL;
+    if (m == 0) return GG_OK;
+    const Span xs{x, M, (uint64_t)k * es, (uint64_t)x_stride * es}, as = dense(a, (uint64_t)g * r * k * es),
+               bs = dense(b, (uint64_t)g * n * r * es), ids = group_sizes ? dense(group_sizes, 4ull * g) : dense(row_group, 4 * M),
+               sc = dense(scaling, 4ull * g), bas{base, M, (uint64_t)n * os, (uint64_t)base_stride * os},
+               outs{out, M, (uint64_t)n * os, (uint64_t)out_stride * os}, vs = dense(v, 4 * M * r), wss = dense(workspace, need);
+    const bool in_place = base == out && base_stride == out_stride;
+    if (meets(outs, xs, as, bs, ids, sc, vs, wss) || (!in_place && meets(outs, bas)) || meets(vs, xs, as, bs, ids, sc, bas, wss) ||
+        meets(wss, xs, as, bs, ids, sc, bas))
+        return GG_ERR_UNSUPPORTED;
+    gg::lora::Rows rows{};
+    rows.group_sizes = group_sizes; rows.row_group = row_group; rows.status = (uint32_t*)workspace; rows.m = (int)m; rows.g = g;
+    gg::lora_rows(rows);
+    const int splits = gg::lora_splits(m, k);
+    float* t = splits == 1 && v ? v : (float*)((char*)workspace + kHeader);
+    gg::lora::Shrink sh{rows, x, a, t, x_stride, (int)k, r, splits};
+    hipError_t e = gg::launch_lora_shrink(sh, dtype == GG_DT_BF16, (hipStream_t)stream);
+    if (e != hipSuccess) return launched(e);
+    rows.status = nullptr;
+    gg::lora::Expand ex{rows, t, b, scaling, base, out, v, base_stride, out_stride, (int)n, r, splits, 0, 0};
+    return launched(gg::launch_lora_expand(ex, dtype == GG_DT_BF16, out_dtype == GG_DT_BF16, (hipStream_t)stream));
+}
+
+gg_status ragged_lora_grad(const void* x, const uint8_t* x_scale, const float* v, const void* dout, const void* a, const void* b,
+                           const int32_t* group_sizes, const float* scaling, const void* dbase, void* dx, void* da, void* db,
+                           int64_t m, int64_t k, int64_t n, int32_t r, int32_t g, gg_dtype x_dtype, gg_dtype dtype,
+                           gg_dtype grad_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+    if (!group_sizes || !workspace) return GG_ERR_NULL_PTR;
+    gg_status st = check_shape(m, k, n, g, group_sizes);
+    if (st != GG_OK) return st;
+    if (r < 1 || r > GG_MAX_RANK) return GG_ERR_BAD_SHAPE;
+    const bool e4m3 = x_dtype == GG_DT_E4M3;
+    if (!floats(dtype) || !floats(grad_dtype) || (e4m3 ? dtype != GG_DT_BF16 : x_dtype != dtype)) return GG_ERR_BAD_DTYPE;
+    if (!e4m3 && x_scale) return GG_ERR_BAD_DTYPE;
+    if (e4m3 && k % 32 != 0) return GG_ERR_UNSUPPORTED;
+    if ((m * k > 0 && (!x || (e4m3 && !x_scale))) || (m > 0 && !v) || (m * n > 0 && !dout) || (k > 0 && (!a || !da)) ||
+        (n > 0 && (!b || !db)) || (dbase && !dx))
+        return GG_ERR_NULL_PTR;
+    const uint64_t es = elem_bytes(dtype), gs = elem_bytes(grad_dtype), xb = elem_bytes(x_dtype), M = (uint64_t)m, K = (uint64_t)k,
+                   N = (uint64_t)n, G = (uint64_t)g * r;
+    if (!aligned(x, e4m3 ? 16 : es) || !aligned(v, 4) || !aligned(dout, es) || !aligned(a, es) || !aligned(b, es) ||
+        !aligned(scaling, 4) || !aligned(dbase, es) || !aligned(dx, es) || !aligned(da, gs) || !aligned(db, gs) || !aligned(workspace, 16))
+        return GG_ERR_MISALIGNED;
+    const size_t need = gg_workspace_bytes(GG_OP_LORA_GRAD, m, k, n, g, r, dtype);
+    if (workspace_bytes < need) return GG_ERR_WORKSPACE_TOO_SMALL;
+    const Span xs = dense(x, M * K * xb), xss = dense(x_scale, M * K / 32), vs = dense(v, 4 * M * r), dos = dense(dout, M * N * es),
+               as = dense(a, G * K * es), bs = dense(b, G * N * es), ids = dense(group_sizes, 4ull * g), sc = dense(scaling, 4ull * g),
+               dbs = dense(dbase, M * K * es), dxs = dense(dx, M * K * es), das = dense(da, G * K * gs), dbw = dense(db, G * N * gs),
+               wss = dense(workspace, need);
+    auto inputs = [&](const Span& o) { return meets(o, xs, xss, vs, dos, as, bs, ids, sc); };
+    if (inputs(dxs) || inputs(das) || inputs(dbw) || inputs(wss) || (dbase != dx && meets(dxs, dbs)) || meets(das, dbs, dxs, dbw, wss) ||
+        meets(dbw, dbs, dxs, wss) || meets(wss, dbs, dxs))
+        return GG_ERR_UNSUPPORTED;
+    const bool bf16 = dtype == GG_DT_BF16;
+    hipStream_t s = (hipStream_t)stream;
+    char* ws = (char*)workspace + kHeader;
+    const LoraGradLayout w = lora_grad_layout(m, k, n, r, g, dtype);
+    const int splits = gg::lora_splits(m, n);
+    float* t = (float*)(ws + w.t);
+    float* u = (float*)(ws + w.u);
+    gg::lora::Rows rows{};
+    rows.group_sizes = group_sizes; rows.m = (int)m; rows.g = g;
+    gg::lora_rows(rows);
+    hipError_t e = gg::launch_lora_turn(b, ws + w.bt, bf16, g, (int)n, r, s);
+    if (e == hipSuccess && dx) e = gg::launch_lora_turn(a, ws + w.at, bf16, g, r, (int)k, s);
+    if (e != hipSuccess) return launched(e);
+    gg::lora::Shrink sh{rows, dout, ws + w.bt, t, n, (int)n, r, splits};
+    e = gg::launch_lora_shrink(sh, bf16, s);
+    if (e != hipSuccess) return launched(e);
+    if (dx || splits > 1) {   // without dx only the sum of the splits
+        gg::lora::Expand ex{rows, t, ws + w.at, scaling, dbase, dx, splits > 1 ? u : nullptr, k, k, dx ? (int)k : 0, r, splits, 0, 0};
+        e = gg::launch_lora_expand(ex, bf16, bf16, s);
+        if (e != hipSuccess) return launched(e);
+    }
+    gg::lora::Outer o{};
+    o.group_sizes = group_sizes; o.status = (uint32_t*)workspace; o.x = x; o.x_scale = e4m3 ? x_scale : nullptr; o.dout = dout;
+    o.u = u; o.v = v; o.scaling = scaling; o.parts = (float*)(ws + w.parts); o.da = da; o.db = db;
+    o.m = (int)m; o.k = (int)k; o.n = (int)n; o.r = r; o.g = g; o.chunk = gg::lora_chunk(m, k, n); o.grads_bf16 = grad_dtype == GG_DT_BF16;
+    return launched(gg::launch_lora_outer(o, bf16, s));
 }
 
 gg_status gg_schedule(const int32_t* group_sizes, int64_t m, int64_t n, int32_t g, int32_t block_m, int32_t block_n,

@@ -112,6 +112,99 @@ hipError_t launch_fp4_quantize_weights(const void* w, bool bf16, int g, int64_t 
 hipError_t launch_fp4_dequantize(const uint8_t* codes, const uint8_t* scale, int g, int64_t n, int64_t k, void* out,
                                  bool out_bf16, hipStream_t s);
 
+// MXFP8 rows (e4m3 codes [rows, k], E8M0 scales [rows, k/32]) and the gated unit that keeps its inputs so; up to
+// 2^31 - 1 eights of elements a call.
+hipError_t launch_fp8_quantize(const void* x, bool bf16, int64_t rows, int64_t k, int64_t stride, uint8_t* codes, uint8_t* scale,
+                               hipStream_t s);
+hipError_t launch_fp8_dequantize(const uint8_t* codes, const uint8_t* scale, int64_t rows, int64_t k, void* out, bool out_bf16,
+                                 hipStream_t s);
+struct GatedActArgs {
+    const void* gate;              // [m, n], rows `stride` elements apart
+    const void* up;                // [m, n], the same stride
+    void* h;                       // [m, n]
+    uint8_t* codes;                // [m, 2 n]
+    uint8_t* scale;                // [m, 2 n / 32]
+    int64_t m, n, stride;
+    bool bf16, out_bf16, gelu;
+};
+hipError_t launch_gated_act(const GatedActArgs& a, hipStream_t s);
+struct GatedActGradArgs {
+    const void* dh;                // [m, n]
+    const uint8_t* codes;          // [m, 2 n]
+    const uint8_t* scale;          // [m, 2 n / 32]
+    void* dgate;                   // [m, n], rows `stride` elements apart
+    void* dup;                     // [m, n], the same stride
+    void* h;                       // [m, n] or NULL
+    int64_t m, n, stride;
+    bool bf16, out_bf16, gelu;
+};
+hipError_t launch_gated_act_grad(const GatedActGradArgs& a, hipStream_t s);
+
+struct KmxParams {                 // ragged_dot_k_mxfp8
+    const uint8_t* lhs;            // [m, k] e4m3
+    const uint8_t* lhs_scale;      // [m, k/32]
+    const uint16_t* dout;          // [m, n] bf16
+    const int32_t* group_sizes;
+    void* out;                     // [g, k, n]
+    uint32_t* status;
+    int m, k, n, g;
+    int out_f32;
+    float alpha, beta;
+};
+hipError_t launch_ragged_k_mx(const KmxParams& p, int grid, hipStream_t s);   // 256 x 256 tiles
+
+// Low-rank adapters.
+constexpr int kMaxRank = 256;
+namespace lora {
+struct Rows {                      // which adapter each row has
+    const int32_t* group_sizes;    // [g]: sorted rows; or NULL and
+    const int32_t* row_group;      // [m]: any order, outside [0, g): none
+    uint32_t* status;              // written by the first workgroup, or NULL
+    int m, g;
+    int chunk, slots;              // any order: rows a chunk, adapters (or rows) a chunk is split by (lora_rows)
+};
+struct Shrink {                    // t[s] = x . w[h]^T over part s of k
+    Rows rows;
+    const void* x;                 // [m, k], rows `stride` elements apart
+    const void* w;                 // [g, r, k]
+    float* t;                      // [splits, m, r]
+    int64_t stride;
+    int k, r, splits;
+};
+struct Expand {                    // out = base + scaling[h] (sum of t) . w[h]^T
+    Rows rows;
+    const float* t;                // [splits, m, r]
+    const void* w;                 // [g, n, r]
+    const float* scaling;          // [g] or NULL
+    const void* base;              // [m, n], or NULL: 0
+    void* out;                     // [m, n]
+    float* v;                      // [m, r] or NULL: the sum of t, 0 for rows without an adapter
+    int64_t base_stride, out_stride;
+    int n, r, splits, cols, col_tiles;
+};
+struct Outer {                     // da[h] = scaling[h] sum u^T x, db[h] = scaling[h] sum dout^T v
+    const int32_t* group_sizes;
+    uint32_t* status;
+    const void* x;                 // [m, k], e4m3 with x_scale
+    const uint8_t* x_scale;        // [m, k/32] or NULL
+    const void* dout;              // [m, n]
+    const float* u;                // [m, r]
+    const float* v;                // [m, r]
+    const float* scaling;
+    float* parts;                  // [2 ceil(m / chunk), (k + n) r]
+    void* da;                      // [g, r, k]
+    void* db;                      // [g, n, r]
+    int m, k, n, r, g, chunk, grads_bf16;
+};
+}  // namespace lora
+void lora_rows(lora::Rows& r);
+int lora_splits(int64_t m, int64_t k);
+int lora_chunk(int64_t m, int64_t k, int64_t n);
+hipError_t launch_lora_shrink(const lora::Shrink& p, bool bf16, hipStream_t s);
+hipError_t launch_lora_expand(const lora::Expand& p, bool bf16, bool out_bf16, hipStream_t s);
+hipError_t launch_lora_turn(const void* a, void* at, bool bf16, int g, int rows, int cols, hipStream_t s);
+hipError_t launch_lora_outer(const lora::Outer& p, bool bf16, hipStream_t s);
+
 // MoE permute / un-permute.
 constexpr int kMaxChunks = 64;   // upper bound on the permute's histogram / rank workgroups
 struct PermuteGeometry { int chunk, nblk; };   // copies per chunk, number of chunks

@@ -43,8 +43,8 @@
 extern "C" {
 #endif
 
-/* 5: the calls up to moe_unpermute.  The MXFP4 calls, GG_DT_E2M1, the gradients of permute and un-permute and
- * gg_mxfp4_kernel were added under the same number: they change no earlier call, and a caller that has to know
+/* 5: the calls up to moe_unpermute.  The MXFP4 calls, GG_DT_E2M1, the gradients of permute and un-permute,
+ * gg_mxfp4_kernel, the 8-bit activation checkpoints and the low-rank adapters were added under the same number: they change no earlier call, and a caller that has to know
  * whether a library holds them looks for the symbols. */
 #define GG_ABI_VERSION 5
 
@@ -80,6 +80,8 @@ typedef enum {
     GG_OP_PADDED_M = 2,            /* padded_dot, non-contracting form                      */
     GG_OP_PADDED_K = 3,            /* padded_dot, contracting form                          */
     GG_OP_PERMUTE = 4,             /* moe_permute (m = tokens * top_k copies)               */
+    GG_OP_LORA = 5,                /* ragged_lora (capacity = r)                            */
+    GG_OP_LORA_GRAD = 6,           /* ragged_lora_grad (capacity = r; in_dtype: dout's)     */
     GG_OP_RANGE_MIN = INT32_MIN, GG_OP_RANGE_MAX = INT32_MAX
 } gg_op;
 
@@ -98,8 +100,13 @@ typedef enum {
 /* Largest group count any call accepts. */
 #define GG_MAX_GROUPS 1024
 
+/* Largest rank of an adapter. */
+#define GG_MAX_RANK 256
+
 /* Workspace bytes a call needs.  Tiny (a few hundred bytes) for the ragged calls; for
- * padded_dot it holds the padded operands and result ([g, capacity, .] buffers).
+ * padded_dot it holds the padded operands and result ([g, capacity, .] buffers), for the adapters
+ * partial products of rank width, and for their gradients also the weights with their axes swapped
+ * and partial weight gradients.
  * in_dtype selects the element size of the padded buffers.  Returns 0 on bad arguments. */
 size_t gg_workspace_bytes(gg_op op, int64_t m, int64_t k, int64_t n, int32_t g, int64_t capacity,
                           gg_dtype in_dtype);
@@ -210,6 +217,91 @@ typedef enum {
     GG_FP4_TILE = 2                /* long groups                                           */
 } gg_fp4_kernel;
 int32_t gg_mxfp4_kernel(int64_t m, int64_t k, int64_t n, int32_t g, int32_t cus);
+
+/* MXFP8 rows, the 8-bit activation checkpoints of a training step -- codes [rows, k] OCP e4m3 and scales
+ * [rows, k/32] E8M0 bytes (value e4m3 * 2^(byte - 127), 255 is NaN), k % 32 == 0: the layout that ragged_dot_m
+ * and moe_permute take.  Codes are 16-byte aligned.  The calls of this group take up to 2^34 - 8 elements
+ * of a matrix (GG_ERR_BAD_SHAPE past that) and need no workspace.
+ *
+ * mxfp8_quantize -- x [rows, k] (fp32 or bf16, rows x_stride >= k elements apart).  Per block of 32 the scale byte is
+ * the smallest (0 at least) with which no value passes 448, so nothing is clipped: max(E - 8 + c, 0) with E the biased
+ * fp32 exponent of the largest magnitude and c = 1 where that magnitude is over 1.75 of its power of two.  255 where
+ * the block holds an infinity or a NaN (all its values read as NaN).  Codes are rounded to nearest, ties to even.
+ * Every byte of codes and scale is written. */
+gg_status mxfp8_quantize(const void* x, uint8_t* codes, uint8_t* scale, int64_t rows, int64_t k, int64_t x_stride,
+                         gg_dtype in_dtype, void* stream);
+
+/* mxfp8_dequantize -- the values, as out [rows, k] bf16 or fp32.  Exact in both, but for values below the
+ * smallest normal number (which may be 0) and values past the largest finite one (infinite). */
+gg_status mxfp8_dequantize(const uint8_t* codes, const uint8_t* scale, void* out, int64_t rows, int64_t k,
+                           gg_dtype out_dtype, void* stream);
+
+/* gated_act_mxfp8 -- the gated unit of an expert block in training (ragged_dot_m_gated computes the same from its
+ * operands, and keeps nothing):
+ *   h[i, :] = act(gate[i, :]) * up[i, :]
+ *   codes [m, 2n], scale [m, 2n/32]: gate | up of every row as mxfp8_quantize gives them
+ *   gate, up [m, n] in_dtype (fp32 or bf16), rows `stride` >= n elements apart (two halves of one matrix, or two
+ *     matrices); h [m, n] out_dtype (fp32 or bf16).  n % 32 == 0.
+ * An infinite gate has the value of x * sigmoid(.) there (-infinity gives NaN).  h and the codes may not lie in gate or up. */
+gg_status gated_act_mxfp8(const void* gate, const void* up, void* h, uint8_t* codes, uint8_t* scale, int64_t m,
+                          int64_t n, int64_t stride, gg_activation act, gg_dtype in_dtype, gg_dtype out_dtype,
+                          void* stream);
+
+/* gated_act_mxfp8_grad -- its backward pass from the checkpoint (gate and up are the values of codes and scale):
+ *   dgate = dh * up * act'(gate),  dup = dh * act(gate),  h = act(gate) * up (for the next layer's weight gradient)
+ *   dh [m, n] in_dtype (fp32 or bf16); dgate, dup [m, n] out_dtype, rows `stride` >= n elements apart; h [m, n]
+ *   out_dtype, or NULL.  fp32 arithmetic, one rounding.  The outputs may not lie in an input or in each other, but
+ *   where the types are the same one of dgate, dup (of stride n) and h may be dh. */
+gg_status gated_act_mxfp8_grad(const void* dh, const uint8_t* codes, const uint8_t* scale, void* dgate, void* dup,
+                               void* h, int64_t m, int64_t n, int64_t stride, gg_activation act, gg_dtype in_dtype,
+                               gg_dtype out_dtype, void* stream);
+
+/* ragged_dot_k_mxfp8 -- ragged_dot_k_epilogue from rows kept in MXFP8:
+ *   out[h] = alpha * value(lhs[rows of h, :])^T . dout[rows of h, :] + beta * out[h]
+ *   lhs [m, k] e4m3, lhs_scale [m, k/32], dout [m, n] bf16, out [g, k, n] fp32 or bf16; every element written (an
+ *   empty group gives beta * out[h]).
+ * Any n; k % 32 == 0 (GG_ERR_UNSUPPORTED).  lhs 16-byte aligned.  Workspace, status and errors as ragged_dot_k. */
+gg_status ragged_dot_k_mxfp8(const void* lhs, const uint8_t* lhs_scale, const void* dout, const int32_t* group_sizes,
+                             void* out, int64_t m, int64_t k, int64_t n, int32_t g, gg_dtype out_dtype, float alpha,
+                             float beta, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ragged_lora -- low-rank adapters of many requests (or experts) at once, beside a shared projection:
+ *   out[i, :] = base[i, :] + scaling[h] * (x[i, :] . a[h]^T) . b[h]^T     where row i has adapter h,
+ *   out[i, :] = base[i, :]                                                where it has none.
+ *   x [m, k] dtype, rows x_stride >= k elements apart; a [g, r, k], b [g, n, r] dtype (fp32 or bf16), as a pair of
+ *     linear layers stores them; 1 <= r <= GG_MAX_RANK
+ *   group_sizes [g]: rows sorted by adapter, rows past the last group have none; or
+ *   row_group [m] int32: rows in any order, a value outside [0, g) is none (exactly one of the two is given)
+ *   scaling [g] fp32, or NULL for 1
+ *   base [m, n] out_dtype (fp32 or bf16): the shared projection's result, or NULL for 0; out [m, n]; rows base_stride and
+ *     out_stride >= n elements apart.  out may be base itself (same stride): then rows without an adapter stay as they
+ *     are.  Other overlaps of an output with an input or another output return GG_ERR_UNSUPPORTED.
+ *   v [m, r] fp32: receives x . a[h]^T (0 for rows without an adapter), which ragged_lora_grad takes; or NULL
+ * x . a^T and the sum are fp32 (bf16 operands: x . a^T enters the second product as two bf16 values, 16 bits of fraction),
+ * one rounding.  Rows of other adapters never meet a row's values, whatever they hold.  Results do not depend on the
+ * launch, but rows sorted and rows in any order, and calls of other m, may add in other orders.
+ * Workspace: gg_workspace_bytes(GG_OP_LORA, m, k, n, g, r, dtype); status and errors as ragged_dot_m (with row_group the
+ * status is 0). */
+gg_status ragged_lora(const void* x, const void* a, const void* b, const int32_t* group_sizes, const int32_t* row_group,
+                      const float* scaling, const void* base, void* out, float* v, int64_t m, int64_t k, int64_t n,
+                      int32_t r, int32_t g, int64_t x_stride, int64_t base_stride, int64_t out_stride, gg_dtype dtype,
+                      gg_dtype out_dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ragged_lora_grad -- the gradients of ragged_lora over rows sorted by adapter:
+ *   u[i, :] = scaling[h] * dout[i, :] . b[h];   dx[i, :] = dbase[i, :] + u[i, :] . a[h]   (dbase: no adapter)
+ *   da[h] = sum over its rows of u[i, :]^T x[i, :],   db[h] = scaling[h] * sum of dout[i, :]^T v[i, :]
+ *   x [m, k] x_dtype: dtype, or (with dtype bf16) e4m3 with x_scale [m, k/32], a checkpoint of mxfp8_quantize
+ *   v [m, r] fp32, as ragged_lora wrote it; dout [m, n], a [g, r, k], b [g, n, r], dbase and dx [m, k]: dtype
+ *   dbase: the shared projection's gradient, or NULL for 0; it may be dx itself (rows without an adapter then stay as
+ *     they are); dx NULL: not computed
+ *   da [g, r, k], db [g, n, r] grad_dtype (fp32 or bf16); every element written, 0 for adapters without rows.  All dense.
+ * Sums are fp32, in an order that depends on sizes alone; no atomics.  bf16 operands meet u and v as two bf16 values
+ * each (16 bits of fraction), three in da and db that leave in fp32.  Other overlaps than dx = dbase return
+ * GG_ERR_UNSUPPORTED.  Workspace: gg_workspace_bytes(GG_OP_LORA_GRAD, m, k, n, g, r, dtype). */
+gg_status ragged_lora_grad(const void* x, const uint8_t* x_scale, const float* v, const void* dout, const void* a,
+                           const void* b, const int32_t* group_sizes, const float* scaling, const void* dbase, void* dx,
+                           void* da, void* db, int64_t m, int64_t k, int64_t n, int32_t r, int32_t g, gg_dtype x_dtype,
+                           gg_dtype dtype, gg_dtype grad_dtype, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ragged_dot_m_epilogue -- ragged_dot_m with a fused epilogue, in place on out:
  *   out[r, :] = alpha * (lhs[r, :] . rhs[h]) + bias[h, :] + beta * out[r, :]

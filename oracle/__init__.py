@@ -436,6 +436,100 @@ def moe_unpermute_grad(dout, y, copy_to_sorted, sorted_to_copy, weights):
     return dy, dw.reshape(T, K), mag.reshape(T, K)
 
 
+# ---------------------------------------------------------------------------------------
+# 8-bit activation checkpoints (MXFP8 rows: e4m3 codes [rows, k], one E8M0 byte per 32 along k) and the gated unit
+
+_c = np.arange(127)
+E4M3 = np.where(_c < 8, _c * 2.0 ** -9, (8 + _c % 8) * 2.0 ** (_c // 8 - 10.0))   # the finite magnitudes, by code
+
+
+def mxfp8_values(codes, scale):
+    """fp64 values [rows, k]; a scale byte of 255 makes its 32 values NaN, and so does the code 127 (either sign)."""
+    c = np.asarray(codes, dtype=np.uint8).astype(np.int64)
+    v = np.where(c & 128, -1.0, 1.0) * np.append(E4M3, np.nan)[c & 127]
+    s = np.asarray(scale, dtype=np.uint8).astype(np.float64)
+    return v * np.repeat(np.where(s == 255, np.nan, 2.0 ** (s - 127)), 32, axis=-1)
+
+
+def mxfp8_quantize(x):
+    """fp64 rows [rows, k] to (codes, scale bytes): per block the smallest exponent E >= -127 with max|x| <= 448 * 2^E,
+    byte E + 127 (255 for a block with an infinity or a NaN, whose codes are returned as 0); codes the nearest e4m3 value
+    to x / 2^E, a tie to the even code."""
+    x = np.asarray(x, dtype=np.float64)
+    b = x.reshape(x.shape[0], -1, 32)
+    ok = np.isfinite(b).all(axis=-1)
+    b = np.where(ok[..., None], b, 0.0)
+    amax = np.abs(b).max(axis=-1) if b.size else np.zeros(b.shape[:-1])
+    _, e = np.frexp(amax)                                    # amax = f * 2^e with f in [0.5, 1): 448 = 0.875 * 2^9
+    f = np.where(amax > 0, np.ldexp(amax, -e), 0.5)
+    e = np.where(amax > 0, np.maximum(e - 9 + (f > 0.875), -127), -127)
+    a = np.ldexp(np.abs(b), -e[..., None])
+    mid = (E4M3[:-1] + E4M3[1:]) / 2
+    code = np.searchsorted(mid, a, side="left")              # midpoints below a
+    tie = (code < 126) & (a == mid[np.minimum(code, 125)])
+    code = np.where(tie & (code % 2 == 1), code + 1, code)
+    code |= np.where(np.signbit(b), 128, 0)
+    return code.reshape(x.shape).astype(np.uint8), np.where(ok, e + 127, 255).astype(np.uint8)
+
+
+def gate_and_slope(x, act):
+    """act(x) and act'(x) in fp64, through the logistic function p(y) (0.5 (1 + tanh z) is p(2 z)), taken from the
+    exponential of -|y|, so that neither tail cancels."""
+    x = np.asarray(x, dtype=np.float64)
+    c = 2 * np.sqrt(2 / np.pi)
+    y, dy = (x, 1.0) if act == "silu" else (c * (x + 0.044715 * x ** 3), c * (1 + 3 * 0.044715 * x * x))
+    e = np.exp(-np.abs(y))
+    p, q = np.where(y >= 0, 1, e) / (1 + e), np.where(y >= 0, e, 1) / (1 + e)
+    return x * p, p + x * p * q * dy
+
+
+def gated_act_grad(dh, gate, up, act):
+    """fp64 (dgate, dup, h)."""
+    f, d = gate_and_slope(gate, act)
+    return dh * up * d, dh * f, f * up
+
+
+def row_groups(group_sizes, m):
+    """Group of every row, -1 past the last one; sizes clamped as in the ragged products."""
+    h, at = np.full(m, -1, dtype=np.int64), 0
+    for i, s in enumerate(np.asarray(group_sizes, dtype=np.int64)):
+        s = min(max(int(s), 0), m - at)
+        h[at:at + s] = i
+        at += s
+    return h
+
+
+# ---------------------------------------------------------------------------------------
+# low-rank adapters
+
+
+def ragged_lora(x, a, b, rows, scaling=None, base=None):
+    """fp64 (out, v) of x [m, k], a [g, r, k], b [g, n, r] and `rows` [m], the adapter of every row (outside [0, g): none):
+    v[i] = x[i] . a[h]^T, out[i] = base[i] + scaling[h] * v[i] . b[h]^T; rows without one have v 0 and out base."""
+    (m, _), (g, n, r) = x.shape, b.shape
+    out = np.zeros((m, n)) if base is None else np.array(base, dtype=np.float64)
+    v = np.zeros((m, r))
+    for i, h in enumerate(rows):
+        if 0 <= h < g:
+            v[i] = a[h] @ x[i]
+            out[i] = out[i] + (1.0 if scaling is None else float(scaling[h])) * (b[h] @ v[i])
+    return out, v
+
+
+def ragged_lora_grad(x, v, dout, a, b, rows, scaling=None, dbase=None):
+    """fp64 (dx, da, db) of the sum of dout * ragged_lora(...)'s out, with v as given for db."""
+    dx = np.zeros(x.shape) if dbase is None else np.array(dbase, dtype=np.float64)
+    da, db = np.zeros(a.shape), np.zeros(b.shape)
+    for i, h in enumerate(rows):
+        if 0 <= h < a.shape[0]:
+            s = 1.0 if scaling is None else float(scaling[h])
+            u = s * (dout[i] @ b[h])
+            dx[i] += u @ a[h]
+            da[h] += np.outer(u, x[i])
+            db[h] += s * np.outer(dout[i], v[i])
+    return dx, da, db
+
+
 def num_threads():
     return lib().oracle_num_threads()
 
