@@ -5,6 +5,7 @@ and the current stream; there is no CPU fallback: if the library is missing or a
 fails, an exception is raised.
 """
 import ctypes
+import functools
 import os
 
 import torch
@@ -623,6 +624,28 @@ def ragged_dot_m_mxfp4(lhs, rhs, group_sizes, lhs_scale, rhs_scale, out=None, ou
     return out
 
 
+# The calls below run in a few microseconds for few rows, where the host's time is what counts: what most calls pass
+# is found right by _fits, and _tensor names what is wrong.
+def _fits(t, index, shape, dtype):
+    return (torch.is_tensor(t) and t.dtype is dtype and t.is_cuda and t.get_device() == index and t.shape == shape
+            and t.is_contiguous())
+
+
+@functools.lru_cache(maxsize=1024)
+def _bytes(op, m, k, n, g, capacity, in_dtype):
+    """workspace_bytes, which depends on its arguments alone."""
+    return workspace_bytes(op, m, k, n, g, capacity, in_dtype)
+
+
+def _scratch(op, m, k, n, g, capacity, in_dtype, dev, workspace):
+    if workspace is not None:
+        return _workspace(op, m, k, n, g, capacity, in_dtype, dev, workspace)
+    need = _bytes(op, m, k, n, g, capacity, in_dtype)
+    if need == 0:
+        raise ValueError("bad arguments for the workspace size")
+    return torch.empty(need, dtype=torch.uint8, device=dev)
+
+
 # ---------------------------------------------------------------------------------------
 # 8-bit activation checkpoints: codes (torch.float8_e4m3fn, or uint8 bytes) and E8M0 scales (uint8 [rows, k/32])
 
@@ -631,6 +654,9 @@ _E4M3 = (torch.float8_e4m3fn, torch.uint8)
 
 def _rows(t, name, device, shape=None, dtype=None, dtypes=None):
     """A matrix with unit column stride and rows that do not overlap; its row stride."""
+    if (device is not None and dtype is not None and _fits(t, device.index, shape, dtype)) or (
+            device is None and torch.is_tensor(t) and t.is_cuda and t.dtype in dtypes and t.dim() == 2 and t.is_contiguous()):
+        return t.shape[1]
     _tensor(t, name, device, shape, dtype, dtypes, contiguous=False)
     if t.dim() != 2:
         raise ValueError(f"{name} must be a matrix")
@@ -654,6 +680,13 @@ def _codes8(out, rows, k, dev):
     return codes, scale
 
 
+def _checkpoint(codes, scale, dev, rows, k, name="codes", scale_name="scale"):
+    """Checks codes [rows, k] and their scales."""
+    if not (_fits(codes, dev.index, (rows, k), torch.float8_e4m3fn) and _fits(scale, dev.index, (rows, k // 32), torch.uint8)):
+        _tensor(codes, name, dev, (rows, k), dtypes=_E4M3)
+        _tensor(scale, scale_name, dev, (rows, k // 32), torch.uint8)
+
+
 def mxfp8_quantize(x, out=None):
     """Rows x [rows, k] (fp32 or bf16, k % 32 == 0, unit column stride, any row stride >= k) to MXFP8:
     (codes torch.float8_e4m3fn [rows, k], scale uint8 [rows, k/32]), one power-of-two scale per 32 elements
@@ -671,11 +704,10 @@ def mxfp8_quantize(x, out=None):
 def mxfp8_dequantize(codes, scale, out=None, out_dtype=None):
     """The values of MXFP8 rows (codes [rows, k], scale [rows, k/32]) as [rows, k]: bf16 (default) or fp32."""
     dev = codes.device
-    _tensor(codes, "codes", None, dtypes=_E4M3)
     if codes.dim() != 2 or codes.shape[1] % 32:
         raise ValueError("codes must be [rows, k] with k % 32 == 0")
     rows, k = codes.shape
-    _tensor(scale, "scale", dev, (rows, k // 32), torch.uint8)
+    _checkpoint(codes, scale, dev, rows, k)
     if out_dtype is None:
         out_dtype = out.dtype if out is not None else torch.bfloat16
     out = _out(out, "out", dev, (rows, k), out_dtype)
@@ -715,24 +747,27 @@ def gated_act_mxfp8_grad(dh, codes, scale, act="silu", out=None, out_dtype=None)
     if dh.dim() != 2 or dh.shape[1] % 32:
         raise ValueError("dh must be [m, n] with n % 32 == 0")
     m, n = dh.shape
-    _tensor(codes, "codes", dev, (m, 2 * n), dtypes=_E4M3)
-    _tensor(scale, "scale", dev, (m, 2 * n // 32), torch.uint8)
+    _checkpoint(codes, scale, dev, m, 2 * n)
     if act not in ACT:
         raise ValueError(f"act must be one of {sorted(ACT)}")
-    dgate, dup, h = out if out is not None else (None, None, None)
-    if out_dtype is None:
-        given = [t.dtype for t in (dgate, dup, h) if t is not None]
-        out_dtype = given[0] if given else dh.dtype
-    if out_dtype not in _FLOATS:
-        raise ValueError(f"out_dtype must be one of {_FLOATS}")
-    if dgate is None:
-        dgate = torch.empty((m, n), dtype=out_dtype, device=dev)
-    if dup is None:
-        dup = torch.empty((m, n), dtype=out_dtype, device=dev)
-    stride = _rows(dgate, "dgate", dev, (m, n), out_dtype)
-    if _rows(dup, "dup", dev, (m, n), out_dtype) != stride:
-        raise ValueError("dgate and dup must have one row stride")
-    h = _out(h, "h", dev, (m, n), out_dtype)
+    if out is None and out_dtype is None:
+        dgate, dup, h = torch.empty_like(dh), torch.empty_like(dh), torch.empty_like(dh)
+        out_dtype, stride = dh.dtype, n
+    else:
+        dgate, dup, h = out if out is not None else (None, None, None)
+        if out_dtype is None:
+            given = [t.dtype for t in (dgate, dup, h) if t is not None]
+            out_dtype = given[0] if given else dh.dtype
+        if out_dtype not in _FLOATS:
+            raise ValueError(f"out_dtype must be one of {_FLOATS}")
+        if dgate is None:
+            dgate = torch.empty((m, n), dtype=out_dtype, device=dev)
+        if dup is None:
+            dup = torch.empty((m, n), dtype=out_dtype, device=dev)
+        stride = _rows(dgate, "dgate", dev, (m, n), out_dtype)
+        if _rows(dup, "dup", dev, (m, n), out_dtype) != stride:
+            raise ValueError("dgate and dup must have one row stride")
+        h = _out(h, "h", dev, (m, n), out_dtype)
     _call("gated_act_mxfp8_grad", dev, dh.data_ptr(), codes.data_ptr(), scale.data_ptr(), dgate.data_ptr(), dup.data_ptr(),
           h.data_ptr(), m, n, stride, ACT[act], GG_DT[dh.dtype], GG_DT[out_dtype])
     return dgate, dup, h
@@ -742,16 +777,24 @@ def gated_act_mxfp8_grad(dh, codes, scale, act="silu", out=None, out_dtype=None)
 # low-rank adapters
 
 
-def _adapter_shapes(a, b, dtype, dev):
+def _adapters(a, b, dtype, dev):
+    """Checks a [g, r, k] and b [g, n, r]; (g, r, k, n)."""
     if a.dim() != 3 or b.dim() != 3:
         raise ValueError("a must be [g, r, k] and b [g, n, r]")
     g, r, k = a.shape
     g2, n, r2 = b.shape
     if g2 != g or r2 != r:
         raise ValueError(f"a is {tuple(a.shape)}, b {tuple(b.shape)}: [g, r, k] and [g, n, r] are expected")
-    _tensor(a, "a", dev, dtype=dtype)
-    _tensor(b, "b", dev, dtype=dtype)
+    if not (_fits(a, dev.index, (g, r, k), dtype) and _fits(b, dev.index, (g, n, r), dtype)):
+        _tensor(a, "a", dev, dtype=dtype)
+        _tensor(b, "b", dev, dtype=dtype)
     return g, r, k, n
+
+
+def _vector(t, name, dev, length, dtype):
+    if not _fits(t, dev.index, (length,), dtype):
+        _tensor(t, name, dev, (length,), dtype)
+    return t.data_ptr()
 
 
 def ragged_lora(x, a, b, group_sizes=None, base=None, row_group=None, scaling=None, v=None, out=None, out_dtype=None,
@@ -764,34 +807,31 @@ def ragged_lora(x, a, b, group_sizes=None, base=None, row_group=None, scaling=No
     [m, r] that receives x[i] . a[h]^T, which ragged_lora_grad takes."""
     dev = x.device
     x_stride = _rows(x, "x", None, dtypes=_FLOATS)
-    g, r, k, n = _adapter_shapes(a, b, x.dtype, dev)
-    m = x.shape[0]
-    if x.shape[1] != k:
-        raise ValueError(f"x has k = {x.shape[1]}, a has {k}")
+    dtype = x.dtype
+    g, r, k, n = _adapters(a, b, dtype, dev)
+    m, xk = x.shape
+    if xk != k:
+        raise ValueError(f"x has k = {xk}, a has {k}")
     if (group_sizes is None) == (row_group is None):
         raise ValueError("exactly one of group_sizes and row_group must be given")
-    if group_sizes is not None:
-        _tensor(group_sizes, "group_sizes", dev, (g,), torch.int32)
-    else:
-        _tensor(row_group, "row_group", dev, (m,), torch.int32)
-    if scaling is not None:
-        _tensor(scaling, "scaling", dev, (g,), torch.float32)
+    sizes = None if group_sizes is None else _vector(group_sizes, "group_sizes", dev, g, torch.int32)
+    ids = None if row_group is None else _vector(row_group, "row_group", dev, m, torch.int32)
+    sc = None if scaling is None else _vector(scaling, "scaling", dev, g, torch.float32)
     if v is not None:
         _tensor(v, "v", dev, (m, r), torch.float32)
-    base_stride = n
-    if base is not None:
-        base_stride = _rows(base, "base", dev, (m, n), dtypes=_FLOATS)
     if out_dtype is None:
-        out_dtype = out.dtype if out is not None else base.dtype if base is not None else x.dtype
+        out_dtype = out.dtype if out is not None else base.dtype if base is not None else dtype
     if out_dtype not in _FLOATS or (base is not None and base.dtype != out_dtype):
         raise ValueError(f"out_dtype must be fp32 or bf16 and base's, not {out_dtype}")
+    base_stride = n if base is None else _rows(base, "base", dev, (m, n), out_dtype)
+    out_stride = n
     if out is None:
         out = torch.empty((m, n), dtype=out_dtype, device=dev)
-    out_stride = _rows(out, "out", dev, (m, n), out_dtype)
-    ws = _workspace("lora", m, k, n, g, r, x.dtype, dev, workspace)
-    _call("ragged_lora", dev, x.data_ptr(), a.data_ptr(), b.data_ptr(), _p(group_sizes), _p(row_group), _p(scaling), _p(base),
-          out.data_ptr(), _p(v), m, k, n, r, g, x_stride, base_stride, out_stride, GG_DT[x.dtype], GG_DT[out_dtype],
-          ws.data_ptr(), ws.numel())
+    else:
+        out_stride = _rows(out, "out", dev, (m, n), out_dtype)
+    ws = _scratch("lora", m, k, n, g, r, dtype, dev, workspace)
+    _call("ragged_lora", dev, x.data_ptr(), a.data_ptr(), b.data_ptr(), sizes, ids, sc, _p(base), out.data_ptr(), _p(v), m, k, n, r,
+          g, x_stride, base_stride, out_stride, GG_DT[dtype], GG_DT[out_dtype], ws.data_ptr(), ws.numel())
     return out
 
 
@@ -805,44 +845,47 @@ def ragged_lora_grad(x, v, dout, a, b, group_sizes, dbase=None, scaling=None, x_
     _tensor(dout, "dout", None, dtypes=_FLOATS)
     if dout.dim() != 2 or x.dim() != 2:
         raise ValueError("x must be [m, k] and dout [m, n]")
-    g, r, k, n = _adapter_shapes(a, b, dout.dtype, dev)
-    m = dout.shape[0]
-    if dout.shape[1] != n:
-        raise ValueError(f"dout has n = {dout.shape[1]}, b has {n}")
-    if torch.is_tensor(x) and _is_e4m3(x):
-        _tensor(x, "x", dev, (m, k), dtypes=_E4M3)
+    dtype = dout.dtype
+    g, r, k, n = _adapters(a, b, dtype, dev)
+    m, dn = dout.shape
+    if dn != n:
+        raise ValueError(f"dout has n = {dn}, b has {n}")
+    if _is_e4m3(x):
         if dout.dtype != torch.bfloat16:
             raise ValueError("e4m3 rows go with bf16 gradients and weights")
         if x_scale is None or k % 32:
             raise ValueError("e4m3 rows need x_scale [m, k/32] (k % 32 == 0)")
-        _tensor(x_scale, "x_scale", dev, (m, k // 32), torch.uint8)
+        _checkpoint(x, x_scale, dev, m, k, "x", "x_scale")
     else:
-        _tensor(x, "x", dev, (m, k), dout.dtype)
+        if not _fits(x, dev.index, (m, k), dtype):
+            _tensor(x, "x", dev, (m, k), dtype)
         if x_scale is not None:
             raise ValueError("x_scale is taken only with e4m3 rows")
-    _tensor(v, "v", dev, (m, r), torch.float32)
-    _tensor(group_sizes, "group_sizes", dev, (g,), torch.int32)
-    if scaling is not None:
-        _tensor(scaling, "scaling", dev, (g,), torch.float32)
+    if not _fits(v, dev.index, (m, r), torch.float32):
+        _tensor(v, "v", dev, (m, r), torch.float32)
+    sizes = _vector(group_sizes, "group_sizes", dev, g, torch.int32)
+    sc = None if scaling is None else _vector(scaling, "scaling", dev, g, torch.float32)
     dx, da, db = out if out is not None else (None, None, None)
     if not need_dx and (dx is not None or dbase is not None):
         raise ValueError("need_dx=False takes neither dbase nor dx")
-    if dbase is not None:
-        _tensor(dbase, "dbase", dev, (m, k), dout.dtype)
+    if dbase is not None and not _fits(dbase, dev.index, (m, k), dtype):
+        _tensor(dbase, "dbase", dev, (m, k), dtype)
     if need_dx:
         if dx is None:
-            dx = torch.empty((m, k), dtype=dout.dtype, device=dev)
+            dx = torch.empty((m, k), dtype=dtype, device=dev)
         else:
-            _tensor(dx, "dx", dev, (m, k), dout.dtype)
+            _tensor(dx, "dx", dev, (m, k), dtype)
     if grad_dtype is None:
         given = [t.dtype for t in (da, db) if t is not None]
         grad_dtype = given[0] if given else torch.float32
+    if grad_dtype not in _FLOATS:
+        raise ValueError(f"grad_dtype must be one of {_FLOATS}")
     da = _out(da, "da", dev, (g, r, k), grad_dtype)
     db = _out(db, "db", dev, (g, n, r), grad_dtype)
-    ws = _workspace("lora_grad", m, k, n, g, r, dout.dtype, dev, workspace)
-    _call("ragged_lora_grad", dev, x.data_ptr(), _p(x_scale), v.data_ptr(), dout.data_ptr(), a.data_ptr(), b.data_ptr(),
-          group_sizes.data_ptr(), _p(scaling), _p(dbase), _p(dx), da.data_ptr(), db.data_ptr(), m, k, n, r, g, GG_DT[x.dtype],
-          GG_DT[dout.dtype], GG_DT[grad_dtype], ws.data_ptr(), ws.numel())
+    ws = _scratch("lora_grad", m, k, n, g, r, dtype, dev, workspace)
+    _call("ragged_lora_grad", dev, x.data_ptr(), _p(x_scale), v.data_ptr(), dout.data_ptr(), a.data_ptr(), b.data_ptr(), sizes, sc,
+          _p(dbase), _p(dx), da.data_ptr(), db.data_ptr(), m, k, n, r, g, GG_DT[x.dtype], GG_DT[dtype], GG_DT[grad_dtype],
+          ws.data_ptr(), ws.numel())
     return dx, da, db
 
 

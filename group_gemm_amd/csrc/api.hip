@@ -211,7 +211,7 @@ void* scratch_address() {
 struct LoraGradLayout { size_t bt, at, t, u, parts, bytes; };
 LoraGradLayout lora_grad_layout(int64_t m, int64_t k, int64_t n, int r, int32_t g, gg_dtype dtype) {
     const size_t es = elem_bytes(dtype), rows = align_up((size_t)m * r * 4, 256);
-    const int splits = gg::lora_splits(m, n);
+    const int splits = gg::lora_splits(m, n, r, g);
     const int64_t chunk = gg::lora_chunk(m, k, n);
     LoraGradLayout w{};
     w.bt = 0;
@@ -291,7 +291,7 @@ size_t gg_workspace_bytes(gg_op op, int64_t m, int64_t k, int64_t n, int32_t g, 
         }
         case GG_OP_LORA: {   // capacity: r
             if (capacity < 1 || capacity > GG_MAX_RANK || !fits_i32(m) || !fits_i32(k) || in == GG_DT_E4M3) return 0;
-            return kHeader + align_up((size_t)gg::lora_splits(m, k) * (size_t)m * (size_t)capacity * 4, 256);
+            return kHeader + align_up((size_t)gg::lora_splits(m, k, (int)capacity, g) * (size_t)m * (size_t)capacity * 4, 256);
         }
         case GG_OP_LORA_GRAD: {
             if (capacity < 1 || capacity > GG_MAX_RANK || !fits_i32(m) || !fits_i32(k) || !fits_i32(n) || in == GG_DT_E4M3) return 0;
@@ -767,7 +767,7 @@ gg_status ragged_lora(const void* x, const void* a, const void* b, const int32_t
     gg::lora::Rows rows{};
     rows.group_sizes = group_sizes; rows.row_group = row_group; rows.status = (uint32_t*)workspace; rows.m = (int)m; rows.g = g;
     gg::lora_rows(rows);
-    const int splits = gg::lora_splits(m, k);
+    const int splits = gg::lora_splits(m, k, r, g);
     float* t = splits == 1 && v ? v : (float*)((char*)workspace + kHeader);
     gg::lora::Shrink sh{rows, x, a, t, x_stride, (int)k, r, splits};
     hipError_t e = gg::launch_lora_shrink(sh, dtype == GG_DT_BF16, (hipStream_t)stream);
@@ -811,28 +811,28 @@ gg_status ragged_lora_grad(const void* x, const uint8_t* x_scale, const float* v
     hipStream_t s = (hipStream_t)stream;
     char* ws = (char*)workspace + kHeader;
     const LoraGradLayout w = lora_grad_layout(m, k, n, r, g, dtype);
-    const int splits = gg::lora_splits(m, n);
+    const int splits = gg::lora_splits(m, n, r, g);
     float* t = (float*)(ws + w.t);
     float* u = (float*)(ws + w.u);
     gg::lora::Rows rows{};
     rows.group_sizes = group_sizes; rows.m = (int)m; rows.g = g;
     gg::lora_rows(rows);
-    hipError_t e = gg::launch_lora_turn(b, ws + w.bt, bf16, g, (int)n, r, s);
-    if (e == hipSuccess && dx) e = gg::launch_lora_turn(a, ws + w.at, bf16, g, r, (int)k, s);
+    hipError_t e = gg::launch_lora_turn(b, ws + w.bt, (int)n, r, dx ? a : nullptr, ws + w.at, r, (int)k, bf16, g, s);
     if (e != hipSuccess) return launched(e);
     gg::lora::Shrink sh{rows, dout, ws + w.bt, t, n, (int)n, r, splits};
     e = gg::launch_lora_shrink(sh, bf16, s);
     if (e != hipSuccess) return launched(e);
-    if (dx || splits > 1) {   // without dx only the sum of the splits
-        gg::lora::Expand ex{rows, t, ws + w.at, scaling, dbase, dx, splits > 1 ? u : nullptr, k, k, dx ? (int)k : 0, r, splits, 0, 0};
-        e = gg::launch_lora_expand(ex, bf16, bf16, s);
-        if (e != hipSuccess) return launched(e);
-    }
+    gg::lora::Expand ex{rows, t, ws + w.at, scaling, dbase, dx, splits > 1 ? u : nullptr, k, k, dx ? (int)k : 0, r, splits, 0, 0};
     gg::lora::Outer o{};
     o.group_sizes = group_sizes; o.status = (uint32_t*)workspace; o.x = x; o.x_scale = e4m3 ? x_scale : nullptr; o.dout = dout;
     o.u = u; o.v = v; o.scaling = scaling; o.parts = (float*)(ws + w.parts); o.da = da; o.db = db;
     o.m = (int)m; o.k = (int)k; o.n = (int)n; o.r = r; o.g = g; o.chunk = gg::lora_chunk(m, k, n); o.grads_bf16 = grad_dtype == GG_DT_BF16;
-    return launched(gg::launch_lora_outer(o, bf16, s));
+    // With splits the expand sums them, so it goes first (without dx it does only that).  Without, the row sums read
+    // dout again, from its end, while the last-level cache still holds that.
+    if (splits > 1) e = gg::launch_lora_expand(ex, bf16, bf16, s);
+    if (e == hipSuccess) e = gg::launch_lora_outer(o, bf16, s);
+    if (e == hipSuccess && splits == 1 && dx) e = gg::launch_lora_expand(ex, bf16, bf16, s);
+    return launched(e);
 }
 
 gg_status gg_schedule(const int32_t* group_sizes, int64_t m, int64_t n, int32_t g, int32_t block_m, int32_t block_n,

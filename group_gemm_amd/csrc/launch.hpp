@@ -198,11 +198,13 @@ struct Outer {                     // da[h] = scaling[h] sum u^T x, db[h] = scal
 };
 }  // namespace lora
 void lora_rows(lora::Rows& r);
-int lora_splits(int64_t m, int64_t k);
+int lora_splits(int64_t m, int64_t k, int r, int g);
 int lora_chunk(int64_t m, int64_t k, int64_t n);
 hipError_t launch_lora_shrink(const lora::Shrink& p, bool bf16, hipStream_t s);
 hipError_t launch_lora_expand(const lora::Expand& p, bool bf16, bool out_bf16, hipStream_t s);
-hipError_t launch_lora_turn(const void* a, void* at, bool bf16, int g, int rows, int cols, hipStream_t s);
+// [g, rows, cols] -> [g, cols, rows] of a and of b (NULL: not)
+hipError_t launch_lora_turn(const void* a, void* at, int rows, int cols, const void* b, void* bt, int rows_b, int cols_b, bool bf16, int g,
+                            hipStream_t s);
 hipError_t launch_lora_outer(const lora::Outer& p, bool bf16, hipStream_t s);
 
 // MoE permute / un-permute.

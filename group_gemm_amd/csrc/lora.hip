@@ -20,13 +20,14 @@
 
 #include "common.hpp"
 #include "launch.hpp"
+#include "ring.hpp"
 
 namespace gg {
 namespace lora {
 
 constexpr int NT = 256;
 constexpr int KC = 64;           // elements of the long axis that a wave takes at a time
-constexpr int MAXCHUNK = 2048;   // rows in any order: of these many, a workgroup takes those of its adapter
+constexpr int MAXCHUNK = 1024;   // rows in any order: of these many, a workgroup takes those of its adapter
 
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -87,29 +88,60 @@ __device__ inline void split(float x, uint16_t (&out)[P]) {
 
 // Which rows a workgroup has: `rows` of adapter h (-1: rows without one), row i being first + i or list[i].
 struct RowTile { int h, rows, first; const int* list; };
-struct RowSmem {
-    union {
-        Tables tab;
-        struct { int list[MAXCHUNK]; int wave[4]; } any;
-    };
-};
+struct RowList { int list[MAXCHUNK]; int wave[4]; };
 
-// Sorted rows: tile `id` of `tm` rows each, adapters first and then the rows behind the last one's.
-__device__ inline RowTile sorted_tile(const Rows& p, int id, int tm, RowSmem& sm) {
-    int tiles, covered;
-    build_tables<NT>(p.group_sizes, p.g, p.m, tm, 1, sm.tab, &tiles, &covered);
-    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && p.status) *p.status = sm.tab.flags;
-    if (id < tiles) {
-        const int h = find_group(sm.tab.tile_off, p.g, id);
-        const int first = sm.tab.row_off[h] + (id - sm.tab.tile_off[h]) * tm;
-        return {h, min(tm, sm.tab.row_off[h + 1] - first), first, nullptr};
+// tile `id` of the rows behind the last adapter's
+__device__ inline RowTile behind(const Rows& p, int covered, int id, int tm) {
+    const int64_t first = covered + (int64_t)id * tm;
+    return {-1, (int)max((int64_t)0, min((int64_t)tm, p.m - first)), (int)min(first, (int64_t)p.m), nullptr};
+}
+// Sorted rows: tile `id` of `tm` rows each, adapters first and then the rows behind the last one's.  Up to 64
+// adapters every wave scans the sizes by itself, which takes a third of the time of the tables' two block scans.
+__device__ inline RowTile sorted_tile(const Rows& p, int id, int tm, Tables& tab) {
+    if (p.g <= 64) {
+        const int l = threadIdx.x & 63, given = l < p.g ? p.group_sizes[l] : 0;
+        uint32_t end = (uint32_t)min(max(given, 0), p.m);
+        const uint32_t own = end;
+        for (int d = 1; d < 64; d <<= 1) {   // sums held to m, which is associative
+            const uint32_t u = (uint32_t)__shfl_up((int)end, d, 64);
+            if (l >= d) end = min(end + u, (uint32_t)p.m);
+        }
+        uint32_t start = (uint32_t)__shfl_up((int)end, 1, 64);
+        if (l == 0) start = 0;
+        const int mine = (int)((end - start + tm - 1) / (uint32_t)tm);
+        int tiles = mine;
+        for (int d = 1; d < 64; d <<= 1) {
+            const int u = __shfl_up(tiles, d, 64);
+            if (l >= d) tiles += u;
+        }
+        const int total = __shfl(tiles, 63, 64), covered = __shfl((int)end, 63, 64);
+        if (p.status && blockIdx.x == 0 && blockIdx.y == 0) {
+            const bool over = __any(end - start < own || (given > p.m));
+            const bool negative = __any(given < 0);
+            if (threadIdx.x == 0) *p.status = (negative ? GG_DEV_NEGATIVE_SIZE : 0u) | (over ? GG_DEV_SUM_EXCEEDS_M : 0u);
+        }
+        if (id < total) {
+            const int h = __popcll(__ballot(tiles <= id));
+            const int first = __shfl((int)start, h, 64) + (id - __shfl(tiles - mine, h, 64)) * tm;
+            return {h, min(tm, __shfl((int)end, h, 64) - first), first, nullptr};
+        }
+        return behind(p, covered, id - total, tm);
     }
-    const int first = covered + (id - tiles) * tm;
-    return {-1, max(0, min(tm, p.m - first)), first, nullptr};
+    int tiles, covered;
+    build_tables<NT>(p.group_sizes, p.g, p.m, tm, 1, tab, &tiles, &covered);
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && p.status) *p.status = tab.flags;
+    RowTile w = behind(p, covered, id - tiles, tm);
+    if (id < tiles) {
+        const int h = find_group(tab.tile_off, p.g, id);
+        const int first = tab.row_off[h] + (id - tab.tile_off[h]) * tm;
+        w = {h, min(tm, tab.row_off[h + 1] - first), first, nullptr};
+    }
+    __syncthreads();   // the tables' memory is used again
+    return w;
 }
 // Rows in any order: slot `id` of a chunk is adapter `id`, or (fewer rows than adapters) the adapter of row `id` of
 // the chunk if no row before it has the same; the last slot is the rows without one.  The list is in row order.
-__device__ inline RowTile any_tile(const Rows& p, int id, RowSmem& sm) {
+__device__ inline RowTile any_tile(const Rows& p, int id, RowList& any) {
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && p.status) *p.status = 0;
     const int slots = p.slots + 1, c = id / slots, slot = id - c * slots;
     const int r0 = c * p.chunk, n = min(p.chunk, p.m - r0);
@@ -128,21 +160,22 @@ __device__ inline RowTile any_tile(const Rows& p, int id, RowSmem& sm) {
         int of = i < n ? p.row_group[r0 + i] : INT32_MIN;
         if (i < n && (of < 0 || of >= p.g)) of = -1;
         const unsigned long long mine = __ballot(of == h);
-        if ((t & 63) == 0) sm.any.wave[w] = __popcll(mine);
+        if ((t & 63) == 0) any.wave[w] = __popcll(mine);
         __syncthreads();
         int at = found;
         for (int j = 0; j < 4; ++j) {
-            if (j < w) at += sm.any.wave[j];
-            found += sm.any.wave[j];
+            if (j < w) at += any.wave[j];
+            found += any.wave[j];
         }
-        if (of == h) sm.any.list[at + __popcll(mine & ((1ull << (t & 63)) - 1))] = r0 + i;
+        if (of == h) any.list[at + __popcll(mine & ((1ull << (t & 63)) - 1))] = r0 + i;
         __syncthreads();
     }
-    if (by_row && h >= 0 && found > 0 && sm.any.list[0] != r0 + slot) found = 0;   // an earlier row's slot has them
-    return {h, found, 0, sm.any.list};
+    if (by_row && h >= 0 && found > 0 && any.list[0] != r0 + slot) found = 0;   // an earlier row's slot has them
+    return {h, found, 0, any.list};
 }
-__device__ inline RowTile row_tile(const Rows& p, int id, int tm, RowSmem& sm) {
-    return p.group_sizes ? sorted_tile(p, id, tm, sm) : any_tile(p, id, sm);
+// `scratch`: LDS that is free until the call returns
+__device__ inline RowTile row_tile(const Rows& p, int id, int tm, RowList& any, void* scratch) {
+    return p.group_sizes ? sorted_tile(p, id, tm, *(Tables*)scratch) : any_tile(p, id, any);
 }
 __device__ inline int row_at(const RowTile& w, int i) { return w.list ? w.list[i] : w.first + i; }
 
@@ -150,12 +183,13 @@ __device__ inline int row_at(const RowTile& w, int i) { return w.list ? w.list[i
 // shrink: t[split, row, j] = x[row] . w[h][j], over the split's part of the long axis.  16 MT rows, 16 NB columns j.
 // The weights are the first operand, so a lane ends with four consecutive j of one row.
 
-template <typename T, int NB, int MT>
+template <typename T, int NB, int MT, int U>   // U pieces of the axis in flight
 __global__ __launch_bounds__(NT) void shrink(Shrink p) {
     constexpr int TM = 16 * MT;
-    __shared__ RowSmem rs;
-    __shared__ f32x4 red[2][MT * NB * 64];
-    const RowTile w = row_tile(p.rows, blockIdx.x, TM, rs);
+    __shared__ RowList rs;
+    __shared__ union { f32x4 red[2][MT * NB * 64]; Tables tab; } sm;
+    auto& red = sm.red;
+    const RowTile w = row_tile(p.rows, blockIdx.x, TM, rs, &sm);
     if (w.h < 0 || w.rows == 0) return;
     const int t = threadIdx.x, l = t & 63, wave = t >> 6, q = l >> 4, i16 = l & 15;
     const int nch = (p.k + KC - 1) / KC, per = (nch + (int)gridDim.y - 1) / (int)gridDim.y;
@@ -173,22 +207,31 @@ __global__ __launch_bounds__(NT) void shrink(Shrink p) {
 #pragma unroll
             for (int b = 0; b < NB; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
         const int whole = min(c1, p.k / KC);   // chunks that lie inside the axis
-        for (int c = c0 + wave; c < whole; c += 4) {
-            Frag<T> x[MT][2], m[NB][2];
+        auto pieces = [&](int c, auto u_c) {
+            constexpr int N = decltype(u_c)::value;
+            Frag<T> x[N][2][MT], m[N][2][NB];
 #pragma unroll
-            for (int s = 0; s < 2; ++s) {
+            for (int u = 0; u < N; ++u)
 #pragma unroll
-                for (int a = 0; a < MT; ++a) x[a][s].load(xp[a] + (int64_t)c * KC + 32 * s);
+                for (int s = 0; s < 2; ++s) {
 #pragma unroll
-                for (int b = 0; b < NB; ++b) m[b][s].load(wp[b] + (int64_t)c * KC + 32 * s);
-            }
+                    for (int a = 0; a < MT; ++a) x[u][s][a].load(xp[a] + (int64_t)(c + 4 * u) * KC + 32 * s);
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
+                    for (int b = 0; b < NB; ++b) m[u][s][b].load(wp[b] + (int64_t)(c + 4 * u) * KC + 32 * s);
+                }
 #pragma unroll
-                for (int b = 0; b < NB; ++b)
+            for (int u = 0; u < N; ++u)
 #pragma unroll
-                    for (int a = 0; a < MT; ++a) acc[a][b] = Frag<T>::mma(m[b][s], x[a][s], acc[a][b]);
-        }
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+#pragma unroll
+                        for (int a = 0; a < MT; ++a) acc[a][b] = Frag<T>::mma(m[u][s][b], x[u][s][a], acc[a][b]);
+        };
+        int c = c0 + wave;
+        for (; c + 4 * (U - 1) < whole; c += 4 * U) pieces(c, std::integral_constant<int, U>{});
+        if constexpr (U > 1)
+            for (; c < whole; c += 4) pieces(c, std::integral_constant<int, 1>{});
         if (c0 <= whole && whole < c1 && (whole - c0) % 4 == wave) {   // the chunk that the axis ends in
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
@@ -237,10 +280,137 @@ __global__ __launch_bounds__(NT) void shrink(Shrink p) {
     }
 }
 
+// The same through LDS, for rows of whole 16 bytes.  A matrix instruction's lanes 0 .. 15 hold sixteen rows, so fragments
+// loaded straight from memory touch a line a lane, and the address path, not the memory, sets the pace (3 TB/s at rank
+// 16, 1.5 at rank 64).  Here eight lanes load 128 contiguous bytes of a row straight into LDS, in a ring of D slots, and
+// the fragments come from there.  A slot is [rows][128 bytes], its 16-byte pieces XOR'ed with the row so that a
+// fragment's lanes read from all banks.  TEAM = 4: the four waves share one ring and the weights in it, 16 rows each;
+// TEAM = 1 (few rows an adapter): each wave has a ring of its own, the pieces of the axis are dealt to the waves, and no
+// barrier is needed until their sums are added up.
+template <typename T> __device__ inline Frag<T> ring_frag(const char* slot, int row, int s);
+template <> __device__ inline Frag<uint16_t> ring_frag<uint16_t>(const char* slot, int row, int s) {
+    const int q = (threadIdx.x & 63) >> 4;
+    Frag<uint16_t> f;
+    f.v = *(const bf16x8*)(slot + row * 128 + 16 * ((4 * s + q) ^ ((row >> 1) & 7)));
+    return f;
+}
+template <> __device__ inline Frag<float> ring_frag<float>(const char* slot, int row, int) {
+    const int q = (threadIdx.x & 63) >> 4;
+    Frag<float> f;
+    f.lo = *(const f32x4*)(slot + row * 128 + 16 * ((2 * q) ^ ((row >> 1) & 7)));
+    f.hi = *(const f32x4*)(slot + row * 128 + 16 * ((2 * q + 1) ^ ((row >> 1) & 7)));
+    return f;
+}
+// 16 bytes a lane from memory straight into LDS at lds + 16 * lane, outside the compiler's wait tracking (ring.hpp)
+__device__ inline void load_lds16_at(const char* p, uint32_t lds) {
+    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" :: "s"(lds), "v"(p) : "memory", "m0");
+}
+
+template <typename T, int NB, int TEAM, int D>
+__global__ __launch_bounds__(NT) void shrink_ring(Shrink p) {
+    constexpr int TM = 16 * TEAM, WB = TEAM == 4 && NB < 2 ? 2 : NB;   // blocks of 16 weight rows in a slot
+    constexpr int SLOT = (TM + 16 * WB) * 128, PER = (TM + 16 * WB) / 8 / TEAM;   // bytes; loads a wave
+    constexpr int KE = 128 / sizeof(T), STEPS = sizeof(T) == 2 ? 2 : 1, RINGS = 4 / TEAM;
+    static_assert(PER * (D - 1) <= 63, "vmcnt range");
+    static_assert(RINGS * D * SLOT >= (RINGS > 1 ? 2 * NB * 64 * 16 : 0), "the sums of the waves fit the rings");
+    __shared__ RowList rs;
+    __shared__ __attribute__((aligned(128))) char rings[RINGS][D * SLOT];
+    static_assert(sizeof(rings) >= sizeof(Tables), "the rings hold the tables first");
+    const RowTile w = row_tile(p.rows, blockIdx.x, TM, rs, rings);
+    if (w.h < 0 || w.rows == 0) return;
+    const int t = threadIdx.x, l = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6), q = l >> 4, i16 = l & 15;
+    const int mate = TEAM == 4 ? wave : 0, ring_id = TEAM == 4 ? 0 : wave;
+    const int nch = (p.k + KE - 1) / KE, per = (nch + (int)gridDim.y - 1) / (int)gridDim.y;
+    const int c0 = blockIdx.y * per, c1 = min(nch, c0 + per), whole = min(c1, p.k / KE);
+    const int count = max(0, whole - c0 - (TEAM == 4 ? 0 : wave) + (RINGS - 1)) / RINGS;   // this ring's pieces: every RINGS-th
+    const char* ring = rings[ring_id];
+    const uint32_t lds = ring::lds_u32(ring);
+    for (int r0 = 0; r0 < w.rows; r0 += TM) {
+        // load u of this wave: rows 8 (PER mate + u) .. + 7 of the slot, x's first and then the weights'
+        const char* src[PER];
+#pragma unroll
+        for (int u = 0; u < PER; ++u) {
+            const int row = 8 * (PER * mate + u) + (l >> 3), piece = 16 * ((l & 7) ^ ((row >> 1) & 7));
+            const T* at = row < TM ? (const T*)p.x + (int64_t)row_at(w, min(r0 + row, w.rows - 1)) * p.stride
+                                   : (const T*)p.w + ((int64_t)w.h * p.r + min(row - TM, p.r - 1)) * p.k;
+            src[u] = (const char*)(at + (int64_t)(c0 + (TEAM == 4 ? 0 : wave)) * KE) + piece;
+        }
+        auto issue = [&](int i, int slot) {   // past the end: the last piece again, which no one reads
+            const int64_t off = (int64_t)min(i, count - 1) * (RINGS * 128);
+#pragma unroll
+            for (int u = 0; u < PER; ++u)
+                load_lds16_at(src[u] + off, __builtin_amdgcn_readfirstlane(lds + slot * SLOT + (PER * mate + u) * 1024));
+        };
+        f32x4 acc[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (r0 > 0 || w.list) ring::lds_barrier();   // the list and the last tile's sums have been read
+        if (count > 0) {
+#pragma unroll
+            for (int d = 0; d < D - 1; ++d) issue(d, d);
+            int slot = 0;
+            for (int i = 0; i < count; ++i) {
+                ring::wait_vm<PER * (D - 2)>();   // piece i is in LDS: this wave's part of it
+                if (TEAM == 4) ring::lds_barrier();   // and the others'; and piece i - 1 has been read
+                const char* at = ring + slot * SLOT;
+#pragma unroll
+                for (int s = 0; s < STEPS; ++s) {
+                    const Frag<T> x = ring_frag<T>(at, 16 * mate + i16, s);
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) acc[b] = Frag<T>::mma(ring_frag<T>(at, TM + 16 * b + i16, s), x, acc[b]);
+                }
+                if (TEAM == 1) asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // a wave alone: its reads are done
+                issue(i + D - 1, slot == 0 ? D - 1 : slot - 1);
+                slot = slot == D - 1 ? 0 : slot + 1;
+            }
+        }
+        ring::wait_vm<0>();
+        const bool tail = c0 <= whole && whole < c1;
+        if (tail && (TEAM == 4 || (whole - c0) % RINGS == wave)) {   // the piece that the axis ends in
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) {
+                const int e0 = whole * KE + 32 * s + 8 * q, valid = p.k - e0;
+                Frag<T> x;
+                x.load_part((const T*)p.x + (int64_t)row_at(w, min(r0 + 16 * mate + i16, w.rows - 1)) * p.stride + e0, valid);
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    Frag<T> m;
+                    m.load_part((const T*)p.w + ((int64_t)w.h * p.r + min(16 * b + i16, p.r - 1)) * p.k + e0, valid);
+                    acc[b] = Frag<T>::mma(m, x, acc[b]);
+                }
+            }
+        }
+        if constexpr (RINGS > 1) {   // waves 2 and 3 to 0 and 1, then 1 to 0
+            f32x4* red = (f32x4*)&rings[0][0];
+            __syncthreads();
+#pragma unroll
+            for (int half = 2; half >= 1; half >>= 1) {
+                if (wave >= half && wave < 2 * half)
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) red[((wave - half) * NB + b) * 64 + l] = acc[b];
+                __syncthreads();
+                if (wave < half)
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) acc[b] += red[(wave * NB + b) * 64 + l];
+                __syncthreads();
+            }
+            if (wave > 0) continue;
+        }
+        const int row = r0 + 16 * mate + i16;
+        if (row >= w.rows) continue;
+        float* to = p.t + ((int64_t)blockIdx.y * p.rows.m + row_at(w, row)) * p.r;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (16 * b + 4 * q + e < p.r) to[16 * b + 4 * q + e] = acc[b][e];
+    }
+}
+
 // ---------------------------------------------------------------------------------------------------------------
 // expand: out[row] = base[row] + s[h] t[row] . w[h]^T for 16 MT rows and `cols` columns, t being the sum of the
-// splits.  The weights are the first operand; row i of two 16-row blocks j = 0, 1 is column 8 (i / 4) + 4 j + i % 4 of
-// 32, so a lane ends with eight consecutive columns of one row.
+// splits.  The weights are the first operand, so a lane ends with four columns of one row, and consecutive lanes with
+// different rows; results turn in LDS so that eight lanes read 128 contiguous bytes of base and write them of out.
 
 template <typename O> struct Out8;
 template <> struct Out8<uint16_t> {
@@ -276,20 +446,23 @@ template <> struct Out8<float> {
     }
 };
 
-// t of a tile's rows as the second operand: `width` elements a row, bf16: [high | low] of 8 ceil(r / 8) each.
+// t of a tile's rows as the second operand, in steps of 32 elements of r: bf16 [high | low], fp32 as it is.
 template <typename T, int NB> struct Narrow {
-    static constexpr bool BF = sizeof(T) == 2;
-    static constexpr int PITCH = BF ? 32 * NB + 8 : 16 * (NB < 2 ? 2 : NB) + 4;
+    static constexpr int STEPS = NB < 2 ? 1 : NB / 2, PARTS = sizeof(T) == 2 ? 2 : 1;
+    static constexpr int PITCH = PARTS * 32 * STEPS + (sizeof(T) == 2 ? 8 : 4);
 };
 
 template <typename T, typename O, int NB, int MT, bool WHOLE>   // WHOLE: r % 8 == 0
 __global__ __launch_bounds__(NT) void expand(Expand p) {
-    constexpr int TM = 16 * MT, PITCH = Narrow<T, NB>::PITCH;
-    constexpr bool BF = sizeof(T) == 2;
-    __shared__ RowSmem rs;
+    using N = Narrow<T, NB>;
+    constexpr int TM = 16 * MT, PITCH = N::PITCH, STEPS = N::STEPS, PARTS = N::PARTS;
+    __shared__ RowList rs;
     __shared__ __attribute__((aligned(16))) T nar[TM * PITCH];
+    constexpr int SP = 64 + 4;                          // 16 rows of 64 columns of a wave, on their way to whole lines
+    __shared__ __attribute__((aligned(16))) float strips[4][16 * SP];
     const int ct = blockIdx.x % p.col_tiles, id = blockIdx.x / p.col_tiles;
-    const RowTile w = row_tile(p.rows, id, TM, rs);
+    static_assert(sizeof(strips) >= sizeof(Tables), "the strips hold the tables first");
+    const RowTile w = row_tile(p.rows, id, TM, rs, strips);
     const int t = threadIdx.x, l = t & 63, wave = t >> 6, q = l >> 4, i16 = l & 15;
     const int col0 = ct * p.cols, col1 = min(p.n, col0 + p.cols);
     const O* base = (const O*)p.base;
@@ -305,106 +478,356 @@ __global__ __launch_bounds__(NT) void expand(Expand p) {
         return;
     }
     const float scale = p.scaling ? p.scaling[w.h] : 1.f;
-    const int rk = (p.r + 7) / 8;                       // eights of r
-    const int eights = BF ? 2 * rk : rk, steps = (eights + 3) / 4;
+    const int last = (p.r + 7) / 8 - 1;                 // the last eight of r
     const T* wb = (const T*)p.w + (int64_t)w.h * p.n * p.r;
     for (int r0 = 0; r0 < w.rows; r0 += TM) {
         if (r0) __syncthreads();
-        for (int e = t; e < TM * 8 * rk; e += NT) {
-            const int i = e / (8 * rk), j = e - i * 8 * rk;
-            float s = 0.f;
-            if (r0 + i < w.rows && j < p.r) {
-                const int64_t at = (int64_t)row_at(w, r0 + i) * p.r + j;
-                for (int k = 0; k < p.splits; ++k) s += p.t[(int64_t)k * p.rows.m * p.r + at];
-                if (p.v && ct == 0 && p.v != p.t) p.v[at] = s;
+        for (int e0 = 0; e0 < TM * 32 * STEPS; e0 += 8 * NT) {   // t: eight values of a thread in flight
+            constexpr int NE = TM * 32 * STEPS < 8 * NT ? TM * 32 * STEPS / NT : 8;
+            float sum[NE];
+            int64_t from[NE];
+            bool have[NE];
+#pragma unroll
+            for (int u = 0; u < NE; ++u) {
+                const int e = e0 + t + NT * u, i = e / (32 * STEPS), j = e % (32 * STEPS);   // (powers of two)
+                have[u] = r0 + i < w.rows && j < p.r;
+                from[u] = have[u] ? (int64_t)row_at(w, r0 + i) * p.r + j : 0;
+                sum[u] = 0.f;
             }
-            s *= scale;
-            if constexpr (BF) {
-                uint16_t two[2];
-                split<2>(s, two);
-                nar[i * PITCH + j] = two[0];
-                nar[i * PITCH + 8 * rk + j] = two[1];
-            } else {
-                nar[i * PITCH + j] = s;
+            for (int k = 0; k < p.splits; k += 4) {   // four parts at a time, added in order
+                float f[4][NE];
+#pragma unroll
+                for (int z = 0; z < 4; ++z)
+#pragma unroll
+                    for (int u = 0; u < NE; ++u) f[z][u] = k + z < p.splits ? p.t[(int64_t)(k + z) * p.rows.m * p.r + from[u]] : 0.f;
+#pragma unroll
+                for (int z = 0; z < 4; ++z)
+#pragma unroll
+                    for (int u = 0; u < NE; ++u) sum[u] += f[z][u];
             }
-        }
-        for (int e = t; e < TM * 8 * (4 * steps - eights); e += NT) {   // up to whole steps
-            const int per = 8 * (4 * steps - eights), i = e / per;
-            nar[i * PITCH + 8 * eights + e - i * per] = (T)0;
+#pragma unroll
+            for (int u = 0; u < NE; ++u) {
+                const int e = e0 + t + NT * u, i = e / (32 * STEPS), j = e % (32 * STEPS);
+                if (!have[u]) sum[u] = 0.f;
+                if (have[u] && p.v && ct == 0 && p.v != p.t) p.v[from[u]] = sum[u];
+                if constexpr (PARTS == 2) {
+                    uint16_t two[2];
+                    split<2>(sum[u] * scale, two);
+                    nar[i * PITCH + j] = two[0];
+                    nar[i * PITCH + 32 * STEPS + j] = two[1];
+                } else {
+                    nar[i * PITCH + j] = sum[u] * scale;
+                }
+            }
         }
         __syncthreads();
-        for (int c = col0 + 32 * wave; c < col1; c += 128) {
-            const int cc = c + 8 * q;   // the lane's eight columns
-            Out8<O> o[MT];
+        // a wave: 64 columns of all rows at a time, the next ones' base on its way
+        auto fetch = [&](Out8<O> (&o)[MT][2], int c) {
 #pragma unroll
-            for (int a = 0; a < MT; ++a) {
-                o[a].zero();
-                const int i = r0 + 16 * a + i16;
-                if (base && i < w.rows && cc + 8 <= p.n) o[a].load(base + (int64_t)row_at(w, i) * p.base_stride + cc);
-            }
-            const T* wr[2];
+            for (int a = 0; a < MT; ++a)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) wr[j] = wb + (int64_t)min(c + 8 * (i16 >> 2) + 4 * j + (i16 & 3), p.n - 1) * p.r;
-            f32x4 acc[MT][2];
-#pragma unroll
-            for (int a = 0; a < MT; ++a) acc[a][0] = acc[a][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-            for (int s = 0; s < steps; ++s) {
-                int e = min(4 * s + q, eights - 1);      // past the end: times the zeros above
-                if (BF && e >= rk) e -= rk;              // the low parts take the same weights
-                Frag<T> m[2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    if (WHOLE) m[j].load(wr[j] + 8 * e);
-                    else m[j].load_part(wr[j] + 8 * e, p.r - 8 * e);
+                for (int d = 0; d < 2; ++d) {
+                    const int i = r0 + 16 * a + 8 * d + (l >> 3), cc = c + 8 * (l & 7);
+                    o[a][d].zero();
+                    if (base && i < w.rows && cc + 8 <= col1) o[a][d].load(base + (int64_t)row_at(w, i) * p.base_stride + cc);
                 }
+        };
+        Out8<O> next[MT][2];
+        fetch(next, col0 + 64 * wave);
+        for (int c = col0 + 64 * wave; c < col1; c += 256) {
+            Out8<O> o[MT][2];
 #pragma unroll
-                for (int a = 0; a < MT; ++a) {
-                    Frag<T> x;
-                    x.load_lds(nar + (16 * a + i16) * PITCH + 8 * (4 * s + q));
+            for (int a = 0; a < MT; ++a) { o[a][0] = next[a][0]; o[a][1] = next[a][1]; }
+            Frag<T> m[4][STEPS];
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) acc[a][j] = Frag<T>::mma(m[j], x, acc[a][j]);
+            for (int j = 0; j < 4; ++j) {
+                const T* wr = wb + (int64_t)min(c + 16 * j + i16, p.n - 1) * p.r;
+#pragma unroll
+                for (int s = 0; s < STEPS; ++s) {
+                    const int e = 8 * min(4 * s + q, last);   // past the end: times the zeros above
+                    if (WHOLE) m[j][s].load(wr + e);
+                    else m[j][s].load_part(wr + e, p.r - e);
                 }
             }
+            fetch(next, c + 256);
 #pragma unroll
             for (int a = 0; a < MT; ++a) {
-                const int i = r0 + 16 * a + i16;
-                if (i >= w.rows || cc >= col1) continue;
-                const int64_t row = row_at(w, i);
-                float v[8];
+                f32x4 acc[4];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) { v[e] = acc[a][0][e]; v[4 + e] = acc[a][1][e]; }
-                if (cc + 8 <= p.n) {
+                for (int j = 0; j < 4; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) v[e] += o[a].get(e);
-                    Out8<O>::store(out + row * p.out_stride + cc, v);
-                } else {
+                for (int s = 0; s < STEPS; ++s)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (cc + e < p.n)
-                            Out8<O>::put(out + row * p.out_stride + cc + e,
-                                         v[e] + (base ? Out8<O>::one(base + row * p.base_stride + cc + e) : 0.f));
+                    for (int z = 0; z < PARTS; ++z) {
+                        Frag<T> x;
+                        x.load_lds(nar + (16 * a + i16) * PITCH + 32 * (STEPS * z + s) + 8 * q);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) acc[j] = Frag<T>::mma(m[j][s], x, acc[j]);
+                    }
+                float* strip = strips[wave];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) *(f32x4*)(strip + i16 * SP + 16 * j + 4 * q) = acc[j];
+#pragma unroll
+                for (int d = 0; d < 2; ++d) {
+                    const int i = r0 + 16 * a + 8 * d + (l >> 3), cc = c + 8 * (l & 7);
+                    const float* from = strip + (8 * d + (l >> 3)) * SP + 8 * (l & 7);
+                    const f32x4 lo = *(const f32x4*)from, hi = *(const f32x4*)(from + 4);
+                    if (i >= w.rows || cc >= col1) continue;
+                    const int64_t row = row_at(w, i);
+                    float v[8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) { v[e] = lo[e]; v[4 + e] = hi[e]; }
+                    if (cc + 8 <= p.n) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) v[e] += o[a][d].get(e);
+                        Out8<O>::store(out + row * p.out_stride + cc, v);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (cc + e < p.n)
+                                Out8<O>::put(out + row * p.out_stride + cc + e, v[e] + (base ? Out8<O>::one(base + row * p.base_stride + cc + e) : 0.f));
+                    }
                 }
             }
         }
     }
 }
 
-// ---------------------------------------------------------------------------------------------------------------
-// turn: [g, rows, cols] -> [g, cols, rows]
+// The same for many rows of bf16 weights, rows of whole 16 bytes and ranks of whole eights: 64 MT rows a workgroup, 16 MT a
+// wave.  All four waves multiply with the same 64 columns' weights, which lie together in memory, so they are loaded as
+// whole lines, once a workgroup, into one of two LDS slots (fragments straight from memory touch a line a lane, and their
+// loads set the pace of the kernel above: 470 MB at rank 64 took 137 us).  t stays in registers.  Base, the weights two
+// steps on and the results are loaded and stored without branches (offsets outside their descriptor read as 0 and are not
+// stored), so no wait counts on fewer operations in flight than there are, and none waits for stores just issued.
+template <typename O> struct Line8;
+template <> struct Line8<uint16_t> {
+    i32x4 q;
+    __device__ void load(ring::rsrc_t r, uint32_t off) { q = __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 2); }
+    __device__ float get(int i) const { return __uint_as_float((i & 1) ? (uint32_t)q[i >> 1] & 0xffff0000u : (uint32_t)q[i >> 1] << 16); }
+    __device__ static void store(ring::rsrc_t r, uint32_t off, const float (&v)[8]) {
+        ring::bstore(r, off, i32x4{(int)ring::pack_bf16(v[0], v[1]), (int)ring::pack_bf16(v[2], v[3]), (int)ring::pack_bf16(v[4], v[5]),
+                                   (int)ring::pack_bf16(v[6], v[7])});
+    }
+};
+template <> struct Line8<float> {
+    i32x4 a, b;
+    __device__ void load(ring::rsrc_t r, uint32_t off) {
+        a = __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 2);
+        b = __builtin_amdgcn_raw_buffer_load_b128(r, off, 16, 2);
+    }
+    __device__ float get(int i) const { return __int_as_float(i < 4 ? a[i] : b[i - 4]); }
+    __device__ static void store(ring::rsrc_t r, uint32_t off, const float (&v)[8]) {
+        ring::bstore(r, off, i32x4{__float_as_int(v[0]), __float_as_int(v[1]), __float_as_int(v[2]), __float_as_int(v[3])});
+        ring::bstore(r, off + 16, i32x4{__float_as_int(v[4]), __float_as_int(v[5]), __float_as_int(v[6]), __float_as_int(v[7])});
+    }
+};
 
-template <typename T>
-__global__ __launch_bounds__(NT) void turn(const T* __restrict__ a, T* __restrict__ at, int rows, int cols, int tr, int tc) {
-    __shared__ T s[32][33];
-    const int id = blockIdx.x, c0 = 32 * (id % tc), r0 = 32 * ((id / tc) % tr);
-    const int64_t h = id / tc / tr, off = h * rows * cols;
-    const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+template <typename O, int NB, int MT>
+__global__ __launch_bounds__(NT) void expand_lines(Expand p) {
+    constexpr int STEPS = NB < 2 ? 1 : NB / 2, TM = 64 * MT, PITCH = 64 * STEPS + 8;   // PITCH: [high | low] of a row of t
+    constexpr int ROWB = 64 * STEPS, SLOT = 64 * ROWB;           // bytes of a column's weights, of 64 columns'
+    constexpr int WL = (64 * 2 * NB + NT - 1) / NT;              // 16-byte loads a thread of 64 columns' weights
+    constexpr int SP = 64 + 4;
+    __shared__ union {
+        Tables tab;
+        __attribute__((aligned(16))) uint16_t nar[TM * PITCH];
+        struct { __attribute__((aligned(16))) char w[2][SLOT]; __attribute__((aligned(16))) float strips[4][16 * SP]; } s;
+    } sm;
+    __shared__ RowList rs;
+    const int ct = blockIdx.x % p.col_tiles, id = blockIdx.x / p.col_tiles;
+    const RowTile w = row_tile(p.rows, id, TM, rs, &sm);
+    const int t = threadIdx.x, l = t & 63, wave = t >> 6, q = l >> 4, i16 = l & 15;
+    const int col0 = ct * p.cols, col1 = min(p.n, col0 + p.cols);
+    constexpr uint32_t os = sizeof(O);
+    if (w.h < 0) {   // rows without an adapter: what was there
+        if (p.v && ct == 0)
+            for (int i = 0; i < w.rows; ++i)
+                for (int j = t; j < p.r; j += NT) p.v[(int64_t)row_at(w, i) * p.r + j] = 0.f;
+        if (p.base == p.out && p.base_stride == p.out_stride) return;
+        const int lines = (col1 - col0) * (int)os / 16;
+        for (int i = t / 64; i < w.rows; i += 4) {
+            const int64_t row = row_at(w, i);
+            const i32x4* from = (const i32x4*)((const O*)p.base + row * p.base_stride + col0);
+            i32x4* to = (i32x4*)((O*)p.out + row * p.out_stride + col0);
+            for (int c = l; c < lines; c += 64) to[c] = p.base ? from[c] : i32x4{0, 0, 0, 0};
+        }
+        return;
+    }
+    const float scale = p.scaling ? p.scaling[w.h] : 1.f;
+    const int pieces = p.r / 8;                                  // 16-byte pieces of a column's weights
+    const ring::rsrc_t rw = ring::make_rsrc((const uint16_t*)p.w + (int64_t)w.h * p.n * p.r, (uint32_t)p.n * p.r * 2u);
+    // where the thread's pieces of 64 columns' weights lie in a slot (rows of ROWB bytes, XOR'ed so that the 16 lanes of a
+    // fragment read from all banks), -1: none
+    int at[WL];
 #pragma unroll
-    for (int i = 0; i < 32; i += 8)
-        if (r0 + y + i < rows && c0 + x < cols) s[y + i][x] = a[off + (int64_t)(r0 + y + i) * cols + c0 + x];
+    for (int u = 0; u < WL; ++u) {
+        const int e = t + NT * u, col = e / pieces;
+        at[u] = e < 64 * pieces ? col * ROWB + 16 * ((e - col * pieces) ^ (STEPS == 1 ? (col >> 2) & 3 : STEPS == 2 ? (col >> 1) & 7 : col & 15)) : -1;
+    }
+    auto slot_frag = [&](const char* slot, int col, int s) {
+        const int x = STEPS == 1 ? (col >> 2) & 3 : STEPS == 2 ? (col >> 1) & 7 : col & 15;
+        return *(const bf16x8*)(slot + col * ROWB + 16 * ((4 * s + q) ^ x));
+    };
+    for (int r0 = 0; r0 < w.rows; r0 += TM) {
+        __syncthreads();
+        {   // t: four values a load, all of a thread's in flight
+            constexpr int NE = TM * 8 * STEPS / NT;
+            f32x4 sum[NE];
+            int64_t from[NE];
+            bool have[NE];
+#pragma unroll
+            for (int u = 0; u < NE; ++u) {
+                const int i = (t + NT * u) / (8 * STEPS), j = 4 * ((t + NT * u) % (8 * STEPS));
+                have[u] = r0 + i < w.rows && j < p.r;
+                from[u] = have[u] ? (int64_t)row_at(w, r0 + i) * p.r + j : 0;
+                sum[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+            }
+            for (int k = 0; k < p.splits; ++k) {
+                const float* part = p.t + (int64_t)k * p.rows.m * p.r;
+                f32x4 f[NE];
+#pragma unroll
+                for (int u = 0; u < NE; ++u) f[u] = *(const f32x4_any*)(part + from[u]);
+#pragma unroll
+                for (int u = 0; u < NE; ++u) sum[u] += f[u];
+            }
+            const bool keep = p.v && ct == 0 && p.v != p.t;
+#pragma unroll
+            for (int u = 0; u < NE; ++u) {
+                if (!have[u]) sum[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+                if (keep && have[u]) *(f32x4_any*)(p.v + from[u]) = sum[u];
+                const int i = (t + NT * u) / (8 * STEPS), j = 4 * ((t + NT * u) % (8 * STEPS));
+                uint16_t two[4][2];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) split<2>(sum[u][e] * scale, two[e]);
+#pragma unroll
+                for (int z = 0; z < 2; ++z)
+                    *(i32x2*)(sm.nar + i * PITCH + 32 * STEPS * z + j) = i32x2{two[0][z] | two[1][z] << 16, two[2][z] | two[3][z] << 16};
+            }
+        }
+        __syncthreads();
+        bf16x8 x[MT][STEPS][2];
+#pragma unroll
+        for (int a = 0; a < MT; ++a)
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+                for (int z = 0; z < 2; ++z) x[a][s][z] = *(const bf16x8*)(sm.nar + (16 * (MT * wave + a) + i16) * PITCH + 32 * (STEPS * z + s) + 8 * q);
+        __syncthreads();
+        // a slot's pieces past r are multiplied with zeros of t: they have to be finite
+        for (int e = t; e < 2 * SLOT / 16; e += NT) *(i32x4*)(&sm.s.w[0][0] + 16 * e) = i32x4{0, 0, 0, 0};
+        // rows of the tile from its first row (a chunk's, in any order): offsets stay in 32 bits
+        const int64_t top = w.list ? (int64_t)w.list[0] : w.first + r0;
+        const ring::rsrc_t rb = ring::make_rsrc((const O*)p.base + top * p.base_stride, p.base ? 0x7fffffffu : 0u);
+        const ring::rsrc_t ro = ring::make_rsrc((O*)p.out + top * p.out_stride, 0x7fffffffu);
+        uint32_t bo[MT][2], oo[MT][2];
+#pragma unroll
+        for (int a = 0; a < MT; ++a)
+#pragma unroll
+            for (int d = 0; d < 2; ++d) {
+                const int i = r0 + 16 * (MT * wave + a) + 8 * d + (l >> 3);
+                const int64_t row = i < w.rows ? row_at(w, i) - top : 0;
+                bo[a][d] = i < w.rows ? (uint32_t)(row * p.base_stride + 8 * (l & 7)) * os : ring::kOOB;
+                oo[a][d] = i < w.rows ? (uint32_t)(row * p.out_stride + 8 * (l & 7)) * os : ring::kOOB;
+            }
+        auto fetch = [&](Line8<O> (&o)[MT][2], int c) {
+            const bool in = c + 8 * (l & 7) < col1;
+#pragma unroll
+            for (int a = 0; a < MT; ++a)
+#pragma unroll
+                for (int d = 0; d < 2; ++d) o[a][d].load(rb, in && bo[a][d] != ring::kOOB ? bo[a][d] + (uint32_t)c * os : ring::kOOB);
+        };
+        auto weights = [&](i32x4 (&v)[WL], int c) {   // columns past n: 0
+#pragma unroll
+            for (int u = 0; u < WL; ++u)
+                v[u] = __builtin_amdgcn_raw_buffer_load_b128(rw, at[u] >= 0 ? (uint32_t)c * p.r * 2u + 16u * (t + NT * u) : ring::kOOB, 0, 0);
+        };
+        auto put = [&](const i32x4 (&v)[WL], int slot) {
+#pragma unroll
+            for (int u = 0; u < WL; ++u)
+                if (at[u] >= 0) *(i32x4*)(sm.s.w[slot] + at[u]) = v[u];
+        };
+        i32x4 wv[WL];
+        Line8<O> o[MT][2], next[MT][2];
+        weights(wv, col0);
+        fetch(o, col0);
+        __syncthreads();                    // the zeros are written
+        put(wv, 0);
+        weights(wv, col0 + 64);
+        int slot = 0;
+        for (int c = col0; c < col1; c += 64, slot ^= 1) {
+            __syncthreads();                // this step's weights are in LDS, and the last one's have been read
+            fetch(next, c + 64);
+            f32x4 acc[MT][4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                bf16x8 m[STEPS];
+#pragma unroll
+                for (int s = 0; s < STEPS; ++s) m[s] = slot_frag(sm.s.w[slot], 16 * j + i16, s);
+#pragma unroll
+                for (int a = 0; a < MT; ++a) {
+                    acc[a][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+                        for (int z = 0; z < 2; ++z) acc[a][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(m[s], x[a][s][z], acc[a][j], 0, 0, 0);
+                }
+            }
+            float* strip = sm.s.strips[wave];
+            const bool in = c + 8 * (l & 7) < col1;
+#pragma unroll
+            for (int a = 0; a < MT; ++a) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) *(f32x4*)(strip + i16 * SP + 16 * j + 4 * q) = acc[a][j];
+#pragma unroll
+                for (int d = 0; d < 2; ++d) {
+                    const float* from = strip + (8 * d + (l >> 3)) * SP + 8 * (l & 7);
+                    const f32x4 lo = *(const f32x4*)from, hi = *(const f32x4*)(from + 4);
+                    float v[8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) { v[e] = lo[e] + o[a][d].get(e); v[4 + e] = hi[e] + o[a][d].get(4 + e); }
+                    Line8<O>::store(ro, in && oo[a][d] != ring::kOOB ? oo[a][d] + (uint32_t)c * os : ring::kOOB, v);
+                }
+            }
+            put(wv, slot ^ 1);
+            weights(wv, c + 128);
+#pragma unroll
+            for (int a = 0; a < MT; ++a) { o[a][0] = next[a][0]; o[a][1] = next[a][1]; }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------------------------------------------
+// turn: two of [g, rows, cols] -> [g, cols, rows], in tiles of 4096 values as wide as the narrower side wants
+
+struct Turn { const void* a; void* at; int rows, cols, lg, tr, tc; };   // 2^lg columns a tile, tr x tc tiles
+template <typename T>
+__global__ __launch_bounds__(NT) void turn(Turn p0, Turn p1, int first) {   // the first `first` workgroups: p0
+    __shared__ T s[4096 + 2048];
+    const bool one = (int)blockIdx.x >= first;
+    const Turn& p = one ? p1 : p0;
+    const int id = one ? blockIdx.x - first : blockIdx.x;
+    const int w = 1 << p.lg, hgt = 4096 >> p.lg, pitch = w + (w < 64 ? 2 : 8);
+    const int c0 = w * (id % p.tc), r0 = hgt * ((id / p.tc) % p.tr);
+    const int64_t off = (int64_t)(id / p.tc / p.tr) * p.rows * p.cols;
+    const T* a = (const T*)p.a + off;
+    T* at = (T*)p.at + off;
+    T v[4096 / NT];   // all of a thread's loads in flight
+#pragma unroll
+    for (int u = 0; u < 4096 / NT; ++u) {
+        const int e = threadIdx.x + NT * u, r = min(r0 + (e >> p.lg), p.rows - 1), c = min(c0 + (e & (w - 1)), p.cols - 1);
+        v[u] = a[(int64_t)r * p.cols + c];
+    }
+#pragma unroll
+    for (int u = 0; u < 4096 / NT; ++u) {
+        const int e = threadIdx.x + NT * u;
+        s[(e >> p.lg) * pitch + (e & (w - 1))] = v[u];
+    }
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 32; i += 8)
-        if (c0 + y + i < cols && r0 + x < rows) at[off + (int64_t)(c0 + y + i) * rows + r0 + x] = s[x][y + i];
+    for (int u = 0; u < 4096 / NT; ++u) {
+        const int e = threadIdx.x + NT * u, c = e >> (12 - p.lg), r = e & (hgt - 1);
+        if (r0 + r < p.rows && c0 + c < p.cols) at[(int64_t)(c0 + c) * p.rows + r0 + r] = s[r * pitch + c];
+    }
 }
 
 // ---------------------------------------------------------------------------------------------------------------
@@ -537,8 +960,8 @@ __global__ __launch_bounds__(NT) void outer(Outer p) {
     build_tables<NT>(p.group_sizes, p.g, p.m, p.chunk, 1, tab, &tiles, &covered);
     if (blockIdx.x == 0 && threadIdx.x == 0 && p.status) *p.status = tab.flags;
     const int xt = (p.k + TC - 1) / TC, dt = (p.n + TC - 1) / TC;
-    const int id = blockIdx.x / (xt + dt), ct = blockIdx.x - id * (xt + dt);
-    if (id >= tiles) return;
+    const int place = blockIdx.x / (xt + dt), id = tiles - 1 - place, ct = blockIdx.x - place * (xt + dt);   // from the end
+    if (id < 0) return;
     const int h = find_group(tab.tile_off, p.g, id), part = id - tab.tile_off[h];
     const int first = tab.row_off[h] + part * p.chunk, rows = min(p.chunk, tab.row_off[h + 1] - first);
     const bool of_x = ct < xt;
@@ -555,39 +978,38 @@ __global__ __launch_bounds__(NT) void outer(Outer p) {
     constexpr int NPER = 32 * 16 * NB / NT;   // narrow values a thread
     auto body = [&](auto wide_c) {
         constexpr Wide W = decltype(wide_c)::value;
-        WideRegs<W> wr;
-        float nr[NPER];
+        struct Step { WideRegs<W> wide; float nar[NPER]; } regs[2];   // two steps on their way
         const void* src = of_x ? p.x : p.dout;
         const int64_t stride = of_x ? p.k : p.n;
-        auto load = [&](int r0) {
-            wr.load(p, first + r0, rows - r0, c0, min(cols, c0 + TC), stride, src);
+        auto load = [&](Step& to, int r0) {
+            to.wide.load(p, first + r0, rows - r0, c0, min(cols, c0 + TC), stride, src);
 #pragma unroll
             for (int e = 0; e < NPER; ++e) {
                 const int at = t + NT * e, i = at / (16 * NB), j = at % (16 * NB);
-                nr[e] = i < rows - r0 && j < p.r ? nsrc[(int64_t)(first + r0 + i) * p.r + j] : 0.f;
+                to.nar[e] = i < rows - r0 && j < p.r ? nsrc[(int64_t)(first + r0 + i) * p.r + j] : 0.f;
             }
         };
-        auto store = [&](int slot) {
-            wr.store(sm.wide[slot]);
+        auto store = [&](const Step& from, int slot) {
+            from.wide.store(sm.wide[slot]);
 #pragma unroll
             for (int e = 0; e < NPER; ++e) {
                 const int at = t + NT * e, i = at / (16 * NB), j = at % (16 * NB);
-                if constexpr (F32) sm.nar[slot][0][i * NPITCH + j] = nr[e];
+                if constexpr (F32) sm.nar[slot][0][i * NPITCH + j] = from.nar[e];
                 else {
                     uint16_t s[P];
-                    split<P>(nr[e], s);
+                    split<P>(from.nar[e], s);
 #pragma unroll
                     for (int z = 0; z < P; ++z) sm.nar[slot][z][i * NPITCH + j] = s[z];
                 }
             }
         };
-        load(0);
-        store(0);
+        load(regs[0], 0);
+        load(regs[1], 32);
+        store(regs[0], 0);
         __syncthreads();
-        int slot = 0;
-        for (int r0 = 0; r0 < rows; r0 += 32, slot ^= 1) {
-            const bool more = r0 + 32 < rows;
-            if (more) load(r0 + 32);
+        auto step = [&](auto slot_c, int r0) {
+            constexpr int slot = decltype(slot_c)::value;
+            load(regs[slot], r0 + 64);
             const E* wd = sm.wide[slot];
             if constexpr (F32) {
 #pragma unroll
@@ -615,8 +1037,12 @@ __global__ __launch_bounds__(NT) void outer(Outer p) {
                         for (int c = 0; c < CB; ++c) acc[a][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(n, b[c], acc[a][c], 0, 0, 0);
                     }
             }
-            if (more) store(slot ^ 1);
+            if (r0 + 32 < rows) store(regs[slot ^ 1], slot ^ 1);
             __syncthreads();
+        };
+        for (int r0 = 0; r0 < rows; r0 += 64) {
+            step(std::integral_constant<int, 0>{}, r0);
+            if (r0 + 32 < rows) step(std::integral_constant<int, 1>{}, r0 + 32);
         }
     };
     if constexpr (XW == E4M3) {
@@ -655,26 +1081,62 @@ __global__ __launch_bounds__(NT) void outer(Outer p) {
         }
 }
 
-// join: groups of several chunks, in their order; groups without rows are 0
+// join: groups of several chunks, in their order; groups without rows are 0.  V consecutive values a thread.
+template <int V>
 __global__ __launch_bounds__(NT) void join(Outer p, int blocks) {
     __shared__ Tables tab;
-    int tiles, covered;
-    build_tables<NT>(p.group_sizes, p.g, p.m, p.chunk, 1, tab, &tiles, &covered);
     const int h = blockIdx.x / blocks, b = blockIdx.x - h * blocks;
-    const int first = tab.row_off[h], rows = tab.row_off[h + 1] - first;
+    int first = 0, rows = 0;
+    if (p.g <= 64) {   // as in sorted_tile
+        const int l = threadIdx.x & 63;
+        uint32_t end = l < p.g ? (uint32_t)min(max(p.group_sizes[l], 0), p.m) : 0u;
+        for (int d = 1; d < 64; d <<= 1) {
+            const uint32_t u = (uint32_t)__shfl_up((int)end, d, 64);
+            if (l >= d) end = min(end + u, (uint32_t)p.m);
+        }
+        first = h ? __shfl((int)end, h - 1, 64) : 0;
+        rows = __shfl((int)end, h, 64) - first;
+    } else {
+        int tiles, covered;
+        build_tables<NT>(p.group_sizes, p.g, p.m, p.chunk, 1, tab, &tiles, &covered);
+        first = tab.row_off[h];
+        rows = tab.row_off[h + 1] - first;
+    }
     if (rows > 0 && rows <= p.chunk) return;
     const int chunks = (rows + p.chunk - 1) / p.chunk;
     const float scale = p.scaling ? p.scaling[h] : 1.f;
     const int64_t ka = (int64_t)p.k * p.r, per = (int64_t)(p.k + p.n) * p.r;
-    for (int64_t e = (int64_t)b * NT + threadIdx.x; e < per; e += (int64_t)blocks * NT) {
-        float s = 0.f;
-        for (int c = 0; c < chunks; ++c) s += p.parts[(2 * (int64_t)((first + c * p.chunk) / p.chunk) + (c == 0)) * per + e];
-        s *= rows > 0 ? scale : 0.f;
-        if (rows == 0) s = 0.f;
+    for (int64_t e = ((int64_t)b * NT + threadIdx.x) * V; e < per; e += (int64_t)blocks * NT * V) {
+        float s[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[i] = 0.f;
+        for (int c = 0; c < chunks; c += 4) {   // four chunks' loads at a time, added in order
+            float f[4][V];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int at = c + u;
+                const float* from = p.parts + (2 * (int64_t)((first + min(at, chunks - 1) * p.chunk) / p.chunk) + (at == 0)) * per + e;
+                if constexpr (V == 4) {
+                    const f32x4 q = at < chunks ? *(const f32x4_any*)from : f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int i = 0; i < V; ++i) f[u][i] = q[i];
+                } else {
+                    f[u][0] = at < chunks ? *from : 0.f;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int i = 0; i < V; ++i) s[i] += f[u][i];
+        }
         void* dst = e < ka ? p.da : p.db;
         const int64_t to = e < ka ? h * ka + e : (int64_t)h * p.n * p.r + (e - ka);
-        if (p.grads_bf16) Out8<uint16_t>::put((uint16_t*)dst + to, s);
-        else ((float*)dst)[to] = s;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float v = rows > 0 ? s[i] * scale : 0.f;
+            if (p.grads_bf16) Out8<uint16_t>::put((uint16_t*)dst + to + i, v);
+            else ((float*)dst)[to + i] = v;
+        }
     }
 }
 
@@ -685,10 +1147,13 @@ __global__ __launch_bounds__(NT) void join(Outer p, int blocks) {
 
 static int64_t up64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Parts of the long axis: enough workgroups for few rows, and no part shorter than one piece of each wave.
-int lora_splits(int64_t m, int64_t k) {
-    const int64_t pieces = up64(k, 4 * lora::KC), want = 512 / std::max<int64_t>(1, up64(m, 16));
-    return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(32, want), pieces));
+// Parts of the long axis: about a thousand workgroups, no part shorter than one piece of each wave, and for many rows
+// parts whose sums are few beside the rows themselves.
+int lora_splits(int64_t m, int64_t k, int r, int g) {
+    const int64_t tiles = std::max<int64_t>(1, up64(m, 64)), few = std::min<int64_t>(m, g);
+    const int64_t pieces = up64(k, 4 * lora::KC), want = few > tiles ? 512 / few : 1024 / tiles;
+    const int64_t most = m >= 1024 ? std::min<int64_t>(8, k / (16 * r)) : 32;
+    return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(most, want), pieces));
 }
 // Rows that a workgroup of the row sums takes: about 1024 workgroups, and chunks long enough that their parts are few.
 int lora_chunk(int64_t m, int64_t k, int64_t n) {
@@ -697,11 +1162,10 @@ int lora_chunk(int64_t m, int64_t k, int64_t n) {
     return (int)std::min<int64_t>(2048, std::max<int64_t>(256, c));
 }
 
-// Rows a tile (16 MT): 64 where a group of sorted rows has that many on average.
-static int lora_mt(const lora::Rows& r, int nb) {
+// Rows a tile (16 MT): more where a group has that many on average.
+static int lora_mt(const lora::Rows& r, int nb, int most) {
     const int64_t rows = r.group_sizes ? r.m / r.g : std::min<int64_t>(r.m, r.chunk) / std::max(1, r.slots);
-    if (nb >= 16) return 1;
-    return rows >= 32 ? (nb >= 8 ? 2 : 4) : 1;
+    return rows >= 32 ? (nb >= 8 ? 2 : most) : 1;
 }
 void lora_rows(lora::Rows& r) {
     r.chunk = (int)std::min<int64_t>(lora::MAXCHUNK, std::max<int64_t>(256, up64((int64_t)32 * r.g, 256) * 256));
@@ -714,18 +1178,36 @@ static int lora_nb(int r) { return r <= 16 ? 1 : r <= 32 ? 2 : r <= 64 ? 4 : r <
 
 template <typename T, int NB, int MT>
 static hipError_t shrink_t(const lora::Shrink& p, hipStream_t s) {
+    constexpr int U = NB + MT <= 2 ? 4 : NB + MT <= 6 ? 2 : 1;
     const int64_t tiles = lora_tiles(p.rows, 16 * MT);
     if (tiles > kMaxBlocks) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((lora::shrink<T, NB, MT>), dim3((uint32_t)tiles, p.splits), dim3(lora::NT), 0, s, p);
+    hipLaunchKernelGGL((lora::shrink<T, NB, MT, U>), dim3((uint32_t)tiles, p.splits), dim3(lora::NT), 0, s, p);
+    return hipGetLastError();
+}
+template <typename T, int NB, int TEAM, int D>
+static hipError_t shrink_ring_t(const lora::Shrink& p, hipStream_t s) {
+    const int64_t tiles = lora_tiles(p.rows, 16 * TEAM);
+    if (tiles > kMaxBlocks) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL((lora::shrink_ring<T, NB, TEAM, D>), dim3((uint32_t)tiles, p.splits), dim3(lora::NT), 0, s, p);
     return hipGetLastError();
 }
 template <typename T>
 static hipError_t shrink_nb(const lora::Shrink& p, hipStream_t s) {
-    const int nb = lora_nb(p.r), mt = lora_mt(p.rows, nb);
+    const int nb = lora_nb(p.r), mt = lora_mt(p.rows, nb, 2);
+    const bool lines = (uintptr_t)p.x % 16 == 0 && (uintptr_t)p.w % 16 == 0 && p.stride * sizeof(T) % 16 == 0 && p.k * sizeof(T) % 16 == 0;
+    if (lines) {
+        switch (nb) {
+            case 1: return mt == 1 ? shrink_ring_t<T, 1, 1, 4>(p, s) : shrink_ring_t<T, 1, 4, 5>(p, s);
+            case 2: return mt == 1 ? shrink_ring_t<T, 2, 1, 3>(p, s) : shrink_ring_t<T, 2, 4, 5>(p, s);
+            case 4: return mt == 1 ? shrink_ring_t<T, 4, 1, 3>(p, s) : shrink_ring_t<T, 4, 4, 4>(p, s);
+            case 8: return mt == 1 ? shrink_ring_t<T, 8, 1, 2>(p, s) : shrink_ring_t<T, 8, 4, 3>(p, s);
+            default: return shrink_ring_t<T, 16, 4, 3>(p, s);   // a ring a wave would not fit the LDS
+        }
+    }
     switch (nb) {
-        case 1: return mt == 1 ? shrink_t<T, 1, 1>(p, s) : shrink_t<T, 1, 4>(p, s);
-        case 2: return mt == 1 ? shrink_t<T, 2, 1>(p, s) : shrink_t<T, 2, 4>(p, s);
-        case 4: return mt == 1 ? shrink_t<T, 4, 1>(p, s) : shrink_t<T, 4, 4>(p, s);
+        case 1: return mt == 1 ? shrink_t<T, 1, 1>(p, s) : shrink_t<T, 1, 2>(p, s);
+        case 2: return mt == 1 ? shrink_t<T, 2, 1>(p, s) : shrink_t<T, 2, 2>(p, s);
+        case 4: return mt == 1 ? shrink_t<T, 4, 1>(p, s) : shrink_t<T, 4, 2>(p, s);
         case 8: return mt == 1 ? shrink_t<T, 8, 1>(p, s) : shrink_t<T, 8, 2>(p, s);
         default: return shrink_t<T, 16, 1>(p, s);
     }
@@ -737,8 +1219,8 @@ hipError_t launch_lora_shrink(const lora::Shrink& p, bool bf16, hipStream_t s) {
 template <typename T, typename O, int NB, int MT>
 static hipError_t expand_t(lora::Expand p, hipStream_t s) {
     const int64_t tiles = lora_tiles(p.rows, 16 * MT);
-    p.cols = 512;
-    while (p.cols > 128 && tiles * up64(p.n, p.cols) < 1024) p.cols /= 2;
+    p.cols = 2048;
+    while (p.cols > 256 && tiles * up64(p.n, p.cols) < 1024) p.cols /= 2;
     p.col_tiles = (int)std::max<int64_t>(1, up64(p.n, p.cols));
     if (tiles * p.col_tiles > kMaxBlocks) return hipErrorInvalidConfiguration;
     const dim3 grid((uint32_t)(tiles * p.col_tiles));
@@ -746,9 +1228,39 @@ static hipError_t expand_t(lora::Expand p, hipStream_t s) {
     else hipLaunchKernelGGL((lora::expand<T, O, NB, MT, false>), grid, dim3(lora::NT), 0, s, p);
     return hipGetLastError();
 }
+template <typename O, int NB, int MT>
+static hipError_t expand_lines_t(lora::Expand p, hipStream_t s) {
+    const int64_t tiles = lora_tiles(p.rows, 64 * MT);
+    p.cols = 2048;
+    while (p.cols > 256 && tiles * up64(p.n, p.cols) < 1024) p.cols /= 2;
+    p.col_tiles = (int)std::max<int64_t>(1, up64(p.n, p.cols));
+    if (tiles * p.col_tiles > kMaxBlocks) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL((lora::expand_lines<O, NB, MT>), dim3((uint32_t)(tiles * p.col_tiles)), dim3(lora::NT), 0, s, p);
+    return hipGetLastError();
+}
+// expand_lines: 16-byte rows and ranks, and 32-bit offsets over an adapter's weights and over the rows of a tile (of a
+// chunk, in any order)
+template <typename O> static bool expand_lines_ok(const lora::Expand& p) {
+    const int64_t span = (p.rows.group_sizes ? 256 : lora::MAXCHUNK) * (int64_t)sizeof(O);
+    return p.r % 8 == 0 && p.n % 8 == 0 && p.base_stride * sizeof(O) % 16 == 0 && p.out_stride * sizeof(O) % 16 == 0 &&
+           (uintptr_t)p.base % 16 == 0 && (uintptr_t)p.out % 16 == 0 && (uintptr_t)p.w % 16 == 0 &&
+           ((int64_t)p.n + 256) * p.r * 2 < (int64_t(1) << 31) && std::max(p.base_stride, p.out_stride) * span < (int64_t(1) << 31);
+}
 template <typename T, typename O>
 static hipError_t expand_nb(const lora::Expand& p, hipStream_t s) {
-    const int nb = lora_nb(p.r), mt = lora_mt(p.rows, nb);
+    if constexpr (sizeof(T) == 2) {
+        const int nb = lora_nb(p.r);
+        if (lora_mt(p.rows, nb, 4) > 1 && expand_lines_ok<O>(p)) {
+            switch (nb) {
+                case 1: return expand_lines_t<O, 1, 2>(p, s);
+                case 2: return expand_lines_t<O, 2, 2>(p, s);
+                case 4: return expand_lines_t<O, 4, 2>(p, s);
+                case 8: return expand_lines_t<O, 8, 1>(p, s);
+                default: return expand_lines_t<O, 16, 1>(p, s);
+            }
+        }
+    }
+    const int nb = lora_nb(p.r), mt = lora_mt(p.rows, nb, 4);
     switch (nb) {
         case 1: return mt == 1 ? expand_t<T, O, 1, 1>(p, s) : expand_t<T, O, 1, 4>(p, s);
         case 2: return mt == 1 ? expand_t<T, O, 2, 1>(p, s) : expand_t<T, O, 2, 4>(p, s);
@@ -762,14 +1274,20 @@ hipError_t launch_lora_expand(const lora::Expand& p, bool bf16, bool out_bf16, h
     return out_bf16 ? expand_nb<float, uint16_t>(p, s) : expand_nb<float, float>(p, s);
 }
 
-hipError_t launch_lora_turn(const void* a, void* at, bool bf16, int g, int rows, int cols, hipStream_t s) {
-    const int64_t tr = up64(rows, 32), tc = up64(cols, 32), blocks = tr * tc * g;
+static lora::Turn turn_of(const void* a, void* at, int rows, int cols) {
+    int lg = 4;
+    while (lg < 8 && (1 << lg) < cols && (4096 >> lg) > rows) ++lg;
+    while (lg < 6 && (1 << lg) < cols) ++lg;
+    return {a, at, rows, cols, lg, (int)up64(rows, 4096 >> lg), (int)up64(cols, 1 << lg)};
+}
+hipError_t launch_lora_turn(const void* a, void* at, int rows, int cols, const void* b, void* bt, int rows_b, int cols_b, bool bf16, int g,
+                            hipStream_t s) {
+    const lora::Turn p = turn_of(a, at, rows, cols), q = turn_of(b, bt, rows_b, cols_b);
+    const int64_t first = a ? (int64_t)p.tr * p.tc * g : 0, blocks = first + (b ? (int64_t)q.tr * q.tc * g : 0);
     if (blocks == 0) return hipSuccess;
     if (blocks > kMaxBlocks) return hipErrorInvalidConfiguration;
-    if (bf16)
-        hipLaunchKernelGGL(lora::turn<uint16_t>, dim3((uint32_t)blocks), dim3(lora::NT), 0, s, (const uint16_t*)a, (uint16_t*)at, rows, cols, (int)tr, (int)tc);
-    else
-        hipLaunchKernelGGL(lora::turn<float>, dim3((uint32_t)blocks), dim3(lora::NT), 0, s, (const float*)a, (float*)at, rows, cols, (int)tr, (int)tc);
+    if (bf16) hipLaunchKernelGGL(lora::turn<uint16_t>, dim3((uint32_t)blocks), dim3(lora::NT), 0, s, p, q, (int)first);
+    else hipLaunchKernelGGL(lora::turn<float>, dim3((uint32_t)blocks), dim3(lora::NT), 0, s, p, q, (int)first);
     return hipGetLastError();
 }
 
@@ -798,9 +1316,11 @@ hipError_t launch_lora_outer(const lora::Outer& p, bool bf16, hipStream_t s) {
     if (e != hipSuccess) return e;
     const int64_t per = (int64_t)(p.k + p.n) * p.r;
     if (per == 0) return hipSuccess;
-    const int blocks = (int)std::min<int64_t>(up64(per, lora::NT * 4), std::max<int64_t>(1, 4096 / p.g));
+    const bool four = (int64_t)p.k * p.r % 4 == 0 && (int64_t)p.n * p.r % 4 == 0;   // neither matrix ends inside a thread's values
+    const int blocks = (int)std::min<int64_t>(up64(per, lora::NT * (four ? 4 : 1)), std::max<int64_t>(1, 4096 / p.g));
     if ((int64_t)blocks * p.g > kMaxBlocks) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL(lora::join, dim3((uint32_t)(blocks * p.g)), dim3(lora::NT), 0, s, p, blocks);
+    if (four) hipLaunchKernelGGL(lora::join<4>, dim3((uint32_t)(blocks * p.g)), dim3(lora::NT), 0, s, p, blocks);
+    else hipLaunchKernelGGL(lora::join<1>, dim3((uint32_t)(blocks * p.g)), dim3(lora::NT), 0, s, p, blocks);
     return hipGetLastError();
 }
 
