@@ -646,6 +646,13 @@ def _scratch(op, m, k, n, g, capacity, in_dtype, dev, workspace):
     return torch.empty(need, dtype=torch.uint8, device=dev)
 
 
+def _like(t, rows, cols, dtype):
+    """A new [rows, cols]; in t's image where that has the shape, which takes two thirds of the time."""
+    if t is not None and t.dtype is dtype and t.shape == (rows, cols) and t.is_contiguous():
+        return torch.empty_like(t)
+    return torch.empty(rows, cols, dtype=dtype, device=t.device if t is not None else None)
+
+
 # ---------------------------------------------------------------------------------------
 # 8-bit activation checkpoints: codes (torch.float8_e4m3fn, or uint8 bytes) and E8M0 scales (uint8 [rows, k/32])
 
@@ -670,11 +677,11 @@ def _rows(t, name, device, shape=None, dtype=None, dtypes=None):
 def _codes8(out, rows, k, dev):
     codes, scale = out
     if codes is None:
-        codes = torch.empty((rows, k), dtype=torch.float8_e4m3fn, device=dev)
+        codes = torch.empty(rows, k, dtype=torch.float8_e4m3fn, device=dev)
     else:
         _tensor(codes, "codes", dev, (rows, k), dtypes=_E4M3)
     if scale is None:
-        scale = torch.empty((rows, k // 32), dtype=torch.uint8, device=dev)
+        scale = torch.empty(rows, k // 32, dtype=torch.uint8, device=dev)
     else:
         _tensor(scale, "scale", dev, (rows, k // 32), torch.uint8)
     return codes, scale
@@ -708,9 +715,12 @@ def mxfp8_dequantize(codes, scale, out=None, out_dtype=None):
         raise ValueError("codes must be [rows, k] with k % 32 == 0")
     rows, k = codes.shape
     _checkpoint(codes, scale, dev, rows, k)
-    if out_dtype is None:
-        out_dtype = out.dtype if out is not None else torch.bfloat16
-    out = _out(out, "out", dev, (rows, k), out_dtype)
+    if out is None:
+        out = torch.empty(rows, k, dtype=out_dtype or torch.bfloat16, device=dev)
+        if out.dtype not in _FLOATS:
+            raise ValueError(f"out_dtype must be one of {_FLOATS}")
+    else:
+        out = _out(out, "out", dev, (rows, k), out_dtype)
     _call("mxfp8_dequantize", dev, codes.data_ptr(), scale.data_ptr(), out.data_ptr(), rows, k, GG_DT[out.dtype])
     return out
 
@@ -729,9 +739,13 @@ def gated_act_mxfp8(gate, up, act="silu", out=None, out_dtype=None):
     if act not in ACT:
         raise ValueError(f"act must be one of {sorted(ACT)}")
     h, codes, scale = out if out is not None else (None, None, None)
-    if out_dtype is None:
-        out_dtype = h.dtype if h is not None else gate.dtype
-    h = _out(h, "h", dev, (m, n), out_dtype)
+    if h is None:
+        out_dtype = out_dtype or gate.dtype
+        if out_dtype not in _FLOATS:
+            raise ValueError(f"out_dtype must be one of {_FLOATS}")
+        h = _like(gate, m, n, out_dtype)
+    else:
+        h = _out(h, "h", dev, (m, n), out_dtype)
     codes, scale = _codes8((codes, scale), m, 2 * n, dev)
     _call("gated_act_mxfp8", dev, gate.data_ptr(), up.data_ptr(), h.data_ptr(), codes.data_ptr(), scale.data_ptr(), m, n,
           stride, ACT[act], GG_DT[gate.dtype], GG_DT[h.dtype])
@@ -826,7 +840,7 @@ def ragged_lora(x, a, b, group_sizes=None, base=None, row_group=None, scaling=No
     base_stride = n if base is None else _rows(base, "base", dev, (m, n), out_dtype)
     out_stride = n
     if out is None:
-        out = torch.empty((m, n), dtype=out_dtype, device=dev)
+        out = _like(base if base is not None else x, m, n, out_dtype)
     else:
         out_stride = _rows(out, "out", dev, (m, n), out_dtype)
     ws = _scratch("lora", m, k, n, g, r, dtype, dev, workspace)
@@ -872,7 +886,7 @@ def ragged_lora_grad(x, v, dout, a, b, group_sizes, dbase=None, scaling=None, x_
         _tensor(dbase, "dbase", dev, (m, k), dtype)
     if need_dx:
         if dx is None:
-            dx = torch.empty((m, k), dtype=dtype, device=dev)
+            dx = torch.empty(m, k, dtype=dtype, device=dev)
         else:
             _tensor(dx, "dx", dev, (m, k), dtype)
     if grad_dtype is None:
@@ -880,8 +894,8 @@ def ragged_lora_grad(x, v, dout, a, b, group_sizes, dbase=None, scaling=None, x_
         grad_dtype = given[0] if given else torch.float32
     if grad_dtype not in _FLOATS:
         raise ValueError(f"grad_dtype must be one of {_FLOATS}")
-    da = _out(da, "da", dev, (g, r, k), grad_dtype)
-    db = _out(db, "db", dev, (g, n, r), grad_dtype)
+    da = torch.empty(g, r, k, dtype=grad_dtype, device=dev) if da is None else _out(da, "da", dev, (g, r, k), grad_dtype)
+    db = torch.empty(g, n, r, dtype=grad_dtype, device=dev) if db is None else _out(db, "db", dev, (g, n, r), grad_dtype)
     ws = _scratch("lora_grad", m, k, n, g, r, dtype, dev, workspace)
     _call("ragged_lora_grad", dev, x.data_ptr(), _p(x_scale), v.data_ptr(), dout.data_ptr(), a.data_ptr(), b.data_ptr(), sizes, sc,
           _p(dbase), _p(dx), da.data_ptr(), db.data_ptr(), m, k, n, r, g, GG_DT[x.dtype], GG_DT[dtype], GG_DT[grad_dtype],

@@ -770,6 +770,10 @@ gg_status ragged_lora(const void* x, const void* a, const void* b, const int32_t
     const int splits = gg::lora_splits(m, k, r, g);
     float* t = splits == 1 && v ? v : (float*)((char*)workspace + kHeader);
     gg::lora::Shrink sh{rows, x, a, t, x_stride, (int)k, r, splits};
+    if (gg::lora_both_ok(sh, dtype == GG_DT_BF16)) {
+        const gg::lora::Expand ex{rows, nullptr, b, scaling, base, out, v, base_stride, out_stride, (int)n, r, 0, 0, 0};
+        return launched(gg::launch_lora_both(sh, ex, dtype == GG_DT_BF16, out_dtype == GG_DT_BF16, (hipStream_t)stream));
+    }
     hipError_t e = gg::launch_lora_shrink(sh, dtype == GG_DT_BF16, (hipStream_t)stream);
     if (e != hipSuccess) return launched(e);
     rows.status = nullptr;
@@ -820,7 +824,8 @@ gg_status ragged_lora_grad(const void* x, const uint8_t* x_scale, const float* v
     hipError_t e = gg::launch_lora_turn(b, ws + w.bt, (int)n, r, dx ? a : nullptr, ws + w.at, r, (int)k, bf16, g, s);
     if (e != hipSuccess) return launched(e);
     gg::lora::Shrink sh{rows, dout, ws + w.bt, t, n, (int)n, r, splits};
-    e = gg::launch_lora_shrink(sh, bf16, s);
+    const bool both = gg::lora_both_ok(sh, bf16);
+    if (!both) e = gg::launch_lora_shrink(sh, bf16, s);
     if (e != hipSuccess) return launched(e);
     gg::lora::Expand ex{rows, t, ws + w.at, scaling, dbase, dx, splits > 1 ? u : nullptr, k, k, dx ? (int)k : 0, r, splits, 0, 0};
     gg::lora::Outer o{};
@@ -829,9 +834,14 @@ gg_status ragged_lora_grad(const void* x, const uint8_t* x_scale, const float* v
     o.m = (int)m; o.k = (int)k; o.n = (int)n; o.r = r; o.g = g; o.chunk = gg::lora_chunk(m, k, n); o.grads_bf16 = grad_dtype == GG_DT_BF16;
     // With splits the expand sums them, so it goes first (without dx it does only that).  Without, the row sums read
     // dout again, from its end, while the last-level cache still holds that.
-    if (splits > 1) e = gg::launch_lora_expand(ex, bf16, bf16, s);
+    if (both) {
+        ex.v = u;
+        e = gg::launch_lora_both(sh, ex, bf16, bf16, s);
+    } else if (splits > 1) {
+        e = gg::launch_lora_expand(ex, bf16, bf16, s);
+    }
     if (e == hipSuccess) e = gg::launch_lora_outer(o, bf16, s);
-    if (e == hipSuccess && splits == 1 && dx) e = gg::launch_lora_expand(ex, bf16, bf16, s);
+    if (e == hipSuccess && !both && splits == 1 && dx) e = gg::launch_lora_expand(ex, bf16, bf16, s);
     return launched(e);
 }
 

@@ -27,7 +27,7 @@ namespace lora {
 
 constexpr int NT = 256;
 constexpr int KC = 64;           // elements of the long axis that a wave takes at a time
-constexpr int MAXCHUNK = 1024;   // rows in any order: of these many, a workgroup takes those of its adapter
+constexpr int MA1024UNK = 1024;   // rows in any order: of these many, a workgroup takes those of its adapter
 
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -50,6 +50,14 @@ template <> struct Frag<uint16_t> {
             if (e < valid) q[e >> 1] |= (int)((uint32_t)p[e] << (16 * (e & 1)));
         v = __builtin_bit_cast(bf16x8, q);
     }
+    // load_part where the eight lie before `end`, the array's: what is loaded past `valid` is masked
+    __device__ void load_tail(const uint16_t* p, int valid, const uint16_t* end) {
+        if (p + 8 > end) { load_part(p, valid); return; }
+        i32x4 q = *(const i32x4_any*)p;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) q[d] &= valid >= 2 * d + 2 ? -1 : valid == 2 * d + 1 ? 0xffff : 0;
+        v = __builtin_bit_cast(bf16x8, q);
+    }
     __device__ static f32x4 mma(const Frag& a, const Frag& b, f32x4 c) {
         return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v, b.v, c, 0, 0, 0);
     }
@@ -63,6 +71,15 @@ template <> struct Frag<float> {
         for (int e = 0; e < 4; ++e) {
             lo[e] = e < valid ? p[e] : 0.f;
             hi[e] = e + 4 < valid ? p[e + 4] : 0.f;
+        }
+    }
+    __device__ void load_tail(const float* p, int valid, const float* end) {
+        if (p + 8 > end) { load_part(p, valid); return; }
+        load(p);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (e >= valid) lo[e] = 0.f;
+            if (e + 4 >= valid) hi[e] = 0.f;
         }
     }
     __device__ static f32x4 mma(const Frag& a, const Frag& b, f32x4 c) {
@@ -88,7 +105,7 @@ __device__ inline void split(float x, uint16_t (&out)[P]) {
 
 // Which rows a workgroup has: `rows` of adapter h (-1: rows without one), row i being first + i or list[i].
 struct RowTile { int h, rows, first; const int* list; };
-struct RowList { int list[MAXCHUNK]; int wave[4]; };
+struct RowList { int list[MA1024UNK]; int wave[4]; };
 
 // tile `id` of the rows behind the last adapter's
 __device__ inline RowTile behind(const Rows& p, int covered, int id, int tm) {
@@ -306,26 +323,22 @@ __device__ inline void load_lds16_at(const char* p, uint32_t lds) {
     asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" :: "s"(lds), "v"(p) : "memory", "m0");
 }
 
-template <typename T, int NB, int TEAM, int D>
-__global__ __launch_bounds__(NT) void shrink_ring(Shrink p) {
-    constexpr int TM = 16 * TEAM, WB = TEAM == 4 && NB < 2 ? 2 : NB;   // blocks of 16 weight rows in a slot
-    constexpr int SLOT = (TM + 16 * WB) * 128, PER = (TM + 16 * WB) / 8 / TEAM;   // bytes; loads a wave
-    constexpr int KE = 128 / sizeof(T), STEPS = sizeof(T) == 2 ? 2 : 1, RINGS = 4 / TEAM;
+// One tile of rows r0 .. of a ring: on return `acc` is the wave's 16 rows' (TEAM = 4) or, in wave 0, the 16 rows' sums
+// over the pieces c0 .. c1 - 1 of the axis.  All waves call it together; the rings may be used again after a barrier.
+template <typename T, int NB, int TEAM, int D> struct Ring {
+    static constexpr int TM = 16 * TEAM, WB = TEAM == 4 && NB < 2 ? 2 : NB;   // rows; blocks of 16 weight rows in a slot
+    static constexpr int SLOT = (TM + 16 * WB) * 128, PER = (TM + 16 * WB) / 8 / TEAM;   // bytes; loads a wave
+    static constexpr int KE = 128 / sizeof(T), STEPS = sizeof(T) == 2 ? 2 : 1, RINGS = 4 / TEAM, BYTES = RINGS * D * SLOT;
     static_assert(PER * (D - 1) <= 63, "vmcnt range");
-    static_assert(RINGS * D * SLOT >= (RINGS > 1 ? 2 * NB * 64 * 16 : 0), "the sums of the waves fit the rings");
-    __shared__ RowList rs;
-    __shared__ __attribute__((aligned(128))) char rings[RINGS][D * SLOT];
-    static_assert(sizeof(rings) >= sizeof(Tables), "the rings hold the tables first");
-    const RowTile w = row_tile(p.rows, blockIdx.x, TM, rs, rings);
-    if (w.h < 0 || w.rows == 0) return;
-    const int t = threadIdx.x, l = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6), q = l >> 4, i16 = l & 15;
-    const int mate = TEAM == 4 ? wave : 0, ring_id = TEAM == 4 ? 0 : wave;
-    const int nch = (p.k + KE - 1) / KE, per = (nch + (int)gridDim.y - 1) / (int)gridDim.y;
-    const int c0 = blockIdx.y * per, c1 = min(nch, c0 + per), whole = min(c1, p.k / KE);
-    const int count = max(0, whole - c0 - (TEAM == 4 ? 0 : wave) + (RINGS - 1)) / RINGS;   // this ring's pieces: every RINGS-th
-    const char* ring = rings[ring_id];
-    const uint32_t lds = ring::lds_u32(ring);
-    for (int r0 = 0; r0 < w.rows; r0 += TM) {
+    static_assert(BYTES >= (RINGS > 1 ? 2 * NB * 64 * 16 : 0), "the sums of the waves fit the rings");
+    static_assert(BYTES >= (int)sizeof(Tables), "the rings hold the tables first");
+    __device__ static void run(f32x4 (&acc)[NB], char* rings, const Shrink& p, const RowTile& w, int r0, int c0, int c1) {
+        const int t = threadIdx.x, l = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6), q = l >> 4, i16 = l & 15;
+        const int mate = TEAM == 4 ? wave : 0, alone = TEAM == 4 ? 0 : wave;
+        const int whole = min(c1, p.k / KE);
+        const int count = max(0, whole - c0 - alone + (RINGS - 1)) / RINGS;   // this ring's pieces: every RINGS-th
+        const char* ring = rings + alone * (D * SLOT);
+        const uint32_t lds = ring::lds_u32(ring);
         // load u of this wave: rows 8 (PER mate + u) .. + 7 of the slot, x's first and then the weights'
         const char* src[PER];
 #pragma unroll
@@ -333,7 +346,7 @@ __global__ __launch_bounds__(NT) void shrink_ring(Shrink p) {
             const int row = 8 * (PER * mate + u) + (l >> 3), piece = 16 * ((l & 7) ^ ((row >> 1) & 7));
             const T* at = row < TM ? (const T*)p.x + (int64_t)row_at(w, min(r0 + row, w.rows - 1)) * p.stride
                                    : (const T*)p.w + ((int64_t)w.h * p.r + min(row - TM, p.r - 1)) * p.k;
-            src[u] = (const char*)(at + (int64_t)(c0 + (TEAM == 4 ? 0 : wave)) * KE) + piece;
+            src[u] = (const char*)(at + (int64_t)(c0 + alone) * KE) + piece;
         }
         auto issue = [&](int i, int slot) {   // past the end: the last piece again, which no one reads
             const int64_t off = (int64_t)min(i, count - 1) * (RINGS * 128);
@@ -341,10 +354,8 @@ __global__ __launch_bounds__(NT) void shrink_ring(Shrink p) {
             for (int u = 0; u < PER; ++u)
                 load_lds16_at(src[u] + off, __builtin_amdgcn_readfirstlane(lds + slot * SLOT + (PER * mate + u) * 1024));
         };
-        f32x4 acc[NB];
 #pragma unroll
         for (int b = 0; b < NB; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (r0 > 0 || w.list) ring::lds_barrier();   // the list and the last tile's sums have been read
         if (count > 0) {
 #pragma unroll
             for (int d = 0; d < D - 1; ++d) issue(d, d);
@@ -365,8 +376,7 @@ __global__ __launch_bounds__(NT) void shrink_ring(Shrink p) {
             }
         }
         ring::wait_vm<0>();
-        const bool tail = c0 <= whole && whole < c1;
-        if (tail && (TEAM == 4 || (whole - c0) % RINGS == wave)) {   // the piece that the axis ends in
+        if (c0 <= whole && whole < c1 && (TEAM == 4 || (whole - c0) % RINGS == wave)) {   // the piece that the axis ends in
 #pragma unroll
             for (int s = 0; s < STEPS; ++s) {
                 const int e0 = whole * KE + 32 * s + 8 * q, valid = p.k - e0;
@@ -381,7 +391,7 @@ __global__ __launch_bounds__(NT) void shrink_ring(Shrink p) {
             }
         }
         if constexpr (RINGS > 1) {   // waves 2 and 3 to 0 and 1, then 1 to 0
-            f32x4* red = (f32x4*)&rings[0][0];
+            f32x4* red = (f32x4*)rings;
             __syncthreads();
 #pragma unroll
             for (int half = 2; half >= 1; half >>= 1) {
@@ -394,10 +404,26 @@ __global__ __launch_bounds__(NT) void shrink_ring(Shrink p) {
                     for (int b = 0; b < NB; ++b) acc[b] += red[(wave * NB + b) * 64 + l];
                 __syncthreads();
             }
-            if (wave > 0) continue;
         }
-        const int row = r0 + 16 * mate + i16;
-        if (row >= w.rows) continue;
+    }
+};
+
+template <typename T, int NB, int TEAM, int D>
+__global__ __launch_bounds__(NT) void shrink_ring(Shrink p) {
+    using R = Ring<T, NB, TEAM, D>;
+    __shared__ RowList rs;
+    __shared__ __attribute__((aligned(128))) char rings[R::BYTES];
+    const RowTile w = row_tile(p.rows, blockIdx.x, R::TM, rs, rings);
+    if (w.h < 0 || w.rows == 0) return;
+    const int l = threadIdx.x & 63, wave = threadIdx.x >> 6, q = l >> 4;
+    const int nch = (p.k + R::KE - 1) / R::KE, per = (nch + (int)gridDim.y - 1) / (int)gridDim.y;
+    const int c0 = blockIdx.y * per, c1 = min(nch, c0 + per);
+    for (int r0 = 0; r0 < w.rows; r0 += R::TM) {
+        if (r0 > 0 || w.list) ring::lds_barrier();   // the list and the last tile's sums have been read
+        f32x4 acc[NB];
+        R::run(acc, rings, p, w, r0, c0, c1);
+        const int row = r0 + (TEAM == 4 ? 16 * wave : 0) + (l & 15);
+        if ((TEAM == 1 && wave > 0) || row >= w.rows) continue;
         float* to = p.t + ((int64_t)blockIdx.y * p.rows.m + row_at(w, row)) * p.r;
 #pragma unroll
         for (int b = 0; b < NB; ++b)
@@ -452,34 +478,127 @@ template <typename T, int NB> struct Narrow {
     static constexpr int PITCH = PARTS * 32 * STEPS + (sizeof(T) == 2 ? 8 : 4);
 };
 
+// Columns col0 .. col1 - 1 of rows r0 .. of a tile, whose t is in `nar`; a strip of 16 rows of 64 columns a wave turns
+// results into whole lines.
+constexpr int SP = 64 + 4;
+struct Strips { __attribute__((aligned(16))) float of[4][16 * SP]; };
+template <typename T, typename O, int NB, int MT, bool WHOLE>   // WHOLE: r % 8 == 0
+__device__ inline void columns(const Expand& p, const RowTile& w, int r0, int col0, int col1, const T* nar, Strips& strips) {
+    using N = Narrow<T, NB>;
+    constexpr int PITCH = N::PITCH, STEPS = N::STEPS, PARTS = N::PARTS;
+    const int t = threadIdx.x, l = t & 63, wave = t >> 6, q = l >> 4, i16 = l & 15;
+    const O* base = (const O*)p.base;
+    O* out = (O*)p.out;
+    const int last = (p.r + 7) / 8 - 1;                 // the last eight of r
+    const T* wb = (const T*)p.w + (int64_t)w.h * p.n * p.r;
+    // a wave: 64 columns of all rows at a time, the next ones' base on its way
+    auto fetch = [&](Out8<O> (&o)[MT][2], int c) {
+#pragma unroll
+        for (int a = 0; a < MT; ++a)
+#pragma unroll
+            for (int d = 0; d < 2; ++d) {
+                const int i = r0 + 16 * a + 8 * d + (l >> 3), cc = c + 8 * (l & 7);
+                o[a][d].zero();
+                if (base && i < w.rows && cc + 8 <= col1) o[a][d].load(base + (int64_t)row_at(w, i) * p.base_stride + cc);
+            }
+    };
+    Out8<O> next[MT][2];
+    fetch(next, col0 + 64 * wave);
+    for (int c = col0 + 64 * wave; c < col1; c += 256) {
+        Out8<O> o[MT][2];
+#pragma unroll
+        for (int a = 0; a < MT; ++a) { o[a][0] = next[a][0]; o[a][1] = next[a][1]; }
+        Frag<T> m[4][STEPS];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const T* wr = wb + (int64_t)min(c + 16 * j + i16, p.n - 1) * p.r;
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) {
+                const int e = 8 * min(4 * s + q, last);   // past the end: times the zeros above
+                if (WHOLE) m[j][s].load(wr + e);
+                else m[j][s].load_tail(wr + e, p.r - e, (const T*)p.w + (int64_t)p.rows.g * p.n * p.r);
+            }
+        }
+        fetch(next, c + 256);
+#pragma unroll
+        for (int a = 0; a < MT; ++a) {
+            f32x4 acc[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+                for (int z = 0; z < PARTS; ++z) {
+                    Frag<T> x;
+                    x.load_lds(nar + (16 * a + i16) * PITCH + 32 * (STEPS * z + s) + 8 * q);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[j] = Frag<T>::mma(m[j][s], x, acc[j]);
+                }
+            float* strip = strips.of[wave];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) *(f32x4*)(strip + i16 * SP + 16 * j + 4 * q) = acc[j];
+#pragma unroll
+            for (int d = 0; d < 2; ++d) {
+                const int i = r0 + 16 * a + 8 * d + (l >> 3), cc = c + 8 * (l & 7);
+                const float* from = strip + (8 * d + (l >> 3)) * SP + 8 * (l & 7);
+                const f32x4 lo = *(const f32x4*)from, hi = *(const f32x4*)(from + 4);
+                if (i >= w.rows || cc >= col1) continue;
+                const int64_t row = row_at(w, i);
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) { v[e] = lo[e]; v[4 + e] = hi[e]; }
+                if (cc + 8 <= p.n) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) v[e] += o[a][d].get(e);
+                    Out8<O>::store(out + row * p.out_stride + cc, v);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (cc + e < p.n)
+                            Out8<O>::put(out + row * p.out_stride + cc + e, v[e] + (base ? Out8<O>::one(base + row * p.base_stride + cc + e) : 0.f));
+                }
+            }
+        }
+    }
+}
+// rows without an adapter: what was there.  E: what moves at once, O or whole 16 bytes of it; eight of a thread in flight
+template <typename O, typename E>
+__device__ inline void untouched(const Expand& p, const RowTile& w, int ct, int col0, int col1) {
+    constexpr int PER = sizeof(E) / sizeof(O);
+    if (p.v && ct == 0)
+        for (int e = threadIdx.x; e < w.rows * p.r; e += NT) p.v[(int64_t)row_at(w, e / p.r) * p.r + e % p.r] = 0.f;
+    if ((p.base == p.out && p.base_stride == p.out_stride) || col1 <= col0) return;
+    const uint32_t width = (uint32_t)(col1 - col0) / PER, total = (uint32_t)w.rows * width;
+    for (uint32_t e0 = threadIdx.x; e0 < total; e0 += 8 * NT) {
+        E v[8];
+        int64_t to[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const uint32_t e = min(e0 + NT * u, total - 1), i = e / width, c = (e - i * width) * PER + col0;
+            const int64_t row = row_at(w, (int)i);
+            to[u] = row * p.out_stride + c;
+            v[u] = p.base ? *(const E*)((const O*)p.base + row * p.base_stride + c) : E{};
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            if (e0 + NT * u < total) *(E*)((O*)p.out + to[u]) = v[u];
+    }
+}
+
 template <typename T, typename O, int NB, int MT, bool WHOLE>   // WHOLE: r % 8 == 0
 __global__ __launch_bounds__(NT) void expand(Expand p) {
     using N = Narrow<T, NB>;
     constexpr int TM = 16 * MT, PITCH = N::PITCH, STEPS = N::STEPS, PARTS = N::PARTS;
     __shared__ RowList rs;
     __shared__ __attribute__((aligned(16))) T nar[TM * PITCH];
-    constexpr int SP = 64 + 4;                          // 16 rows of 64 columns of a wave, on their way to whole lines
-    __shared__ __attribute__((aligned(16))) float strips[4][16 * SP];
+    __shared__ Strips strips;
     const int ct = blockIdx.x % p.col_tiles, id = blockIdx.x / p.col_tiles;
     static_assert(sizeof(strips) >= sizeof(Tables), "the strips hold the tables first");
-    const RowTile w = row_tile(p.rows, id, TM, rs, strips);
-    const int t = threadIdx.x, l = t & 63, wave = t >> 6, q = l >> 4, i16 = l & 15;
+    const RowTile w = row_tile(p.rows, id, TM, rs, &strips);
+    const int t = threadIdx.x;
     const int col0 = ct * p.cols, col1 = min(p.n, col0 + p.cols);
-    const O* base = (const O*)p.base;
-    O* out = (O*)p.out;
-    if (w.h < 0) {   // rows without an adapter: what was there
-        for (int i = 0; i < w.rows; ++i) {
-            const int64_t row = row_at(w, i);
-            if (p.v && ct == 0)
-                for (int j = t; j < p.r; j += NT) p.v[row * p.r + j] = 0.f;
-            if (base == out && p.base_stride == p.out_stride) continue;
-            for (int c = col0 + t; c < col1; c += NT) out[row * p.out_stride + c] = base ? base[row * p.base_stride + c] : (O)0;
-        }
-        return;
-    }
+    if (w.h < 0) { untouched<O, O>(p, w, ct, col0, col1); return; }
     const float scale = p.scaling ? p.scaling[w.h] : 1.f;
-    const int last = (p.r + 7) / 8 - 1;                 // the last eight of r
-    const T* wb = (const T*)p.w + (int64_t)w.h * p.n * p.r;
     for (int r0 = 0; r0 < w.rows; r0 += TM) {
         if (r0) __syncthreads();
         for (int e0 = 0; e0 < TM * 32 * STEPS; e0 += 8 * NT) {   // t: eight values of a thread in flight
@@ -521,75 +640,54 @@ __global__ __launch_bounds__(NT) void expand(Expand p) {
             }
         }
         __syncthreads();
-        // a wave: 64 columns of all rows at a time, the next ones' base on its way
-        auto fetch = [&](Out8<O> (&o)[MT][2], int c) {
+        columns<T, O, NB, MT, WHOLE>(p, w, r0, col0, col1, nar, strips);
+    }
+}
+
+// Both products of few rows an adapter in one launch: a workgroup contracts the whole long axis of its 16 rows by itself
+// and then takes its columns.  The first weights are read once for every `cols` columns, from L2, and there is no second
+// launch to wait for and no t in memory.
+struct Both { Shrink s; Expand e; };
+template <typename T, typename O, int NB, int D, bool WHOLE>
+__global__ __launch_bounds__(NT) void both(Both b) {
+    using R = Ring<T, NB, 1, D>;
+    using N = Narrow<T, NB>;
+    constexpr int PITCH = N::PITCH, STEPS = N::STEPS;
+    __shared__ RowList rs;
+    struct After { float t[16][16 * NB + 4]; __attribute__((aligned(16))) T nar[16 * PITCH]; Strips strips; };
+    __shared__ __attribute__((aligned(128))) char rings[R::BYTES > (int)sizeof(After) ? R::BYTES : sizeof(After)];
+    const Expand& p = b.e;
+    const int ct = blockIdx.x % p.col_tiles, id = blockIdx.x / p.col_tiles;
+    const RowTile w = row_tile(p.rows, id, 16, rs, rings);
+    const int t = threadIdx.x, l = t & 63, wave = t >> 6, q = l >> 4;
+    const int col0 = ct * p.cols, col1 = min(p.n, col0 + p.cols);
+    if (w.h < 0) { untouched<O, O>(p, w, ct, col0, col1); return; }
+    const float scale = p.scaling ? p.scaling[w.h] : 1.f;
+    After& a = *(After*)rings;
+    for (int r0 = 0; r0 < w.rows; r0 += 16) {
+        __syncthreads();
+        f32x4 acc[NB];
+        R::run(acc, rings, b.s, w, r0, 0, (b.s.k + R::KE - 1) / R::KE);
+        if (wave == 0)
 #pragma unroll
-            for (int a = 0; a < MT; ++a)
-#pragma unroll
-                for (int d = 0; d < 2; ++d) {
-                    const int i = r0 + 16 * a + 8 * d + (l >> 3), cc = c + 8 * (l & 7);
-                    o[a][d].zero();
-                    if (base && i < w.rows && cc + 8 <= col1) o[a][d].load(base + (int64_t)row_at(w, i) * p.base_stride + cc);
-                }
-        };
-        Out8<O> next[MT][2];
-        fetch(next, col0 + 64 * wave);
-        for (int c = col0 + 64 * wave; c < col1; c += 256) {
-            Out8<O> o[MT][2];
-#pragma unroll
-            for (int a = 0; a < MT; ++a) { o[a][0] = next[a][0]; o[a][1] = next[a][1]; }
-            Frag<T> m[4][STEPS];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const T* wr = wb + (int64_t)min(c + 16 * j + i16, p.n - 1) * p.r;
-#pragma unroll
-                for (int s = 0; s < STEPS; ++s) {
-                    const int e = 8 * min(4 * s + q, last);   // past the end: times the zeros above
-                    if (WHOLE) m[j][s].load(wr + e);
-                    else m[j][s].load_part(wr + e, p.r - e);
-                }
-            }
-            fetch(next, c + 256);
-#pragma unroll
-            for (int a = 0; a < MT; ++a) {
-                f32x4 acc[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int s = 0; s < STEPS; ++s)
-#pragma unroll
-                    for (int z = 0; z < PARTS; ++z) {
-                        Frag<T> x;
-                        x.load_lds(nar + (16 * a + i16) * PITCH + 32 * (STEPS * z + s) + 8 * q);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) acc[j] = Frag<T>::mma(m[j][s], x, acc[j]);
-                    }
-                float* strip = strips[wave];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) *(f32x4*)(strip + i16 * SP + 16 * j + 4 * q) = acc[j];
-#pragma unroll
-                for (int d = 0; d < 2; ++d) {
-                    const int i = r0 + 16 * a + 8 * d + (l >> 3), cc = c + 8 * (l & 7);
-                    const float* from = strip + (8 * d + (l >> 3)) * SP + 8 * (l & 7);
-                    const f32x4 lo = *(const f32x4*)from, hi = *(const f32x4*)(from + 4);
-                    if (i >= w.rows || cc >= col1) continue;
-                    const int64_t row = row_at(w, i);
-                    float v[8];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) { v[e] = lo[e]; v[4 + e] = hi[e]; }
-                    if (cc + 8 <= p.n) {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] += o[a][d].get(e);
-                        Out8<O>::store(out + row * p.out_stride + cc, v);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            if (cc + e < p.n)
-                                Out8<O>::put(out + row * p.out_stride + cc + e, v[e] + (base ? Out8<O>::one(base + row * p.base_stride + cc + e) : 0.f));
-                    }
-                }
+            for (int i = 0; i < NB; ++i) *(f32x4*)&a.t[l & 15][16 * i + 4 * q] = acc[i];
+        __syncthreads();
+        for (int e = t; e < 16 * 32 * STEPS; e += NT) {
+            const int i = e / (32 * STEPS), j = e % (32 * STEPS);
+            const bool have = r0 + i < w.rows && j < p.r;
+            const float s = have ? a.t[i][j] : 0.f;
+            if (have && p.v && ct == 0) p.v[(int64_t)row_at(w, r0 + i) * p.r + j] = s;
+            if constexpr (N::PARTS == 2) {
+                uint16_t two[2];
+                split<2>(s * scale, two);
+                a.nar[i * PITCH + j] = two[0];
+                a.nar[i * PITCH + 32 * STEPS + j] = two[1];
+            } else {
+                a.nar[i * PITCH + j] = s * scale;
             }
         }
+        __syncthreads();
+        columns<T, O, NB, 1, WHOLE>(p, w, r0, col0, col1, a.nar, a.strips);
     }
 }
 
@@ -627,7 +725,6 @@ __global__ __launch_bounds__(NT) void expand_lines(Expand p) {
     constexpr int STEPS = NB < 2 ? 1 : NB / 2, TM = 64 * MT, PITCH = 64 * STEPS + 8;   // PITCH: [high | low] of a row of t
     constexpr int ROWB = 64 * STEPS, SLOT = 64 * ROWB;           // bytes of a column's weights, of 64 columns'
     constexpr int WL = (64 * 2 * NB + NT - 1) / NT;              // 16-byte loads a thread of 64 columns' weights
-    constexpr int SP = 64 + 4;
     __shared__ union {
         Tables tab;
         __attribute__((aligned(16))) uint16_t nar[TM * PITCH];
@@ -639,20 +736,7 @@ __global__ __launch_bounds__(NT) void expand_lines(Expand p) {
     const int t = threadIdx.x, l = t & 63, wave = t >> 6, q = l >> 4, i16 = l & 15;
     const int col0 = ct * p.cols, col1 = min(p.n, col0 + p.cols);
     constexpr uint32_t os = sizeof(O);
-    if (w.h < 0) {   // rows without an adapter: what was there
-        if (p.v && ct == 0)
-            for (int i = 0; i < w.rows; ++i)
-                for (int j = t; j < p.r; j += NT) p.v[(int64_t)row_at(w, i) * p.r + j] = 0.f;
-        if (p.base == p.out && p.base_stride == p.out_stride) return;
-        const int lines = (col1 - col0) * (int)os / 16;
-        for (int i = t / 64; i < w.rows; i += 4) {
-            const int64_t row = row_at(w, i);
-            const i32x4* from = (const i32x4*)((const O*)p.base + row * p.base_stride + col0);
-            i32x4* to = (i32x4*)((O*)p.out + row * p.out_stride + col0);
-            for (int c = l; c < lines; c += 64) to[c] = p.base ? from[c] : i32x4{0, 0, 0, 0};
-        }
-        return;
-    }
+    if (w.h < 0) { untouched<O, i32x4>(p, w, ct, col0, col1); return; }
     const float scale = p.scaling ? p.scaling[w.h] : 1.f;
     const int pieces = p.r / 8;                                  // 16-byte pieces of a column's weights
     const ring::rsrc_t rw = ring::make_rsrc((const uint16_t*)p.w + (int64_t)w.h * p.n * p.r, (uint32_t)p.n * p.r * 2u);
@@ -961,7 +1045,27 @@ __global__ __launch_bounds__(NT) void outer(Outer p) {
     if (blockIdx.x == 0 && threadIdx.x == 0 && p.status) *p.status = tab.flags;
     const int xt = (p.k + TC - 1) / TC, dt = (p.n + TC - 1) / TC;
     const int place = blockIdx.x / (xt + dt), id = tiles - 1 - place, ct = blockIdx.x - place * (xt + dt);   // from the end
-    if (id < 0) return;
+    if (id < 0) {
+        // With no more rows than a chunk every group with rows has one, join is not launched, and the places left over are
+        // the groups' without rows: h - tile_off[h] of them lie before group h.
+        const int e = -1 - id;
+        if (p.m > p.chunk || e >= p.g - tiles) return;
+        int lo = 0, hi = p.g - 1;   // the first h with more than e such groups up to it
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (mid + 1 - tab.tile_off[mid + 1] > e) hi = mid; else lo = mid + 1;
+        }
+        const bool in_x = ct < xt;
+        const int from = (in_x ? ct : ct - xt) * TC, width = min(TC, (in_x ? p.k : p.n) - from);
+        for (int i = threadIdx.x; i < width * p.r; i += NT) {
+            const int64_t at = in_x ? (int64_t)lo * p.r * p.k + (int64_t)(i / width) * p.k + from + i % width
+                                    : (int64_t)lo * p.n * p.r + (int64_t)from * p.r + i;
+            void* dst = in_x ? p.da : p.db;
+            if (p.grads_bf16) ((uint16_t*)dst)[at] = 0;
+            else ((float*)dst)[at] = 0.f;
+        }
+        return;
+    }
     const int h = find_group(tab.tile_off, p.g, id), part = id - tab.tile_off[h];
     const int first = tab.row_off[h] + part * p.chunk, rows = min(p.chunk, tab.row_off[h + 1] - first);
     const bool of_x = ct < xt;
@@ -1010,7 +1114,7 @@ __global__ __launch_bounds__(NT) void outer(Outer p) {
         auto step = [&](auto slot_c, int r0) {
             constexpr int slot = decltype(slot_c)::value;
             load(regs[slot], r0 + 64);
-            const E* wd = sm.wide[slot];
+                        const E* wd = sm.wide[slot];
             if constexpr (F32) {
 #pragma unroll
                 for (int s = 0; s < 8; ++s) {
@@ -1159,7 +1263,7 @@ int lora_splits(int64_t m, int64_t k, int r, int g) {
 int lora_chunk(int64_t m, int64_t k, int64_t n) {
     const int64_t tiles = up64(k, 256) + up64(n, 256);
     const int64_t c = up64(up64(m * tiles, 1024), 32) * 32;
-    return (int)std::min<int64_t>(2048, std::max<int64_t>(256, c));
+    return (int)std::min<int64_t>(2048, std::max<int64_t>(512, c));
 }
 
 // Rows a tile (16 MT): more where a group has that many on average.
@@ -1168,7 +1272,7 @@ static int lora_mt(const lora::Rows& r, int nb, int most) {
     return rows >= 32 ? (nb >= 8 ? 2 : most) : 1;
 }
 void lora_rows(lora::Rows& r) {
-    r.chunk = (int)std::min<int64_t>(lora::MAXCHUNK, std::max<int64_t>(256, up64((int64_t)32 * r.g, 256) * 256));
+    r.chunk = (int)std::min<int64_t>(lora::MA1024UNK, std::max<int64_t>(256, up64((int64_t)32 * r.g, 256) * 256));
     r.slots = (int)std::min<int64_t>(r.g, std::min<int64_t>(r.m, r.chunk));
 }
 static int64_t lora_tiles(const lora::Rows& r, int tm) {
@@ -1191,11 +1295,13 @@ static hipError_t shrink_ring_t(const lora::Shrink& p, hipStream_t s) {
     hipLaunchKernelGGL((lora::shrink_ring<T, NB, TEAM, D>), dim3((uint32_t)tiles, p.splits), dim3(lora::NT), 0, s, p);
     return hipGetLastError();
 }
+static bool shrink_lines(const lora::Shrink& p, int64_t es) {   // rows of whole 16 bytes
+    return (uintptr_t)p.x % 16 == 0 && (uintptr_t)p.w % 16 == 0 && p.stride * es % 16 == 0 && p.k * es % 16 == 0;
+}
 template <typename T>
 static hipError_t shrink_nb(const lora::Shrink& p, hipStream_t s) {
     const int nb = lora_nb(p.r), mt = lora_mt(p.rows, nb, 2);
-    const bool lines = (uintptr_t)p.x % 16 == 0 && (uintptr_t)p.w % 16 == 0 && p.stride * sizeof(T) % 16 == 0 && p.k * sizeof(T) % 16 == 0;
-    if (lines) {
+    if (shrink_lines(p, sizeof(T))) {
         switch (nb) {
             case 1: return mt == 1 ? shrink_ring_t<T, 1, 1, 4>(p, s) : shrink_ring_t<T, 1, 4, 5>(p, s);
             case 2: return mt == 1 ? shrink_ring_t<T, 2, 1, 3>(p, s) : shrink_ring_t<T, 2, 4, 5>(p, s);
@@ -1241,7 +1347,7 @@ static hipError_t expand_lines_t(lora::Expand p, hipStream_t s) {
 // expand_lines: 16-byte rows and ranks, and 32-bit offsets over an adapter's weights and over the rows of a tile (of a
 // chunk, in any order)
 template <typename O> static bool expand_lines_ok(const lora::Expand& p) {
-    const int64_t span = (p.rows.group_sizes ? 256 : lora::MAXCHUNK) * (int64_t)sizeof(O);
+    const int64_t span = (p.rows.group_sizes ? 256 : lora::MA1024UNK) * (int64_t)sizeof(O);
     return p.r % 8 == 0 && p.n % 8 == 0 && p.base_stride * sizeof(O) % 16 == 0 && p.out_stride * sizeof(O) % 16 == 0 &&
            (uintptr_t)p.base % 16 == 0 && (uintptr_t)p.out % 16 == 0 && (uintptr_t)p.w % 16 == 0 &&
            ((int64_t)p.n + 256) * p.r * 2 < (int64_t(1) << 31) && std::max(p.base_stride, p.out_stride) * span < (int64_t(1) << 31);
@@ -1260,7 +1366,8 @@ static hipError_t expand_nb(const lora::Expand& p, hipStream_t s) {
             }
         }
     }
-    const int nb = lora_nb(p.r), mt = lora_mt(p.rows, nb, 4);
+    // few rows and columns: small tiles (more workgroups, and half the instructions for each to fetch)
+    const int nb = lora_nb(p.r), mt = up64(p.rows.m, 64) * up64(p.n, 256) < 512 ? 1 : lora_mt(p.rows, nb, 4);
     switch (nb) {
         case 1: return mt == 1 ? expand_t<T, O, 1, 1>(p, s) : expand_t<T, O, 1, 4>(p, s);
         case 2: return mt == 1 ? expand_t<T, O, 2, 1>(p, s) : expand_t<T, O, 2, 4>(p, s);
@@ -1268,6 +1375,37 @@ static hipError_t expand_nb(const lora::Expand& p, hipStream_t s) {
         case 8: return mt == 1 ? expand_t<T, O, 8, 1>(p, s) : expand_t<T, O, 8, 2>(p, s);
         default: return expand_t<T, O, 16, 1>(p, s);
     }
+}
+// Few rows an adapter, rows of whole 16 bytes, and first weights of at most 128 KiB an adapter: both products in one launch.
+// (One token at rank 16 and 4096 columns: 7.2 us in one launch, 4.1 + 5.2 in two, and the host's 2.8 for the second; 96 rows at 64
+// adapters of 448 KiB: 20 us in one, since every workgroup streams the weights for itself, 6.9 + 6.8 in two.)
+bool lora_both_ok(const lora::Shrink& p, bool bf16) {
+    const int64_t es = bf16 ? 2 : 4;
+    return lora_mt(p.rows, 1, 4) == 1 && p.r <= 64 && p.r * (int64_t)p.k * es <= (1 << 17) && shrink_lines(p, es);
+}
+template <typename T, typename O, int NB, int D>
+static hipError_t both_t(const lora::Shrink& sh, lora::Expand p, hipStream_t s) {
+    const int64_t tiles = lora_tiles(p.rows, 16);
+    p.cols = 4096;
+    while (p.cols > 256 && tiles * up64(p.n, p.cols) < 256) p.cols /= 2;
+    p.col_tiles = (int)std::max<int64_t>(1, up64(p.n, p.cols));
+    if (tiles * p.col_tiles > kMaxBlocks) return hipErrorInvalidConfiguration;
+    const dim3 grid((uint32_t)(tiles * p.col_tiles));
+    if (p.r % 8 == 0) hipLaunchKernelGGL((lora::both<T, O, NB, D, true>), grid, dim3(lora::NT), 0, s, lora::Both{sh, p});
+    else hipLaunchKernelGGL((lora::both<T, O, NB, D, false>), grid, dim3(lora::NT), 0, s, lora::Both{sh, p});
+    return hipGetLastError();
+}
+template <typename T, typename O>
+static hipError_t both_nb(const lora::Shrink& sh, const lora::Expand& p, hipStream_t s) {
+    switch (lora_nb(p.r)) {
+        case 1: return both_t<T, O, 1, 4>(sh, p, s);
+        case 2: return both_t<T, O, 2, 3>(sh, p, s);
+        default: return both_t<T, O, 4, 3>(sh, p, s);
+    }
+}
+hipError_t launch_lora_both(const lora::Shrink& sh, const lora::Expand& p, bool bf16, bool out_bf16, hipStream_t s) {
+    if (bf16) return out_bf16 ? both_nb<uint16_t, uint16_t>(sh, p, s) : both_nb<uint16_t, float>(sh, p, s);
+    return out_bf16 ? both_nb<float, uint16_t>(sh, p, s) : both_nb<float, float>(sh, p, s);
 }
 hipError_t launch_lora_expand(const lora::Expand& p, bool bf16, bool out_bf16, hipStream_t s) {
     if (bf16) return out_bf16 ? expand_nb<uint16_t, uint16_t>(p, s) : expand_nb<uint16_t, float>(p, s);
@@ -1300,6 +1438,15 @@ static hipError_t outer_t(const lora::Outer& p, hipStream_t s) {
 }
 template <lora::Wide XW, int P>
 static hipError_t outer_nb(const lora::Outer& p, hipStream_t s) {
+    // few workgroups: narrower ones (375 rows of 5 groups in fp32, k 1030, n 515: 15.2 -> 10 us)
+    const int64_t groups = std::max<int64_t>(up64(p.m, p.chunk), std::min<int64_t>(p.g, up64(p.m, 32)));
+    if (p.r <= 64 && groups * (up64(p.k, 256) + up64(p.n, 256)) < 256) {
+        switch (lora_nb(p.r)) {
+            case 1: return outer_t<XW, 1, P, 1>(p, s);
+            case 2: return outer_t<XW, 2, P, 1>(p, s);
+            default: return outer_t<XW, 4, P, 1>(p, s);
+        }
+    }
     switch (lora_nb(p.r)) {
         case 1: return outer_t<XW, 1, P, 4>(p, s);
         case 2: return outer_t<XW, 2, P, 4>(p, s);
@@ -1315,7 +1462,7 @@ hipError_t launch_lora_outer(const lora::Outer& p, bool bf16, hipStream_t s) {
     else e = p.grads_bf16 ? outer_nb<lora::BF16, 2>(p, s) : outer_nb<lora::BF16, 3>(p, s);
     if (e != hipSuccess) return e;
     const int64_t per = (int64_t)(p.k + p.n) * p.r;
-    if (per == 0) return hipSuccess;
+    if (per == 0 || p.m <= p.chunk) return hipSuccess;   // no group has two chunks
     const bool four = (int64_t)p.k * p.r % 4 == 0 && (int64_t)p.n * p.r % 4 == 0;   // neither matrix ends inside a thread's values
     const int blocks = (int)std::min<int64_t>(up64(per, lora::NT * (four ? 4 : 1)), std::max<int64_t>(1, 4096 / p.g));
     if ((int64_t)blocks * p.g > kMaxBlocks) return hipErrorInvalidConfiguration;
