@@ -728,13 +728,13 @@ gg_status ragged_dot_k_mxfp8(const void* lhs, const uint8_t* lhs_scale, const vo
     if (!aligned(lhs, 16) || !aligned(dout, 2) || !aligned(out, elem_bytes(out_dtype))) return GG_ERR_MISALIGNED;
     int cus;
     if (device_cus(&cus) != 0) return GG_ERR_HIP;
-    const int64_t bound = (int64_t)g * cdiv64(k, 256) * cdiv64(n, 256);
+    const int64_t bound = (int64_t)g * cdiv64(k, 128) * cdiv64(n, 256);   // tiles of the smallest size
     if (!fits_i32(bound)) return GG_ERR_BAD_SHAPE;
     gg::KmxParams p{};
     p.lhs = (const uint8_t*)lhs; p.lhs_scale = lhs_scale; p.dout = (const uint16_t*)dout; p.group_sizes = group_sizes; p.out = out;
     p.status = (uint32_t*)workspace; p.m = (int)m; p.k = (int)k; p.n = (int)n; p.g = g; p.out_f32 = out_dtype == GG_DT_F32;
     p.alpha = alpha; p.beta = beta;
-    return gg::launch_ragged_k_mx(p, persistent_grid(bound, 1, cus), (hipStream_t)stream) == hipSuccess ? GG_OK : GG_ERR_HIP;
+    return gg::launch_ragged_k_mx(p, cus, (hipStream_t)stream) == hipSuccess ? GG_OK : GG_ERR_HIP;
 }
 
 gg_status ragged_lora(const void* x, const void* a, const void* b, const int32_t* group_sizes, const int32_t* row_group,

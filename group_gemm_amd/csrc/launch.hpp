@@ -151,7 +151,7 @@ struct KmxParams {                 // ragged_dot_k_mxfp8
     int out_f32;
     float alpha, beta;
 };
-hipError_t launch_ragged_k_mx(const KmxParams& p, int grid, hipStream_t s);   // 256 x 256 tiles
+hipError_t launch_ragged_k_mx(const KmxParams& p, int cus, hipStream_t s);   // 256 x 256 tiles
 
 // Low-rank adapters.
 constexpr int kMaxRank = 256;

@@ -260,8 +260,7 @@ def wgrad_case(seed, m, k, n, g):
 
 def check_wgrad(out, x, d, sizes, alpha=1.0, beta=0.0, old=None):
     at, m = 0, x.shape[0]
-    out = out if isinstance(out, np.ndarray) else (val(out), out.dtype)
-    got, dtype = out
+    got, dtype = out if isinstance(out, tuple) else (val(out), out.dtype)
     for h, s in enumerate(sizes):
         s = min(max(int(s), 0), m - at)
         a, b = x[at:at + s], d[at:at + s]
@@ -293,11 +292,45 @@ def test_weight_gradient(case, out_dtype):
     assert G.read_device_status(ws) == want
 
 
-@pytest.mark.parametrize("n", [264, 263])
+# whole 128 columns of k and whole 16 bytes of n: every count of 32-row slices up to the ring's wrap, long groups, tiles that
+# end inside a wave's part, several tiles a group
+RING = [(1, 128, 8, [1]), (300, 128, 264, [31, 32, 33, 64, 65, 75]), (500, 256, 256, [97, 128, 129, 146]), (700, 384, 520, [160, 161, 0, 379]),
+        (1500, 640, 72, [700, 0, 333, 400]), (900, 128, 1032, [225, 256, 257, 162]), (2100, 896, 312, [2100]), (64, 1152, 2064, [40, 24])]
+
+
 @pytest.mark.parametrize("out_dtype", [F32, BF])
-def test_weight_gradient_accumulates(n, out_dtype):
-    say("wgrad in place", n, out_dtype)
-    m, k, sizes = 150, 288, [70, 0, 80]
+@pytest.mark.parametrize("case", range(len(RING)))
+def test_weight_gradient_in_the_ring(case, out_dtype):
+    m, k, n, sizes = RING[case]
+    say("wgrad ring", RING[case], out_dtype)
+    codes, scale, dout, x, d = wgrad_case(20 + case, m, k, n, len(sizes))
+    gs = torch.tensor(sizes, dtype=torch.int32, device=DEV)
+    out, c = framed((len(sizes), k, n), out_dtype)
+    for alpha in (1.0, -0.5):
+        G.ragged_dot_k(codes, dout, gs, out=out, lhs_scale=scale, alpha=alpha)
+        c()
+        check_wgrad(out, x, d, sizes, alpha)
+
+
+def test_weight_gradient_past_32_bits():
+    """dout of more than 2 GiB: the last rows of a long group, and a short one behind it."""
+    say("wgrad long")
+    m, k, n = 66000, 128, 16392
+    codes, scale, dout = torch.zeros(m, k, dtype=torch.uint8, device=DEV), torch.zeros(m, 4, dtype=torch.uint8, device=DEV), torch.ones(m, n, dtype=BF, device=DEV)
+    c, s, _, x, _ = wgrad_case(70, 40, k, 8, 1)
+    codes[-40:], scale[-40:] = c.view(torch.uint8), s
+    sizes = [m - 10, 7]
+    out = G.ragged_dot_k(codes, dout, torch.tensor(sizes, dtype=torch.int32, device=DEV), lhs_scale=scale)
+    ones = np.ones((40, 16))
+    check_wgrad((val(out[:, :, -16:]), F32), x, ones, [30, 7])
+    check_wgrad((val(out[:, :, :16]), F32), x, ones, [30, 7])
+
+
+@pytest.mark.parametrize("k,n", [(256, 264), (288, 264), (288, 263)])
+@pytest.mark.parametrize("out_dtype", [F32, BF])
+def test_weight_gradient_accumulates(k, n, out_dtype):
+    say("wgrad in place", k, n, out_dtype)
+    m, sizes = 150, [70, 0, 80]
     codes, scale, dout, x, d = wgrad_case(50, m, k, n, 3)
     gs = torch.tensor(sizes, dtype=torch.int32, device=DEV)
     old = torch.randn(3, k, n, device=DEV).to(out_dtype)
@@ -306,10 +339,11 @@ def test_weight_gradient_accumulates(n, out_dtype):
     check_wgrad(out, x, d, sizes, 0.75, -0.5, val(old))
 
 
-def test_weight_gradient_of_values_behind_the_groups():
+@pytest.mark.parametrize("k", [256, 288])
+def test_weight_gradient_of_values_behind_the_groups(k):
     """Rows past the last group and other groups' rows hold NaN: none reaches a gradient."""
-    say("wgrad NaN")
-    m, k, n, sizes = 140, 288, 264, [50, 0, 40]
+    say("wgrad NaN", k)
+    m, n, sizes = 140, 264, [50, 0, 40]
     codes, scale, dout, x, d = wgrad_case(60, m, k, n, 3)
     scale[90:] = 255
     dout[90:] = float("nan")
