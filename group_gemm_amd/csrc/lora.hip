@@ -916,130 +916,44 @@ __global__ __launch_bounds__(NT) void turn(Turn p0, Turn p1, int first) {   // t
 
 // ---------------------------------------------------------------------------------------------------------------
 // outer: sums over rows.  A workgroup takes a chunk of rows of one group and TC columns of x (then da [r, k]) or of
-// dout (then db [n, r]), 32 rows at a time through LDS; both operands have the rows as their slow axis and are read
-// with the transposing LDS reads.  The narrow operand (u or v) is the first, so a lane ends with four consecutive j
+// dout (then db [n, r]), some rows at a time through LDS.  The narrow operand (u or v) is the first, so a lane ends with four consecutive j
 // of one column.
 
-enum Wide { BF16 = 0, FP32 = 1, E4M3 = 2 };
-
-// the wide operand's 32 rows in LDS
-constexpr int WP16 = 256 + 16, WP32 = 256 + 4;
-
-template <bool F32, int NB, int P> struct OuterSmem;
-template <int NB, int P> struct OuterSmem<false, NB, P> {
-    __attribute__((aligned(16))) uint16_t wide[2][32 * WP16];
-    __attribute__((aligned(16))) uint16_t nar[2][P][32 * (16 * NB + 8)];
-};
-template <int NB, int P> struct OuterSmem<true, NB, P> {
-    __attribute__((aligned(16))) float wide[2][32 * WP32];
-    __attribute__((aligned(16))) float nar[2][1][32 * (16 * NB + 4)];
-};
-
-// 8 rows (of 32) of one column, from two transposing reads of 4 x 16 values
-__device__ inline bf16x8 column8(const uint16_t* base, int pitch, int col0) {
-    const int l = threadIdx.x & 63, q = l >> 4, i = l & 15;
-    const uint16_t* p = base + (8 * q + (i >> 2)) * pitch + col0 + 4 * (i & 3);
-    const i16x4 lo = lds_read_tr16(p), hi = lds_read_tr16(p + 4 * pitch);
-    typedef short i16x8 __attribute__((ext_vector_type(8)));
-    const i16x8 v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-    return __builtin_bit_cast(bf16x8, v);
+// What a wave holds of da's or db's sums over one chunk (NB x CB blocks, lane: four consecutive j of one column) to its place.
+struct Chunk { int h, part, first, rows, c0, cols; bool of_x, whole; };
+template <int NB, int CB>
+__device__ inline void outer_store(const Outer& p, const Chunk& w, const f32x4 (&acc)[NB][CB]) {
+    const int l = threadIdx.x & 63, wave = threadIdx.x >> 6, q = l >> 4, i16 = l & 15;
+    // one chunk: the result; more: the chunk's part, at a place that no other chunk of such a group has (two such
+    // chunks begin in the same `chunk` rows only if one is a group's first and the other is not)
+    const float scale = w.whole && p.scaling ? p.scaling[w.h] : 1.f;
+    const int64_t per = (int64_t)(p.k + p.n) * p.r;
+    float* part_at = p.parts + (2 * (int64_t)(w.first / p.chunk) + (w.part == 0)) * per;
+#pragma unroll
+    for (int a = 0; a < NB; ++a)
+#pragma unroll
+        for (int c = 0; c < CB; ++c) {
+            const int col = w.c0 + 16 * (CB * wave + c) + i16;
+            if (col >= w.cols) continue;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int j = 16 * a + 4 * q + e;
+                if (j >= p.r) continue;
+                const int64_t at = w.of_x ? (int64_t)j * p.k + col : (int64_t)col * p.r + j;
+                if (!w.whole) part_at[(w.of_x ? 0 : (int64_t)p.k * p.r) + at] = acc[a][c][e];
+                else {
+                    const float v = acc[a][c][e] * scale;
+                    const int64_t to = (int64_t)w.h * (w.of_x ? p.k : p.n) * p.r + at;
+                    void* dst = w.of_x ? p.da : p.db;
+                    if (p.grads_bf16) Out8<uint16_t>::put((uint16_t*)dst + to, v);
+                    else ((float*)dst)[to] = v;
+                }
+            }
+        }
 }
-
-// what a thread holds of the next 32 rows
-template <Wide W> struct WideRegs;
-template <> struct WideRegs<BF16> {   // row t / 32 + 8 i, eight columns at 8 (t % 32)
-    i32x4 v[4];
-    __device__ void load(const Outer& p, int row0, int rows, int c0, int cols, int64_t stride, const void* src) {
-        const int t = threadIdx.x, c = c0 + 8 * (t & 31);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = (t >> 5) + 8 * i;
-            v[i] = i32x4{0, 0, 0, 0};
-            if (r >= rows || c >= cols) continue;
-            const uint16_t* at = (const uint16_t*)src + (int64_t)(row0 + r) * stride + c;
-            if (c + 8 <= cols) v[i] = *(const i32x4_any*)at;
-            else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (c + e < cols) v[i][e >> 1] |= (int)((uint32_t)at[e] << (16 * (e & 1)));
-            }
-        }
-    }
-    __device__ void store(uint16_t* to) const {
-        const int t = threadIdx.x;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) *(i32x4*)(to + ((t >> 5) + 8 * i) * WP16 + 8 * (t & 31)) = v[i];
-    }
-};
-template <> struct WideRegs<FP32> {   // row t / 32 + 8 i, eight columns
-    f32x4 v[4][2];
-    __device__ void load(const Outer& p, int row0, int rows, int c0, int cols, int64_t stride, const void* src) {
-        const int t = threadIdx.x, c = c0 + 8 * (t & 31);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = (t >> 5) + 8 * i;
-            v[i][0] = v[i][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-            if (r >= rows || c >= cols) continue;
-            const float* at = (const float*)src + (int64_t)(row0 + r) * stride + c;
-            if (c + 8 <= cols) { v[i][0] = *(const f32x4_any*)at; v[i][1] = *(const f32x4_any*)(at + 4); }
-            else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    if (c + e < cols) v[i][e >> 2][e & 3] = at[e];
-            }
-        }
-    }
-    __device__ void store(float* to) const {
-        const int t = threadIdx.x;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float* at = to + ((t >> 5) + 8 * i) * WP32 + 8 * (t & 31);
-            *(f32x4*)at = v[i][0];
-            *(f32x4*)(at + 4) = v[i][1];
-        }
-    }
-};
-template <> struct WideRegs<E4M3> {   // row t / 8, one block of 32 columns at 32 (t % 8)
-    i32x4 v[2];
-    int byte;
-    __device__ void load(const Outer& p, int row0, int rows, int c0, int cols, int64_t stride, const void* src) {
-        const int t = threadIdx.x, r = t >> 3, c = c0 + 32 * (t & 7);
-        v[0] = v[1] = i32x4{0, 0, 0, 0};
-        byte = 0;
-        if (r < rows && c < cols) {
-            const i32x4* at = (const i32x4*)((const uint8_t*)src + (int64_t)(row0 + r) * stride + c);
-            v[0] = at[0];
-            v[1] = at[1];
-            byte = p.x_scale[(int64_t)(row0 + r) * (stride >> 5) + (c >> 5)];
-        }
-    }
-    __device__ void store(uint16_t* to) const {
-        const int t = threadIdx.x;
-        const float s = __uint_as_float((uint32_t)byte << 23);   // exponent field 255 is NaN to the conversion
-        uint16_t* at = to + (t >> 3) * WP16 + 32 * (t & 7);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            i32x4 q;
-#pragma unroll
-            for (int d = 0; d < 2; ++d) {
-                const uint32_t c = (uint32_t)v[i >> 1][2 * (i & 1) + d];
-                q[2 * d] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, s, false));
-                q[2 * d + 1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, s, true));
-            }
-            *(i32x4*)(at + 8 * i) = q;
-        }
-    }
-};
-
-template <Wide XW, int NB, int P, int CB>   // XW: x's type; CB: 16-column blocks a wave
-__global__ __launch_bounds__(NT) void outer(Outer p) {
-    constexpr bool F32 = XW == FP32;
-    constexpr int TC = 64 * CB;
-    constexpr int NPITCH = 16 * NB + (F32 ? 4 : 8);
-    using E = typename std::conditional<F32, float, uint16_t>::type;
-    __shared__ Tables tab;
-    __shared__ OuterSmem<F32, NB, P> sm;
-    static_assert(TC <= 256, "the staged columns");
+// Which chunk of which group, and which columns (TC of them) a workgroup has; false: none (a group without rows is cleared).
+template <int TC>
+__device__ inline bool outer_chunk(const Outer& p, Tables& tab, Chunk& w) {
     int tiles, covered;
     build_tables<NT>(p.group_sizes, p.g, p.m, p.chunk, 1, tab, &tiles, &covered);
     if (blockIdx.x == 0 && threadIdx.x == 0 && p.status) *p.status = tab.flags;
@@ -1049,7 +963,7 @@ __global__ __launch_bounds__(NT) void outer(Outer p) {
         // With no more rows than a chunk every group with rows has one, join is not launched, and the places left over are
         // the groups' without rows: h - tile_off[h] of them lie before group h.
         const int e = -1 - id;
-        if (p.m > p.chunk || e >= p.g - tiles) return;
+        if (p.m > p.chunk || e >= p.g - tiles) return false;
         int lo = 0, hi = p.g - 1;   // the first h with more than e such groups up to it
         while (lo < hi) {
             const int mid = (lo + hi) >> 1;
@@ -1064,125 +978,254 @@ __global__ __launch_bounds__(NT) void outer(Outer p) {
             if (p.grads_bf16) ((uint16_t*)dst)[at] = 0;
             else ((float*)dst)[at] = 0.f;
         }
-        return;
+        return false;
     }
-    const int h = find_group(tab.tile_off, p.g, id), part = id - tab.tile_off[h];
-    const int first = tab.row_off[h] + part * p.chunk, rows = min(p.chunk, tab.row_off[h + 1] - first);
-    const bool of_x = ct < xt;
-    const int c0 = (of_x ? ct : ct - xt) * TC, cols = of_x ? p.k : p.n;
-    const float* nsrc = of_x ? p.u : p.v;
-    const int t = threadIdx.x, l = t & 63, wave = t >> 6, q = l >> 4, i16 = l & 15;
+    w.h = find_group(tab.tile_off, p.g, id);
+    w.part = id - tab.tile_off[w.h];
+    const int size = tab.row_off[w.h + 1] - tab.row_off[w.h];
+    w.first = tab.row_off[w.h] + w.part * p.chunk;
+    w.rows = min(p.chunk, size - w.part * p.chunk);
+    w.whole = size <= p.chunk;
+    w.of_x = ct < xt;
+    w.c0 = (w.of_x ? ct : ct - xt) * TC;
+    w.cols = w.of_x ? p.k : p.n;
+    return true;
+}
 
+// bf16 dout, and x in bf16 or e4m3.  The wide operand's rows lie in LDS as [BR][256], 32-byte units XOR'ed with the row so
+// that the eight rows which half of a transposing read's lanes touch lie in distinct banks; u or v lies there turned,
+// [part][j][row], so that a fragment is one read.  A thread holds the next BR rows' part while these are multiplied.
+template <bool X8, int NB, int P, int CB>   // X8: x is e4m3; CB: 16-column blocks a wave
+__global__ __launch_bounds__(NT) void outer16(Outer p) {
+    constexpr int BR = NB <= 4 ? 64 : 32, TC = 64 * CB, NP = BR + 8;
+    constexpr int RG = BR / 4, JB = NT / (16 * RG), PASSES = (NB + JB - 1) / JB;   // narrow: four rows of a j a thread and pass
+    __shared__ union {
+        Tables tab;
+        struct {
+            __attribute__((aligned(16))) uint16_t wide[BR * 256];
+            __attribute__((aligned(16))) uint16_t nar[P][16 * NB * NP];
+        };
+    } sm;
+    Chunk w;
+    if (!outer_chunk<TC>(p, sm.tab, w)) return;
+    __syncthreads();   // the tables' memory is used again
+    const int t = threadIdx.x, l = t & 63, wave = t >> 6, q = l >> 4, i16 = l & 15;
+    const int c1 = min(w.cols, w.c0 + TC);
     f32x4 acc[NB][CB];
 #pragma unroll
     for (int a = 0; a < NB; ++a)
 #pragma unroll
         for (int b = 0; b < CB; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+    auto unit = [](int row, int col) { return row * 256 + ((((col >> 4) ^ ((row & 3) | (((row >> 3) & 1) << 2))) << 4) | (col & 15)); };
 
-    constexpr int NPER = 32 * 16 * NB / NT;   // narrow values a thread
-    auto body = [&](auto wide_c) {
-        constexpr Wide W = decltype(wide_c)::value;
-        struct Step { WideRegs<W> wide; float nar[NPER]; } regs[2];   // two steps on their way
-        const void* src = of_x ? p.x : p.dout;
-        const int64_t stride = of_x ? p.k : p.n;
-        auto load = [&](Step& to, int r0) {
-            to.wide.load(p, first + r0, rows - r0, c0, min(cols, c0 + TC), stride, src);
+    // the narrow operand: j = 16 (JB pass + ...) + t % 16, rows 4 (t / 16 % RG) .. + 3
+    const int nj = 16 * (t / (16 * RG)) + (t & 15), nr = 4 * ((t >> 4) % RG);
+    const float* nsrc = (w.of_x ? p.u : p.v) + (int64_t)(w.first + nr) * p.r + nj;
+    float nv[PASSES][4];
+    auto load_nar = [&](int r0) {
 #pragma unroll
-            for (int e = 0; e < NPER; ++e) {
-                const int at = t + NT * e, i = at / (16 * NB), j = at % (16 * NB);
-                to.nar[e] = i < rows - r0 && j < p.r ? nsrc[(int64_t)(first + r0 + i) * p.r + j] : 0.f;
-            }
-        };
-        auto store = [&](const Step& from, int slot) {
-            from.wide.store(sm.wide[slot]);
+        for (int z = 0; z < PASSES; ++z)
 #pragma unroll
-            for (int e = 0; e < NPER; ++e) {
-                const int at = t + NT * e, i = at / (16 * NB), j = at % (16 * NB);
-                if constexpr (F32) sm.nar[slot][0][i * NPITCH + j] = from.nar[e];
-                else {
-                    uint16_t s[P];
-                    split<P>(from.nar[e], s);
+            for (int e = 0; e < 4; ++e)
+                nv[z][e] = nj + 16 * JB * z < p.r && r0 + nr + e < w.rows ? nsrc[(int64_t)(r0 + e) * p.r + 16 * JB * z] : 0.f;
+    };
+    auto store_nar = [&]() {
 #pragma unroll
-                    for (int z = 0; z < P; ++z) sm.nar[slot][z][i * NPITCH + j] = s[z];
-                }
-            }
-        };
-        load(regs[0], 0);
-        load(regs[1], 32);
-        store(regs[0], 0);
-        __syncthreads();
-        auto step = [&](auto slot_c, int r0) {
-            constexpr int slot = decltype(slot_c)::value;
-            load(regs[slot], r0 + 64);
-                        const E* wd = sm.wide[slot];
-            if constexpr (F32) {
+        for (int z = 0; z < PASSES; ++z) {
+            if (NB < JB && nj >= 16 * NB) continue;
+            uint16_t s[4][P];
 #pragma unroll
-                for (int s = 0; s < 8; ++s) {
-                    float b[CB];
+            for (int e = 0; e < 4; ++e) split<P>(nv[z][e], s[e]);
 #pragma unroll
-                    for (int c = 0; c < CB; ++c) b[c] = wd[(4 * s + q) * WP32 + 16 * (CB * wave + c) + i16];
-#pragma unroll
-                    for (int a = 0; a < NB; ++a) {
-                        const float n = sm.nar[slot][0][(4 * s + q) * NPITCH + 16 * a + i16];
-#pragma unroll
-                        for (int c = 0; c < CB; ++c) acc[a][c] = __builtin_amdgcn_mfma_f32_16x16x4f32(n, b[c], acc[a][c], 0, 0, 0);
-                    }
-                }
-            } else {
-                bf16x8 b[CB];
-#pragma unroll
-                for (int c = 0; c < CB; ++c) b[c] = column8(wd, WP16, 16 * (CB * wave + c));
-#pragma unroll
-                for (int a = 0; a < NB; ++a)
-#pragma unroll
-                    for (int z = 0; z < P; ++z) {
-                        const bf16x8 n = column8(sm.nar[slot][z], NPITCH, 16 * a);
-#pragma unroll
-                        for (int c = 0; c < CB; ++c) acc[a][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(n, b[c], acc[a][c], 0, 0, 0);
-                    }
-            }
-            if (r0 + 32 < rows) store(regs[slot ^ 1], slot ^ 1);
-            __syncthreads();
-        };
-        for (int r0 = 0; r0 < rows; r0 += 64) {
-            step(std::integral_constant<int, 0>{}, r0);
-            if (r0 + 32 < rows) step(std::integral_constant<int, 1>{}, r0 + 32);
+            for (int i = 0; i < P; ++i)
+                *(i32x2*)(&sm.nar[i][(nj + 16 * JB * z) * NP + nr]) = i32x2{s[0][i] | s[1][i] << 16, s[2][i] | s[3][i] << 16};
         }
     };
-    if constexpr (XW == E4M3) {
-        if (of_x) body(std::integral_constant<Wide, E4M3>{});
-        else body(std::integral_constant<Wide, BF16>{});
-    } else {
-        body(std::integral_constant<Wide, XW>{});
+    auto multiply = [&]() {
+#pragma unroll
+        for (int s = 0; s < BR / 32; ++s) {
+            bf16x8 b[CB];
+#pragma unroll
+            for (int c = 0; c < CB; ++c) {   // rows 32 s + 8 q .. + 7 of one column, from two transposing reads of 4 x 16 values
+                const int row = 32 * s + 8 * q + (i16 >> 2), col = 16 * (CB * wave + c) + 4 * (i16 & 3);
+                const i16x4 lo = lds_read_tr16(sm.wide + unit(row, col)), hi = lds_read_tr16(sm.wide + unit(row + 4, col));
+                typedef short i16x8 __attribute__((ext_vector_type(8)));
+                const i16x8 v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+                b[c] = __builtin_bit_cast(bf16x8, v);
+            }
+#pragma unroll
+            for (int a = 0; a < NB; ++a)
+#pragma unroll
+                for (int i = 0; i < P; ++i) {
+                    const bf16x8 n = *(const bf16x8*)(&sm.nar[i][(16 * a + i16) * NP + 32 * s + 8 * q]);
+#pragma unroll
+                    for (int c = 0; c < CB; ++c) acc[a][c] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(n, b[c], acc[a][c], 0, 0, 0);
+                }
+        }
+    };
+    auto steps = [&](auto& load, auto& store) {
+        load(0);
+        load_nar(0);
+        for (int r0 = 0; r0 < w.rows; r0 += BR) {
+            store();
+            store_nar();
+            __syncthreads();
+            if (r0 + BR < w.rows) {
+                load(r0 + BR);
+                load_nar(r0 + BR);
+            }
+            multiply();
+            __syncthreads();
+        }
+    };
+    if (X8 && w.of_x) {   // row t / (256 / BR'), blocks of 32 columns
+        constexpr int BLK = BR / 32, TR = 8 / BLK;              // blocks a thread, threads a row
+        const int row = t / TR, col = 32 * BLK * (t % TR), c = w.c0 + col;
+        const uint8_t* src = (const uint8_t*)p.x + (int64_t)(w.first + row) * p.k + c;
+        const uint8_t* scl = p.x_scale + (int64_t)(w.first + row) * (p.k >> 5) + (c >> 5);
+        i32x4 v[BLK][2];
+        int byte[BLK];
+        auto load = [&](int r0) {
+#pragma unroll
+            for (int b = 0; b < BLK; ++b) {
+                v[b][0] = v[b][1] = i32x4{0, 0, 0, 0};
+                byte[b] = 0;
+                if (r0 + row < w.rows && c + 32 * b < c1) {
+                    const i32x4* at = (const i32x4*)(src + (int64_t)r0 * p.k + 32 * b);
+                    v[b][0] = at[0];
+                    v[b][1] = at[1];
+                    byte[b] = scl[(int64_t)r0 * (p.k >> 5) + b];
+                }
+            }
+        };
+        auto store = [&]() {
+#pragma unroll
+            for (int b = 0; b < BLK; ++b) {
+                const float s = __uint_as_float((uint32_t)byte[b] << 23);   // exponent field 255 is NaN to the conversion
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    i32x4 o;
+#pragma unroll
+                    for (int d = 0; d < 2; ++d) {
+                        const uint32_t x = (uint32_t)v[b][i >> 1][2 * (i & 1) + d];
+                        o[2 * d] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, s, false));
+                        o[2 * d + 1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, s, true));
+                    }
+                    *(i32x4*)(sm.wide + unit(row, col + 32 * b + 8 * i)) = o;
+                }
+            }
+        };
+        steps(load, store);
+    } else {   // rows t / 32 + 8 i, eight columns
+        const int row = t >> 5, col = 8 * (t & 31), c = w.c0 + col;
+        const int64_t stride = w.of_x ? p.k : p.n;
+        const uint16_t* src = (const uint16_t*)(w.of_x ? p.x : p.dout) + (int64_t)(w.first + row) * stride + c;
+        i32x4 v[BR / 8];
+        const bool all = c + 8 <= c1;
+        auto load = [&](int r0) {
+#pragma unroll
+            for (int i = 0; i < BR / 8; ++i) {
+                v[i] = i32x4{0, 0, 0, 0};
+                if (r0 + row + 8 * i < w.rows && all) v[i] = *(const i32x4_any*)(src + (int64_t)(r0 + 8 * i) * stride);
+            }
+            if (!all && c < c1) {
+                for (int i = 0; i < BR / 8; ++i)
+                    if (r0 + row + 8 * i < w.rows) {
+                        i32x4 x = {0, 0, 0, 0};
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (c + e < c1) x[e >> 1] |= (int)((uint32_t)src[(int64_t)(r0 + 8 * i) * stride + e] << (16 * (e & 1)));
+#pragma unroll
+                        for (int z = 0; z < BR / 8; ++z)
+                            if (z == i) v[z] = x;
+                    }
+            }
+        };
+        auto store = [&]() {
+#pragma unroll
+            for (int i = 0; i < BR / 8; ++i) *(i32x4*)(sm.wide + unit(row + 8 * i, col)) = v[i];
+        };
+        steps(load, store);
     }
+    outer_store<NB, CB>(p, w, acc);
+}
 
-    // one chunk: the result; more: the chunk's part, at a place that no other chunk of such a group has (two such
-    // chunks begin in the same `chunk` rows only if one is a group's first and the other is not)
-    const bool whole = tab.row_off[h + 1] - tab.row_off[h] <= p.chunk;
-    const float scale = whole && p.scaling ? p.scaling[h] : 1.f;
-    const int64_t per = (int64_t)(p.k + p.n) * p.r;
-    float* part_at = p.parts + (2 * (int64_t)(first / p.chunk) + (part == 0)) * per;
+// fp32: both operands are read from LDS as they lie, instruction i of 32 rows taking rows 4 i + q.
+constexpr int WP32 = 256 + 4;
+template <int NB, int CB>
+__global__ __launch_bounds__(NT) void outer32(Outer p) {
+    constexpr int TC = 64 * CB, NP = 16 * NB + 4, NPER = 32 * 16 * NB / NT;
+    __shared__ Tables tab;
+    __shared__ __attribute__((aligned(16))) float wide[2][32 * WP32];
+    __shared__ __attribute__((aligned(16))) float nar[2][32 * NP];
+    Chunk w;
+    if (!outer_chunk<TC>(p, tab, w)) return;
+    const float* nsrc = w.of_x ? p.u : p.v;
+    const float* wsrc = (const float*)(w.of_x ? p.x : p.dout);
+    const int t = threadIdx.x, l = t & 63, wave = t >> 6, q = l >> 4, i16 = l & 15;
+    const int c = w.c0 + 8 * (t & 31), c1 = min(w.cols, w.c0 + TC);
+    f32x4 acc[NB][CB];
 #pragma unroll
     for (int a = 0; a < NB; ++a)
 #pragma unroll
-        for (int c = 0; c < CB; ++c) {
-            const int col = c0 + 16 * (CB * wave + c) + i16;
-            if (col >= cols) continue;
+        for (int b = 0; b < CB; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+    f32x4 v[4][2];      // row t / 32 + 8 i, eight columns
+    float nv[NPER];
+    auto load = [&](int r0) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int j = 16 * a + 4 * q + e;
-                if (j >= p.r) continue;
-                const int64_t at = of_x ? (int64_t)j * p.k + col : (int64_t)col * p.r + j;
-                if (!whole) part_at[(of_x ? 0 : (int64_t)p.k * p.r) + at] = acc[a][c][e];
-                else {
-                    const float v = acc[a][c][e] * scale;
-                    const int64_t to = (int64_t)h * (of_x ? p.k : p.n) * p.r + at;
-                    void* dst = of_x ? p.da : p.db;
-                    if (p.grads_bf16) Out8<uint16_t>::put((uint16_t*)dst + to, v);
-                    else ((float*)dst)[to] = v;
-                }
+        for (int i = 0; i < 4; ++i) {
+            const int r = r0 + (t >> 5) + 8 * i;
+            v[i][0] = v[i][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (r >= w.rows || c >= c1) continue;
+            const float* at = wsrc + (int64_t)(w.first + r) * w.cols + c;
+            if (c + 8 <= c1) { v[i][0] = *(const f32x4_any*)at; v[i][1] = *(const f32x4_any*)(at + 4); }
+            else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (c + e < c1) v[i][e >> 2][e & 3] = at[e];
             }
         }
+#pragma unroll
+        for (int e = 0; e < NPER; ++e) {
+            const int at = t + NT * e, i = at / (16 * NB), j = at % (16 * NB);
+            nv[e] = r0 + i < w.rows && j < p.r ? nsrc[(int64_t)(w.first + r0 + i) * p.r + j] : 0.f;
+        }
+    };
+    auto store = [&](int slot) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float* at = wide[slot] + ((t >> 5) + 8 * i) * WP32 + 8 * (t & 31);
+            *(f32x4*)at = v[i][0];
+            *(f32x4*)(at + 4) = v[i][1];
+        }
+#pragma unroll
+        for (int e = 0; e < NPER; ++e) {
+            const int at = t + NT * e;
+            nar[slot][at / (16 * NB) * NP + at % (16 * NB)] = nv[e];
+        }
+    };
+    load(0);
+    store(0);
+    __syncthreads();
+    int slot = 0;
+    for (int r0 = 0; r0 < w.rows; r0 += 32, slot ^= 1) {
+        if (r0 + 32 < w.rows) load(r0 + 32);
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+            float b[CB];
+#pragma unroll
+            for (int c = 0; c < CB; ++c) b[c] = wide[slot][(4 * s + q) * WP32 + 16 * (CB * wave + c) + i16];
+#pragma unroll
+            for (int a = 0; a < NB; ++a) {
+                const float n = nar[slot][(4 * s + q) * NP + 16 * a + i16];
+#pragma unroll
+                for (int c = 0; c < CB; ++c) acc[a][c] = __builtin_amdgcn_mfma_f32_16x16x4f32(n, b[c], acc[a][c], 0, 0, 0);
+            }
+        }
+        if (r0 + 32 < w.rows) store(slot ^ 1);
+        __syncthreads();
+    }
+    outer_store<NB, CB>(p, w, acc);
 }
 
 // join: groups of several chunks, in their order; groups without rows are 0.  V consecutive values a thread.
@@ -1429,37 +1472,41 @@ hipError_t launch_lora_turn(const void* a, void* at, int rows, int cols, const v
     return hipGetLastError();
 }
 
-template <lora::Wide XW, int NB, int P, int CB>
+enum class OuterX { bf16, e4m3, f32 };
+template <OuterX X, int NB, int P, int CB>
 static hipError_t outer_t(const lora::Outer& p, hipStream_t s) {
     const int64_t tiles = up64(p.m, p.chunk) + p.g, cols = up64(p.k, 64 * CB) + up64(p.n, 64 * CB);
     if (tiles * cols > kMaxBlocks) return hipErrorInvalidConfiguration;
-    if (tiles * cols > 0) hipLaunchKernelGGL((lora::outer<XW, NB, P, CB>), dim3((uint32_t)(tiles * cols)), dim3(lora::NT), 0, s, p);
+    if (tiles * cols == 0) return hipSuccess;
+    const dim3 grid((uint32_t)(tiles * cols));
+    if constexpr (X == OuterX::f32) hipLaunchKernelGGL((lora::outer32<NB, CB>), grid, dim3(lora::NT), 0, s, p);
+    else hipLaunchKernelGGL((lora::outer16<X == OuterX::e4m3, NB, P, CB>), grid, dim3(lora::NT), 0, s, p);
     return hipGetLastError();
 }
-template <lora::Wide XW, int P>
+template <OuterX X, int P>
 static hipError_t outer_nb(const lora::Outer& p, hipStream_t s) {
-    // few workgroups: narrower ones (375 rows of 5 groups in fp32, k 1030, n 515: 15.2 -> 10 us)
+    // few workgroups: narrower ones (375 rows of 5 groups in fp32, k 1030, n 515: 15.2 -> 11.8 us)
     const int64_t groups = std::max<int64_t>(up64(p.m, p.chunk), std::min<int64_t>(p.g, up64(p.m, 32)));
     if (p.r <= 64 && groups * (up64(p.k, 256) + up64(p.n, 256)) < 256) {
         switch (lora_nb(p.r)) {
-            case 1: return outer_t<XW, 1, P, 1>(p, s);
-            case 2: return outer_t<XW, 2, P, 1>(p, s);
-            default: return outer_t<XW, 4, P, 1>(p, s);
+            case 1: return outer_t<X, 1, P, 1>(p, s);
+            case 2: return outer_t<X, 2, P, 1>(p, s);
+            default: return outer_t<X, 4, P, 1>(p, s);
         }
     }
     switch (lora_nb(p.r)) {
-        case 1: return outer_t<XW, 1, P, 4>(p, s);
-        case 2: return outer_t<XW, 2, P, 4>(p, s);
-        case 4: return outer_t<XW, 4, P, 4>(p, s);
-        case 8: return outer_t<XW, 8, P, 2>(p, s);
-        default: return outer_t<XW, 16, P, 1>(p, s);
+        case 1: return outer_t<X, 1, P, 4>(p, s);
+        case 2: return outer_t<X, 2, P, 4>(p, s);
+        case 4: return outer_t<X, 4, P, 4>(p, s);
+        case 8: return outer_t<X, 8, P, 2>(p, s);
+        default: return outer_t<X, 16, P, 1>(p, s);
     }
 }
 hipError_t launch_lora_outer(const lora::Outer& p, bool bf16, hipStream_t s) {
     hipError_t e;
-    if (!bf16) e = outer_nb<lora::FP32, 1>(p, s);
-    else if (p.x_scale) e = p.grads_bf16 ? outer_nb<lora::E4M3, 2>(p, s) : outer_nb<lora::E4M3, 3>(p, s);
-    else e = p.grads_bf16 ? outer_nb<lora::BF16, 2>(p, s) : outer_nb<lora::BF16, 3>(p, s);
+    if (!bf16) e = outer_nb<OuterX::f32, 1>(p, s);
+    else if (p.x_scale) e = p.grads_bf16 ? outer_nb<OuterX::e4m3, 2>(p, s) : outer_nb<OuterX::e4m3, 3>(p, s);
+    else e = p.grads_bf16 ? outer_nb<OuterX::bf16, 2>(p, s) : outer_nb<OuterX::bf16, 3>(p, s);
     if (e != hipSuccess) return e;
     const int64_t per = (int64_t)(p.k + p.n) * p.r;
     if (per == 0 || p.m <= p.chunk) return hipSuccess;   // no group has two chunks
