@@ -27,7 +27,8 @@ namespace lora {
 
 constexpr int NT = 256;
 constexpr int KC = 64;           // elements of the long axis that a wave takes at a time
-constexpr int MA1024UNK = 1024;   // rows in any order: of these many, a workgroup takes those of its adapter
+constexpr int MAXCHUNK = 1024;   // rows in any order: of these many, a workgroup takes those of its adapter
+constexpr int NONE = 64;         // and of these many those without one
 
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -105,7 +106,7 @@ __device__ inline void split(float x, uint16_t (&out)[P]) {
 
 // Which rows a workgroup has: `rows` of adapter h (-1: rows without one), row i being first + i or list[i].
 struct RowTile { int h, rows, first; const int* list; };
-struct RowList { int list[MA1024UNK]; int wave[4]; };
+struct RowList { int list[MAXCHUNK]; int wave[4]; };
 
 // tile `id` of the rows behind the last adapter's
 __device__ inline RowTile behind(const Rows& p, int covered, int id, int tm) {
@@ -157,15 +158,20 @@ __device__ inline RowTile sorted_tile(const Rows& p, int id, int tm, Tables& tab
     return w;
 }
 // Rows in any order: slot `id` of a chunk is adapter `id`, or (fewer rows than adapters) the adapter of row `id` of
-// the chunk if no row before it has the same; the last slot is the rows without one.  The list is in row order.
+// the chunk if no row before it has the same; the last slots are the rows without one, of
+// NONE rows each.  The list is in row order.
 __device__ inline RowTile any_tile(const Rows& p, int id, RowList& any) {
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && p.status) *p.status = 0;
-    const int slots = p.slots + 1, c = id / slots, slot = id - c * slots;
-    const int r0 = c * p.chunk, n = min(p.chunk, p.m - r0);
+    const int slots = p.slots + p.chunk / NONE, c = id / slots, slot = id - c * slots;
+    int r0 = c * p.chunk, n = min(p.chunk, p.m - r0);
     const bool by_row = p.slots < p.g;
     int h = slot;
-    if (slot == p.slots) h = -1;
-    else if (by_row) {
+    if (slot >= p.slots) {
+        h = -1;
+        r0 += (slot - p.slots) * NONE;
+        n = min(NONE, p.m - r0);
+        if (slot - p.slots >= p.chunk / NONE || n <= 0) return {-1, 0, 0, nullptr};
+    } else if (by_row) {
         if (slot >= n) return {-1, 0, 0, nullptr};
         h = p.row_group[r0 + slot];
         if (h < 0 || h >= p.g) return {-1, 0, 0, nullptr};
@@ -424,6 +430,81 @@ __global__ __launch_bounds__(NT) void shrink_ring(Shrink p) {
         R::run(acc, rings, p, w, r0, c0, c1);
         const int row = r0 + (TEAM == 4 ? 16 * wave : 0) + (l & 15);
         if ((TEAM == 1 && wave > 0) || row >= w.rows) continue;
+        float* to = p.t + ((int64_t)blockIdx.y * p.rows.m + row_at(w, row)) * p.r;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (16 * b + 4 * q + e < p.r) to[16 * b + 4 * q + e] = acc[b][e];
+    }
+}
+
+// The same for many rows of any alignment: 64 rows a workgroup, through registers (loads straight into LDS take whole
+// dwords), two pieces on their way.
+template <typename T, int NB>
+__global__ __launch_bounds__(NT) void shrink_staged(Shrink p) {
+    constexpr int TM = 64, KE = 128 / sizeof(T), STEPS = sizeof(T) == 2 ? 2 : 1, EL = 16 / sizeof(T);
+    constexpr int ROWS = TM + 16 * NB, PER = (ROWS + 31) / 32;   // rows of a slot; 16-byte loads a thread
+    __shared__ RowList rs;
+    __shared__ union { Tables tab; __attribute__((aligned(128))) char slot[2][PER * 32 * 128]; } sm;
+    const RowTile w = row_tile(p.rows, blockIdx.x, TM, rs, &sm);
+    if (w.h < 0 || w.rows == 0) return;
+    const int t = threadIdx.x, l = t & 63, wave = t >> 6, q = l >> 4, i16 = l & 15;
+    const int nch = (p.k + KE - 1) / KE, per = (nch + (int)gridDim.y - 1) / (int)gridDim.y;
+    const int c0 = blockIdx.y * per, c1 = min(nch, c0 + per);
+    for (int r0 = 0; r0 < w.rows; r0 += TM) {
+        const T* src[PER];
+        int at[PER];
+#pragma unroll
+        for (int u = 0; u < PER; ++u) {   // row t / 8 + 32 u of a slot, x's first and then the weights', 16 bytes of it
+            const int row = (t >> 3) + 32 * u;
+            src[u] = (row < TM ? (const T*)p.x + (int64_t)row_at(w, min(r0 + row, w.rows - 1)) * p.stride
+                               : (const T*)p.w + ((int64_t)w.h * p.r + min(row - TM, p.r - 1)) * p.k) + EL * (t & 7);
+            at[u] = row * 128 + 16 * ((t & 7) ^ ((row >> 1) & 7));
+        }
+        i32x4 v[2][PER];
+        auto load = [&](i32x4 (&to)[PER], int c) {
+            const int valid = min(p.k - c * KE - EL * (t & 7), EL);   // of the thread's elements
+            if (c >= c1) return;
+#pragma unroll
+            for (int u = 0; u < PER; ++u) {
+                if (valid == EL) to[u] = *(const i32x4_any*)(src[u] + (int64_t)c * KE);
+                else {
+                    to[u] = i32x4{0, 0, 0, 0};
+#pragma unroll
+                    for (int e = 0; e < EL; ++e)
+                        if (e < valid) {
+                            if constexpr (sizeof(T) == 2) to[u][e >> 1] |= (int)((uint32_t)src[u][(int64_t)c * KE + e] << (16 * (e & 1)));
+                            else to[u][e] = __float_as_int(src[u][(int64_t)c * KE + e]);
+                        }
+                }
+            }
+        };
+        f32x4 acc[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+        auto step = [&](auto z_c, int c) {
+            constexpr int z = decltype(z_c)::value;
+#pragma unroll
+            for (int u = 0; u < PER; ++u) *(i32x4*)(sm.slot[z] + at[u]) = v[z][u];
+            load(v[z], c + 2);
+            __syncthreads();   // the other slot is written only after every wave has passed this, its reads done
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) {
+                const Frag<T> x = ring_frag<T>(sm.slot[z], 16 * wave + i16, s);
+#pragma unroll
+                for (int b = 0; b < NB; ++b) acc[b] = Frag<T>::mma(ring_frag<T>(sm.slot[z], TM + 16 * b + i16, s), x, acc[b]);
+            }
+        };
+        __syncthreads();       // the list, and the last tile's slots, have been read
+        load(v[0], c0);
+        load(v[1], c0 + 1);
+        for (int c = c0; c < c1; c += 2) {
+            step(std::integral_constant<int, 0>{}, c);
+            if (c + 1 < c1) step(std::integral_constant<int, 1>{}, c + 1);
+        }
+        const int row = r0 + 16 * wave + i16;
+        if (row >= w.rows) continue;
         float* to = p.t + ((int64_t)blockIdx.y * p.rows.m + row_at(w, row)) * p.r;
 #pragma unroll
         for (int b = 0; b < NB; ++b)
@@ -1156,8 +1237,8 @@ template <int NB, int CB>
 __global__ __launch_bounds__(NT) void outer32(Outer p) {
     constexpr int TC = 64 * CB, NP = 16 * NB + 4, NPER = 32 * 16 * NB / NT;
     __shared__ Tables tab;
-    __shared__ __attribute__((aligned(16))) float wide[2][32 * WP32];
-    __shared__ __attribute__((aligned(16))) float nar[2][32 * NP];
+    __shared__ __attribute__((aligned(16))) float wide[32 * WP32];
+    __shared__ __attribute__((aligned(16))) float nar[32 * NP];
     Chunk w;
     if (!outer_chunk<TC>(p, tab, w)) return;
     const float* nsrc = w.of_x ? p.u : p.v;
@@ -1191,38 +1272,36 @@ __global__ __launch_bounds__(NT) void outer32(Outer p) {
             nv[e] = r0 + i < w.rows && j < p.r ? nsrc[(int64_t)(w.first + r0 + i) * p.r + j] : 0.f;
         }
     };
-    auto store = [&](int slot) {
+    auto store = [&]() {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            float* at = wide[slot] + ((t >> 5) + 8 * i) * WP32 + 8 * (t & 31);
+            float* at = wide + ((t >> 5) + 8 * i) * WP32 + 8 * (t & 31);
             *(f32x4*)at = v[i][0];
             *(f32x4*)(at + 4) = v[i][1];
         }
 #pragma unroll
         for (int e = 0; e < NPER; ++e) {
             const int at = t + NT * e;
-            nar[slot][at / (16 * NB) * NP + at % (16 * NB)] = nv[e];
+            nar[at / (16 * NB) * NP + at % (16 * NB)] = nv[e];
         }
     };
     load(0);
-    store(0);
-    __syncthreads();
-    int slot = 0;
-    for (int r0 = 0; r0 < w.rows; r0 += 32, slot ^= 1) {
+    for (int r0 = 0; r0 < w.rows; r0 += 32) {
+        store();
+        __syncthreads();
         if (r0 + 32 < w.rows) load(r0 + 32);
 #pragma unroll
         for (int s = 0; s < 8; ++s) {
             float b[CB];
 #pragma unroll
-            for (int c = 0; c < CB; ++c) b[c] = wide[slot][(4 * s + q) * WP32 + 16 * (CB * wave + c) + i16];
+            for (int c = 0; c < CB; ++c) b[c] = wide[(4 * s + q) * WP32 + 16 * (CB * wave + c) + i16];
 #pragma unroll
             for (int a = 0; a < NB; ++a) {
-                const float n = nar[slot][(4 * s + q) * NP + 16 * a + i16];
+                const float n = nar[(4 * s + q) * NP + 16 * a + i16];
 #pragma unroll
                 for (int c = 0; c < CB; ++c) acc[a][c] = __builtin_amdgcn_mfma_f32_16x16x4f32(n, b[c], acc[a][c], 0, 0, 0);
             }
         }
-        if (r0 + 32 < w.rows) store(slot ^ 1);
         __syncthreads();
     }
     outer_store<NB, CB>(p, w, acc);
@@ -1315,11 +1394,11 @@ static int lora_mt(const lora::Rows& r, int nb, int most) {
     return rows >= 32 ? (nb >= 8 ? 2 : most) : 1;
 }
 void lora_rows(lora::Rows& r) {
-    r.chunk = (int)std::min<int64_t>(lora::MA1024UNK, std::max<int64_t>(256, up64((int64_t)32 * r.g, 256) * 256));
+    r.chunk = (int)std::min<int64_t>(lora::MAXCHUNK, std::max<int64_t>(256, up64((int64_t)32 * r.g, 256) * 256));
     r.slots = (int)std::min<int64_t>(r.g, std::min<int64_t>(r.m, r.chunk));
 }
 static int64_t lora_tiles(const lora::Rows& r, int tm) {
-    return r.group_sizes ? up64(r.m, tm) + r.g + 1 : std::max<int64_t>(1, up64(r.m, r.chunk)) * (r.slots + 1);
+    return r.group_sizes ? up64(r.m, tm) + r.g + 1 : std::max<int64_t>(1, up64(r.m, r.chunk)) * (r.slots + r.chunk / lora::NONE);
 }
 static int lora_nb(int r) { return r <= 16 ? 1 : r <= 32 ? 2 : r <= 64 ? 4 : r <= 128 ? 8 : 16; }
 
@@ -1329,6 +1408,13 @@ static hipError_t shrink_t(const lora::Shrink& p, hipStream_t s) {
     const int64_t tiles = lora_tiles(p.rows, 16 * MT);
     if (tiles > kMaxBlocks) return hipErrorInvalidConfiguration;
     hipLaunchKernelGGL((lora::shrink<T, NB, MT, U>), dim3((uint32_t)tiles, p.splits), dim3(lora::NT), 0, s, p);
+    return hipGetLastError();
+}
+template <typename T, int NB>
+static hipError_t shrink_staged_t(const lora::Shrink& p, hipStream_t s) {
+    const int64_t tiles = lora_tiles(p.rows, 64);
+    if (tiles > kMaxBlocks) return hipErrorInvalidConfiguration;
+    hipLaunchKernelGGL((lora::shrink_staged<T, NB>), dim3((uint32_t)tiles, p.splits), dim3(lora::NT), 0, s, p);
     return hipGetLastError();
 }
 template <typename T, int NB, int TEAM, int D>
@@ -1353,11 +1439,20 @@ static hipError_t shrink_nb(const lora::Shrink& p, hipStream_t s) {
             default: return shrink_ring_t<T, 16, 4, 3>(p, s);   // a ring a wave would not fit the LDS
         }
     }
+    if (mt > 1) {
+        switch (nb) {
+            case 1: return shrink_staged_t<T, 1>(p, s);
+            case 2: return shrink_staged_t<T, 2>(p, s);
+            case 4: return shrink_staged_t<T, 4>(p, s);
+            case 8: return shrink_staged_t<T, 8>(p, s);
+            default: return shrink_staged_t<T, 16>(p, s);
+        }
+    }
     switch (nb) {
-        case 1: return mt == 1 ? shrink_t<T, 1, 1>(p, s) : shrink_t<T, 1, 2>(p, s);
-        case 2: return mt == 1 ? shrink_t<T, 2, 1>(p, s) : shrink_t<T, 2, 2>(p, s);
-        case 4: return mt == 1 ? shrink_t<T, 4, 1>(p, s) : shrink_t<T, 4, 2>(p, s);
-        case 8: return mt == 1 ? shrink_t<T, 8, 1>(p, s) : shrink_t<T, 8, 2>(p, s);
+        case 1: return shrink_t<T, 1, 1>(p, s);
+        case 2: return shrink_t<T, 2, 1>(p, s);
+        case 4: return shrink_t<T, 4, 1>(p, s);
+        case 8: return shrink_t<T, 8, 1>(p, s);
         default: return shrink_t<T, 16, 1>(p, s);
     }
 }
@@ -1390,7 +1485,7 @@ static hipError_t expand_lines_t(lora::Expand p, hipStream_t s) {
 // expand_lines: 16-byte rows and ranks, and 32-bit offsets over an adapter's weights and over the rows of a tile (of a
 // chunk, in any order)
 template <typename O> static bool expand_lines_ok(const lora::Expand& p) {
-    const int64_t span = (p.rows.group_sizes ? 256 : lora::MA1024UNK) * (int64_t)sizeof(O);
+    const int64_t span = (p.rows.group_sizes ? 256 : lora::MAXCHUNK) * (int64_t)sizeof(O);
     return p.r % 8 == 0 && p.n % 8 == 0 && p.base_stride * sizeof(O) % 16 == 0 && p.out_stride * sizeof(O) % 16 == 0 &&
            (uintptr_t)p.base % 16 == 0 && (uintptr_t)p.out % 16 == 0 && (uintptr_t)p.w % 16 == 0 &&
            ((int64_t)p.n + 256) * p.r * 2 < (int64_t(1) << 31) && std::max(p.base_stride, p.out_stride) * span < (int64_t(1) << 31);

@@ -7,7 +7,7 @@
 // thread, and the product is the bf16 one.  Both tiles have the contracted rows as their slow axis and are read with
 // ds_read_b64_tr_b16 into row-consecutive fragments.  Groups longest first, as in ragged_k.hip.
 //
-// Two kernels: the ring one below for k a multiple of 128, n of 8 and 16-byte aligned operands, the general one for the rest.
+// Two kernels: the ring one below for n a multiple of 8 and 16-byte aligned operands, the general one for the rest.
 #include <algorithm>
 
 #include "common.hpp"
@@ -232,12 +232,18 @@ constexpr int LPT_MAX_G = 256;           // longest-first order up to this many 
 constexpr int SJ = 8;                    // n-tiles per super-tile column
 static_assert(PER * (STAGES - 1) <= 63, "vmcnt range");
 
+// one byte a lane, as a dword, straight into LDS at lds_addr + 4 * lane (ring.hpp)
+__device__ inline void load_lds1(i32x4 r, uint32_t lds_addr, uint32_t off) {
+    asm volatile("s_mov_b32 m0, %0\n\tbuffer_load_ubyte %1, %2, 0 offen lds"
+                 :: "s"(lds_addr), "v"(off), "s"(r) : "memory", "m0");
+}
+
 struct Smem {
     struct {
         uint16_t b[STAGES][SLICE];
         uint16_t a[2][SLICE];
         uint8_t codes[STAGES][SLICE];
-        uint32_t scale[STAGES][4][64];   // a wave's 8 rows of 8 bytes, and zeros
+        uint32_t scale[STAGES][4][64];   // a wave's 8 rows of 8 scale bytes, one a dword
     } ring;
     Tables tab;
     int order[LPT_MAX_G];
@@ -300,8 +306,8 @@ __global__ __launch_bounds__(NT, 1) void kernel(KmxParams p) {
 
     // ring-load roles.  dout: slice [32 rows][256 cols] in 1 KiB blocks of 2 rows; wave w fills blocks 4 w + u; lane l writes
     // physical chunk l % 32 of row 2 (4 w + u) + l / 32, which holds logical chunk (l & 31) ^ swz(row).  Codes: load u of
-    // wave w is rows 8 w + 4 u .. + 3, lane l the 16 codes at 16 (l % 16) of row l / 16.  Scales: lane l < 16 the four
-    // bytes at 4 (l % 2) of row 8 w + l / 2; the other lanes read zeros.
+    // wave w is rows 8 w + 4 u .. + 3, lane l the 16 codes at 16 (l % 16) of row l / 16.  Scales: lane l byte l % 8 of row
+    // 8 w + l / 8.
     const int wave_u = __builtin_amdgcn_readfirstlane(wave);
     int ch8[4];
     uint32_t b_lane[4];
@@ -312,7 +318,7 @@ __global__ __launch_bounds__(NT, 1) void kernel(KmxParams p) {
         b_lane[u] = (uint32_t)(l >> 5) * n2 + (uint32_t)ch8[u] * 2u;
     }
     const uint32_t a_lane = (uint32_t)(l >> 4) * k1 + 16u * (uint32_t)(l & 15);
-    const uint32_t s_lane = l < 16 ? (uint32_t)(l >> 1) * ks + 4u * (uint32_t)(l & 1) : kOOB;
+    const uint32_t s_lane = (uint32_t)(l >> 3) * ks + (uint32_t)(l & 7);
     const uint32_t lds_b = lds_u32(&sm.ring.b[0][0]) + (uint32_t)(4 * wave_u) * 1024u;
     const uint32_t lds_c = lds_u32(&sm.ring.codes[0][0]) + (uint32_t)wave_u * 2048u;
     const uint32_t lds_s = lds_u32(&sm.ring.scale[0][0][0]) + (uint32_t)wave_u * 256u;
@@ -368,9 +374,9 @@ __global__ __launch_bounds__(NT, 1) void kernel(KmxParams p) {
                 load_lds16(r.a, lds_c + (uint32_t)slot * SLICE + d * 1024u,
                            FULL || ok ? a_lane + (srow + (uint32_t)(8 * wave_u + 4 * d)) * k1 + (uint32_t)i0 : kOOB);
             } else if constexpr (d == 2) {
-                const bool ok = live && 128 * (l & 1) < p.k - i0 && l < 16;
-                load_lds4(r.s, lds_s + (uint32_t)slot * 1024u,
-                          (FULL ? l < 16 : ok) ? s_lane + (srow + (uint32_t)(8 * wave_u)) * ks + ((uint32_t)i0 >> 5) : kOOB);
+                const bool ok = live && 32 * (l & 7) < p.k - i0;
+                load_lds1(r.s, lds_s + (uint32_t)slot * 1024u,
+                          FULL || ok ? s_lane + (srow + (uint32_t)(8 * wave_u)) * ks + ((uint32_t)i0 >> 5) : kOOB);
             } else {
                 constexpr int u = d - 3;
                 const bool ok = live && ch8[u] < p.n - j0;
@@ -386,7 +392,7 @@ __global__ __launch_bounds__(NT, 1) void kernel(KmxParams p) {
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     q.c[u] = *(const i32x4*)(&sm.ring.codes[slot][0] + wave * 2048 + u * 1024 + 16 * l);
-                    q.byte[u] = ((const uint8_t*)&sm.ring.scale[slot][wave][0])[8 * (4 * u + (l >> 4)) + ((l & 15) >> 1)];
+                    q.byte[u] = sm.ring.scale[slot][wave][8 * (4 * u + (l >> 4)) + ((l & 15) >> 1)];
                 }
             }
             if constexpr (O >= 4 && O < 12) {   // two values a conversion, four values a step
@@ -498,11 +504,11 @@ __global__ __launch_bounds__(NT, 1) void kernel(KmxParams p) {
     wait_vm<0>();   // no ring load may still be writing LDS when the workgroup ends
 }
 
-// 32-bit buffer offsets over one 32-row slice of lhs / dout and one 256-row output tile, whole scale words
+// 32-bit buffer offsets over one 32-row slice of lhs / dout and one 256-row output tile
 bool ok(const KmxParams& p) {
     const uint64_t a = 33ull * (uint64_t)p.k, b = 33ull * (uint64_t)p.n * 2u, o = 256ull * (uint64_t)p.n * 4u;
-    return p.k % 128 == 0 && p.n % 8 == 0 && a < (1ull << 31) && b < (1ull << 31) && o < (1ull << 31) && (uintptr_t)p.lhs % 16 == 0 &&
-           (uintptr_t)p.lhs_scale % 4 == 0 && (uintptr_t)p.dout % 16 == 0 && (uintptr_t)p.out % 16 == 0;
+    return p.n % 8 == 0 && a < (1ull << 31) && b < (1ull << 31) && o < (1ull << 31) && (uintptr_t)p.lhs % 16 == 0 &&
+           (uintptr_t)p.dout % 16 == 0 && (uintptr_t)p.out % 16 == 0;
 }
 template <bool REBASE>
 void launch(const KmxParams& p, int grid, hipStream_t s) {
