@@ -268,8 +268,12 @@ size_t gg_workspace_bytes(gg_op op, int64_t m, int64_t k, int64_t n, int32_t g, 
         !(in == GG_DT_E2M1 && (op == GG_OP_RAGGED_M || op == GG_OP_PERMUTE)))
         return 0;
     switch (op) {
-        case GG_OP_RAGGED_M:
-        case GG_OP_RAGGED_K: return kHeader;
+        case GG_OP_RAGGED_M: return kHeader;
+        case GG_OP_RAGGED_K: {
+            if (in != GG_DT_E4M3 || !fits_i32(m) || !fits_i32(k) || !fits_i32(n)) return kHeader;
+            const int splits = gg::ragged_k_mx_splits(m, k, n, g);
+            return kHeader + (splits > 1 ? (size_t)g * splits * (size_t)k * (size_t)n * 4 : 0);
+        }
         case GG_OP_PADDED_M: {
             if (capacity < 1) return 0;
             const size_t rows = (size_t)g * (size_t)capacity;
@@ -720,7 +724,8 @@ gg_status gated_act_mxfp8_grad(const void* dh, const uint8_t* codes, const uint8
 gg_status ragged_dot_k_mxfp8(const void* lhs, const uint8_t* lhs_scale, const void* dout, const int32_t* group_sizes, void* out,
                              int64_t m, int64_t k, int64_t n, int32_t g, gg_dtype out_dtype, float alpha, float beta,
                              void* workspace, size_t workspace_bytes, void* stream) {
-    gg_status st = check_common(m, k, n, g, group_sizes, workspace, workspace_bytes, kHeader);
+    gg_status st = check_common(m, k, n, g, group_sizes, workspace, workspace_bytes,
+                                gg_workspace_bytes(GG_OP_RAGGED_K, m, k, n, g, 0, GG_DT_E4M3));
     if (st != GG_OK) return st;
     if (!floats(out_dtype)) return GG_ERR_BAD_DTYPE;
     if (k % 32 != 0) return GG_ERR_UNSUPPORTED;
@@ -728,12 +733,13 @@ gg_status ragged_dot_k_mxfp8(const void* lhs, const uint8_t* lhs_scale, const vo
     if (!aligned(lhs, 16) || !aligned(dout, 2) || !aligned(out, elem_bytes(out_dtype))) return GG_ERR_MISALIGNED;
     int cus;
     if (device_cus(&cus) != 0) return GG_ERR_HIP;
-    const int64_t bound = (int64_t)g * cdiv64(k, 128) * cdiv64(n, 256);   // tiles of the smallest size
+    const int splits = gg::ragged_k_mx_splits(m, k, n, g);
+    const int64_t bound = (int64_t)g * splits * cdiv64(k, 128) * cdiv64(n, 256);   // tiles of the smallest size
     if (!fits_i32(bound)) return GG_ERR_BAD_SHAPE;
     gg::KmxParams p{};
     p.lhs = (const uint8_t*)lhs; p.lhs_scale = lhs_scale; p.dout = (const uint16_t*)dout; p.group_sizes = group_sizes; p.out = out;
     p.status = (uint32_t*)workspace; p.m = (int)m; p.k = (int)k; p.n = (int)n; p.g = g; p.out_f32 = out_dtype == GG_DT_F32;
-    p.alpha = alpha; p.beta = beta;
+    p.alpha = alpha; p.beta = beta; p.splits = splits; p.parts = (float*)((char*)workspace + kHeader);
     return gg::launch_ragged_k_mx(p, cus, (hipStream_t)stream) == hipSuccess ? GG_OK : GG_ERR_HIP;
 }
 

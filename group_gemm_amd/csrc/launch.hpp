@@ -150,7 +150,10 @@ struct KmxParams {                 // ragged_dot_k_mxfp8
     int m, k, n, g;
     int out_f32;
     float alpha, beta;
+    int splits;                    // parts of each group's rows
+    float* parts;                  // [g, splits, k, n] where splits > 1
 };
+int ragged_k_mx_splits(int64_t m, int64_t k, int64_t n, int g);
 hipError_t launch_ragged_k_mx(const KmxParams& p, int cus, hipStream_t s);   // 256 x 256 tiles
 
 // Low-rank adapters.

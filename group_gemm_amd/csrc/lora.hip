@@ -1202,24 +1202,22 @@ __global__ __launch_bounds__(NT) void outer16(Outer p) {
         const int64_t stride = w.of_x ? p.k : p.n;
         const uint16_t* src = (const uint16_t*)(w.of_x ? p.x : p.dout) + (int64_t)(w.first + row) * stride + c;
         i32x4 v[BR / 8];
-        const bool all = c + 8 <= c1;
+        const uint16_t* end = (const uint16_t*)(w.of_x ? p.x : p.dout) + (int64_t)p.m * stride;
+        i32x4 mask;
+#pragma unroll
+        for (int d = 0; d < 4; ++d) mask[d] = c + 2 * d + 2 <= c1 ? -1 : c + 2 * d + 1 == c1 ? 0xffff : 0;
         auto load = [&](int r0) {
 #pragma unroll
             for (int i = 0; i < BR / 8; ++i) {
                 v[i] = i32x4{0, 0, 0, 0};
-                if (r0 + row + 8 * i < w.rows && all) v[i] = *(const i32x4_any*)(src + (int64_t)(r0 + 8 * i) * stride);
-            }
-            if (!all && c < c1) {
-                for (int i = 0; i < BR / 8; ++i)
-                    if (r0 + row + 8 * i < w.rows) {
-                        i32x4 x = {0, 0, 0, 0};
+                if (r0 + row + 8 * i >= w.rows || c >= c1) continue;
+                const uint16_t* at = src + (int64_t)(r0 + 8 * i) * stride;
+                if (at + 8 <= end) v[i] = *(const i32x4_any*)at & mask;   // what lies behind the row is masked
+                else {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            if (c + e < c1) x[e >> 1] |= (int)((uint32_t)src[(int64_t)(r0 + 8 * i) * stride + e] << (16 * (e & 1)));
-#pragma unroll
-                        for (int z = 0; z < BR / 8; ++z)
-                            if (z == i) v[z] = x;
-                    }
+                    for (int e = 0; e < 8; ++e)
+                        if (c + e < c1) v[i][e >> 1] |= (int)((uint32_t)at[e] << (16 * (e & 1)));
+                }
             }
         };
         auto store = [&]() {
@@ -1259,8 +1257,13 @@ __global__ __launch_bounds__(NT) void outer32(Outer p) {
             v[i][0] = v[i][1] = f32x4{0.f, 0.f, 0.f, 0.f};
             if (r >= w.rows || c >= c1) continue;
             const float* at = wsrc + (int64_t)(w.first + r) * w.cols + c;
-            if (c + 8 <= c1) { v[i][0] = *(const f32x4_any*)at; v[i][1] = *(const f32x4_any*)(at + 4); }
-            else {
+            if (at + 8 <= wsrc + (int64_t)p.m * w.cols) {   // what lies behind the row is masked
+                v[i][0] = *(const f32x4_any*)at;
+                v[i][1] = *(const f32x4_any*)(at + 4);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (c + e >= c1) v[i][e >> 2][e & 3] = 0.f;
+            } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     if (c + e < c1) v[i][e >> 2][e & 3] = at[e];

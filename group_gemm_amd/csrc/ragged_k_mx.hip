@@ -15,6 +15,16 @@
 #include "ring.hpp"
 
 namespace gg {
+
+// With few tiles a group's rows are dealt to `splits` workgroups in runs of whole 32-row slices; their results are added
+// up in order by kmx::add_up.
+__device__ inline void part_of(int splits, int part, int& row0, int& size) {
+    if (splits == 1) return;
+    const int run = cdiv(cdiv(size, splits), 32) * 32, at = (int)min((int64_t)part * run, (int64_t)size);
+    row0 += at;
+    size = min(run, size - at);
+}
+
 namespace kmx {
 
 constexpr int BN = 256, NT = 512;   // a tile is 64 MI x 256 of k x n (MI 4, or 2 for few rows), BR rows a step
@@ -60,8 +70,11 @@ __device__ inline void load(Regs<BR>& v, const KmxParams& p, int row0, int rows,
         v.b[i] = i32x4{0, 0, 0, 0};
         if (q >= rows || n0 >= p.n) continue;
         const uint16_t* at = p.dout + (int64_t)(row0 + q) * p.n + n0;
-        if (n0 + 8 <= p.n) v.b[i] = *(const i32x4_any*)at;
-        else {
+        if (at + 8 <= p.dout + (int64_t)p.m * p.n) {   // what lies behind the row is masked
+            v.b[i] = *(const i32x4_any*)at;
+#pragma unroll
+            for (int d = 0; d < 4; ++d) v.b[i][d] &= n0 + 2 * d + 2 <= p.n ? -1 : n0 + 2 * d + 1 == p.n ? 0xffff : 0;
+        } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 if (n0 + e < p.n) v.b[i][e >> 1] |= (int)((uint32_t)at[e] << (16 * (e & 1)));
@@ -118,7 +131,7 @@ __global__ __launch_bounds__(NT, MI == 2 ? 4 : 1) void kernel(KmxParams p) {
     constexpr int BM = 64 * MI;
     __shared__ Smem<BR, SLOTS> sm;
     const int t = threadIdx.x, wave = t >> 6, wm = wave >> 2, wn = wave & 3, l = t & 63;
-    const int nti = cdiv(p.k, BM), ntj = cdiv(p.n, BN), per = nti * ntj, total = p.g * per;
+    const int nti = cdiv(p.k, BM), ntj = cdiv(p.n, BN), per = nti * ntj, total = p.g * p.splits * per;
     const bool lpt = p.g <= LPT_MAX_G;
     int gemm_tiles, covered;
     build_tables<NT>(p.group_sizes, p.g, p.m, 1, 0, sm.tab, &gemm_tiles, &covered);
@@ -136,8 +149,9 @@ __global__ __launch_bounds__(NT, MI == 2 ? 4 : 1) void kernel(KmxParams p) {
         __syncthreads();
     }
     for (int tile = xcd_virtual_id(blockIdx.x, gridDim.x); tile < total; tile += gridDim.x) {
-        const int pg = tile / per, local = tile - pg * per, grp = lpt ? sm.order[pg] : pg;
-        const int row0 = sm.tab.row_off[grp], size = sm.tab.row_off[grp + 1] - row0;
+        const int vg = tile / per, local = tile - vg * per, pg = vg / p.splits, part = vg - pg * p.splits, grp = lpt ? sm.order[pg] : pg;
+        int row0 = sm.tab.row_off[grp], size = sm.tab.row_off[grp + 1] - row0;
+        part_of(p.splits, part, row0, size);
         const int i0 = (local % nti) * BM, j0 = (local / nti) * BN;
         f32x16 acc[MI][2];
 #pragma unroll
@@ -174,7 +188,7 @@ __global__ __launch_bounds__(NT, MI == 2 ? 4 : 1) void kernel(KmxParams p) {
         }
         // results turn in LDS, a strip of 32 x 64 a wave, and leave as whole row segments of 128 or 256 bytes, at any
         // alignment
-        O* out = (O*)p.out + (int64_t)grp * p.k * p.n;
+        O* out = (O*)p.out + ((int64_t)grp * p.splits + part) * p.k * p.n;
         float* strip = sm.strips[wave];
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
@@ -210,6 +224,39 @@ __global__ __launch_bounds__(NT, MI == 2 ? 4 : 1) void kernel(KmxParams p) {
         }
         __syncthreads();   // the strips share memory with the tiles
     }
+}
+
+// out[h] = alpha * (sum of its parts) + beta * out[h]; V consecutive values a thread
+template <typename O, int V>
+__global__ __launch_bounds__(256) void add_up(const float* __restrict__ parts, O* __restrict__ out, int64_t per, int splits, float alpha,
+                                              float beta) {
+    const int64_t e = ((int64_t)blockIdx.x * 256 + threadIdx.x) * V;
+    if (e >= per) return;
+    const float* from = parts + (int64_t)blockIdx.y * splits * per + e;
+    O* to = out + (int64_t)blockIdx.y * per + e;
+    float s[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) s[i] = 0.f;
+    for (int z = 0; z < splits; z += 4) {   // four parts' loads at a time, added in order
+        float f[4][V];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const float* at = from + (int64_t)min(z + u, splits - 1) * per;
+            if constexpr (V == 4) {
+                const f32x4 q = *(const f32x4_any*)at;
+#pragma unroll
+                for (int i = 0; i < V; ++i) f[u][i] = q[i];
+            } else {
+                f[u][0] = *at;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int i = 0; i < V; ++i) s[i] += z + u < splits ? f[u][i] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) put(to + i, alpha * s[i] + (beta != 0.f ? beta * get(to + i) : 0.f));
 }
 
 }  // namespace kmx
@@ -284,7 +331,7 @@ __global__ __launch_bounds__(NT, 1) void kernel(KmxParams p) {
     const int r0w = 128 * wm, c0w = 128 * wn;   // wave's sub-tile: output rows (k) r0w.., columns (n) c0w..
     const int nti = cdiv(p.k, BM), ntj = cdiv(p.n, BN);
     const int per = nti * ntj;
-    const int total = p.g * per;
+    const int total = p.g * p.splits * per;
     const bool lpt = p.g <= LPT_MAX_G;
     int gemm_tiles, covered;
     build_tables<NT>(p.group_sizes, p.g, p.m, 1, 0, sm.tab, &gemm_tiles, &covered);
@@ -324,10 +371,11 @@ __global__ __launch_bounds__(NT, 1) void kernel(KmxParams p) {
     const uint32_t lds_s = lds_u32(&sm.ring.scale[0][0][0]) + (uint32_t)wave_u * 256u;
 
     for (int tile = xcd_virtual_id(blockIdx.x, gridDim.x); tile < total; tile += gridDim.x) {
-        const int pg = tile / per;
-        int local = tile - pg * per;
-        const int grp = lpt ? sm.order[pg] : pg;
-        const int row_base = sm.tab.row_off[grp], size = sm.tab.row_off[grp + 1] - row_base;
+        const int vg = tile / per;
+        int local = tile - vg * per;
+        const int pg = vg / p.splits, part = vg - pg * p.splits, grp = lpt ? sm.order[pg] : pg;
+        int row_base = sm.tab.row_off[grp], size = sm.tab.row_off[grp + 1] - row_base;
+        part_of(p.splits, part, row_base, size);
         // (k-tile, n-tile) in super-tiles of SJ n-tiles
         const int full_sc = ntj / SJ;
         int it, jt;
@@ -494,7 +542,7 @@ __global__ __launch_bounds__(NT, 1) void kernel(KmxParams p) {
         wait_vm<0>();
         lds_barrier();
 
-        const rsrc_t ro = make_rsrc((const char*)p.out + ((size_t)grp * p.k + i0) * p.n * osz, (uint32_t)(rows_valid * p.n * osz));
+        const rsrc_t ro = make_rsrc((const char*)p.out + (((size_t)grp * p.splits + part) * p.k + i0) * p.n * osz, (uint32_t)(rows_valid * p.n * osz));
         static_assert(4 * 32 * (WCOLS + 4) * 4 <= (int)sizeof(sm.ring), "epilogue strips fit the ring");
         const EpiTile ep{nullptr, p.alpha, p.beta};
         store_acc<MI, NJ, WCOLS, OutT, EPI, true>(acc, reinterpret_cast<float*>(&sm.ring) + wave * 32 * (WCOLS + 4), ro, p.n, j0,
@@ -526,15 +574,23 @@ void launch(const KmxParams& p, int grid, hipStream_t s) {
 
 template <int MI, int BR, int SLOTS>
 static void launch_kmx(const KmxParams& p, int per_cu, int cus, hipStream_t s) {
-    const int64_t tiles = (int64_t)p.g * ((p.k + 64 * MI - 1) / (64 * MI)) * ((p.n + 255) / 256);
+    const int64_t tiles = (int64_t)p.g * p.splits * ((p.k + 64 * MI - 1) / (64 * MI)) * ((p.n + 255) / 256);
     const dim3 grid((uint32_t)std::max<int64_t>(1, std::min<int64_t>(tiles, (int64_t)per_cu * cus)));
     if (p.out_f32) hipLaunchKernelGGL((kmx::kernel<float, MI, BR, SLOTS>), grid, dim3(kmx::NT), 0, s, p);
     else hipLaunchKernelGGL((kmx::kernel<uint16_t, MI, BR, SLOTS>), grid, dim3(kmx::NT), 0, s, p);
 }
 
-hipError_t launch_ragged_k_mx(const KmxParams& p, int cus, hipStream_t s) {
+// Parts of a group's rows: where the tiles leave half the chip idle, as many as fill it, of at least 256 rows on average
+// (13232 rows of one group, k 192, n 4480, 18 tiles: 303 -> 45 us with 14 parts, 25 of them the sum of the parts).
+int ragged_k_mx_splits(int64_t m, int64_t k, int64_t n, int g) {
+    const int64_t tiles = g * ((k + 255) / 256) * ((n + 255) / 256);
+    if (tiles == 0 || tiles >= 128) return 1;
+    return (int)std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(32, 256 / tiles), m / (256 * (int64_t)g)));
+}
+
+static hipError_t launch_tiles(const KmxParams& p, int cus, hipStream_t s) {
     if (kmxr::ok(p)) {
-        const int64_t tiles = (int64_t)p.g * ((p.k + 255) / 256) * ((p.n + 255) / 256);
+        const int64_t tiles = (int64_t)p.g * p.splits * ((p.k + 255) / 256) * ((p.n + 255) / 256);
         const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(tiles, cus));
         const uint64_t a = ((uint64_t)p.m + 64u) * (uint64_t)p.k, b = ((uint64_t)p.m + 64u) * (uint64_t)p.n * 2u;
         if (a < (1ull << 31) && b < (1ull << 31)) kmxr::launch<false>(p, grid, s);
@@ -545,6 +601,25 @@ hipError_t launch_ragged_k_mx(const KmxParams& p, int cus, hipStream_t s) {
         launch_kmx<2, 32, 1>(p, 2, cus, s);
     } else {
         launch_kmx<4, 64, 2>(p, 1, cus, s);
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_ragged_k_mx(const KmxParams& p, int cus, hipStream_t s) {
+    if (p.splits == 1) return launch_tiles(p, cus, s);
+    KmxParams q = p;
+    q.out = q.parts; q.out_f32 = 1; q.alpha = 1.f; q.beta = 0.f;
+    const hipError_t e = launch_tiles(q, cus, s);
+    if (e != hipSuccess) return e;
+    const int64_t per = (int64_t)p.k * p.n;
+    const bool four = per % 4 == 0;
+    const dim3 grid((uint32_t)((per + (four ? 1024 : 256) - 1) / (four ? 1024 : 256)), p.g);
+    if (p.out_f32) {
+        if (four) hipLaunchKernelGGL((kmx::add_up<float, 4>), grid, dim3(256), 0, s, p.parts, (float*)p.out, per, p.splits, p.alpha, p.beta);
+        else hipLaunchKernelGGL((kmx::add_up<float, 1>), grid, dim3(256), 0, s, p.parts, (float*)p.out, per, p.splits, p.alpha, p.beta);
+    } else {
+        if (four) hipLaunchKernelGGL((kmx::add_up<uint16_t, 4>), grid, dim3(256), 0, s, p.parts, (uint16_t*)p.out, per, p.splits, p.alpha, p.beta);
+        else hipLaunchKernelGGL((kmx::add_up<uint16_t, 1>), grid, dim3(256), 0, s, p.parts, (uint16_t*)p.out, per, p.splits, p.alpha, p.beta);
     }
     return hipGetLastError();
 }

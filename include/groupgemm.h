@@ -260,7 +260,9 @@ gg_status gated_act_mxfp8_grad(const void* dh, const uint8_t* codes, const uint8
  *   out[h] = alpha * value(lhs[rows of h, :])^T . dout[rows of h, :] + beta * out[h]
  *   lhs [m, k] e4m3, lhs_scale [m, k/32], dout [m, n] bf16, out [g, k, n] fp32 or bf16; every element written (an
  *   empty group gives beta * out[h]).
- * Any n; k % 32 == 0 (GG_ERR_UNSUPPORTED).  lhs 16-byte aligned.  Workspace, status and errors as ragged_dot_k. */
+ * Any n; k % 32 == 0 (GG_ERR_UNSUPPORTED).  lhs 16-byte aligned.  Status and errors as ragged_dot_k; workspace
+ * gg_workspace_bytes(GG_OP_RAGGED_K, m, k, n, g, 0, GG_DT_E4M3): with few groups and small k and n a group's rows are
+ * summed in parts there, whose number depends on the sizes alone.  Overlaps of out with an input are not checked. */
 gg_status ragged_dot_k_mxfp8(const void* lhs, const uint8_t* lhs_scale, const void* dout, const int32_t* group_sizes,
                              void* out, int64_t m, int64_t k, int64_t n, int32_t g, gg_dtype out_dtype, float alpha,
                              float beta, void* workspace, size_t workspace_bytes, void* stream);

@@ -284,7 +284,7 @@ def test_weight_gradient(case, out_dtype):
     codes, scale, dout, x, d = wgrad_case(case, m, k, n, len(sizes))
     gs = torch.tensor(sizes, dtype=torch.int32, device=DEV)
     out, c = framed((len(sizes), k, n), out_dtype)
-    ws = torch.empty(256, dtype=torch.uint8, device=DEV)
+    ws = torch.empty(G.workspace_bytes("ragged_k", m, k, n, len(sizes), 0, torch.uint8), dtype=torch.uint8, device=DEV)
     G.ragged_dot_k(codes, dout, gs, out=out, lhs_scale=scale, workspace=ws)
     c()
     check_wgrad(out, x, d, sizes)
@@ -295,7 +295,8 @@ def test_weight_gradient(case, out_dtype):
 # whole 128 columns of k and whole 16 bytes of n: every count of 32-row slices up to the ring's wrap, long groups, tiles that
 # end inside a wave's part, several tiles a group
 RING = [(1, 128, 8, [1]), (300, 128, 264, [31, 32, 33, 64, 65, 75]), (500, 256, 256, [97, 128, 129, 146]), (700, 384, 520, [160, 161, 0, 379]),
-        (1500, 640, 72, [700, 0, 333, 400]), (900, 128, 1032, [225, 256, 257, 162]), (2100, 896, 312, [2100]), (64, 1152, 2064, [40, 24])]
+        (1500, 640, 72, [700, 0, 333, 400]), (900, 128, 1032, [225, 256, 257, 162]), (2100, 896, 312, [2100]), (64, 1152, 2064, [40, 24]),
+        (1700, 96, 40, [1500, 0, 190]), (3000, 64, 77, [2999, 1]), (900, 32, 520, [33, 867])]   # rows in parts
 
 
 @pytest.mark.parametrize("out_dtype", [F32, BF])
