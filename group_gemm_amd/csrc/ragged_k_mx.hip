@@ -70,10 +70,8 @@ __device__ inline void load(Regs<BR>& v, const KmxParams& p, int row0, int rows,
         v.b[i] = i32x4{0, 0, 0, 0};
         if (q >= rows || n0 >= p.n) continue;
         const uint16_t* at = p.dout + (int64_t)(row0 + q) * p.n + n0;
-        if (at + 8 <= p.dout + (int64_t)p.m * p.n) {   // what lies behind the row is masked
+        if (at + 8 <= p.dout + (int64_t)p.m * p.n) {   // what lies behind the row is masked later, so that no load waits
             v.b[i] = *(const i32x4_any*)at;
-#pragma unroll
-            for (int d = 0; d < 4; ++d) v.b[i][d] &= n0 + 2 * d + 2 <= p.n ? -1 : n0 + 2 * d + 1 == p.n ? 0xffff : 0;
         } else {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
@@ -82,7 +80,7 @@ __device__ inline void load(Regs<BR>& v, const KmxParams& p, int row0, int rows,
     }
 }
 template <int BR>
-__device__ inline void store(const Regs<BR>& v, uint16_t* a, uint16_t* b) {
+__device__ inline void store(const Regs<BR>& v, uint16_t* a, uint16_t* b, int cols) {   // cols: dout's left, from the tile's first
     const int t = threadIdx.x;
     const float s = __uint_as_float((uint32_t)v.byte << 23);   // exponent field 255 is NaN to the conversion
     if (t < 8 * BR)
@@ -98,7 +96,12 @@ __device__ inline void store(const Regs<BR>& v, uint16_t* a, uint16_t* b) {
         *(i32x4*)(a + off(t >> 3, 32 * (t & 7) + 8 * i)) = q;
     }
 #pragma unroll
-    for (int i = 0; i < BR / 16; ++i) *(i32x4*)(b + off((t >> 5) + 16 * i, 8 * (t & 31))) = v.b[i];
+    for (int i = 0; i < BR / 16; ++i) {
+        i32x4 q = v.b[i];
+#pragma unroll
+        for (int d = 0; d < 4; ++d) q[d] &= 8 * (t & 31) + 2 * d + 2 <= cols ? -1 : 8 * (t & 31) + 2 * d + 1 == cols ? 0xffff : 0;
+        *(i32x4*)(b + off((t >> 5) + 16 * i, 8 * (t & 31))) = q;
+    }
 }
 
 // rows 16 s + 8 (l / 32) .. + 7 of column col0 + l % 32
@@ -163,7 +166,7 @@ __global__ __launch_bounds__(NT, MI == 2 ? 4 : 1) void kernel(KmxParams p) {
         Regs<BR> v;
         if (size > 0) {
             load(v, p, row0, size, i0, min(p.k, i0 + BM), j0);
-            store(v, sm.a[0], sm.b[0]);
+            store(v, sm.a[0], sm.b[0], p.n - j0);
             __syncthreads();
         }
         int slot = 0;
@@ -183,7 +186,7 @@ __global__ __launch_bounds__(NT, MI == 2 ? 4 : 1) void kernel(KmxParams p) {
                     for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(b[j], a[i], acc[i][j], 0, 0, 0);
             }
             if (SLOTS == 1) __syncthreads();
-            if (more) store(v, sm.a[slot ^ (SLOTS - 1)], sm.b[slot ^ (SLOTS - 1)]);
+            if (more) store(v, sm.a[slot ^ (SLOTS - 1)], sm.b[slot ^ (SLOTS - 1)], p.n - j0);
             __syncthreads();
         }
         // results turn in LDS, a strip of 32 x 64 a wave, and leave as whole row segments of 128 or 256 bytes, at any
