@@ -51,10 +51,13 @@ template <> struct Frag<uint16_t> {
             if (e < valid) q[e >> 1] |= (int)((uint32_t)p[e] << (16 * (e & 1)));
         v = __builtin_bit_cast(bf16x8, q);
     }
-    // load_part where the eight lie before `end`, the array's: what is loaded past `valid` is masked
+    // load_part in two: what is loaded past `valid`, but before `end`, the array's, is masked when all loads are on their way
     __device__ void load_tail(const uint16_t* p, int valid, const uint16_t* end) {
-        if (p + 8 > end) { load_part(p, valid); return; }
-        i32x4 q = *(const i32x4_any*)p;
+        if (p + 8 > end) load_part(p, valid);
+        else load(p);
+    }
+    __device__ void mask(int valid) {
+        i32x4 q = __builtin_bit_cast(i32x4, v);
 #pragma unroll
         for (int d = 0; d < 4; ++d) q[d] &= valid >= 2 * d + 2 ? -1 : valid == 2 * d + 1 ? 0xffff : 0;
         v = __builtin_bit_cast(bf16x8, q);
@@ -75,8 +78,10 @@ template <> struct Frag<float> {
         }
     }
     __device__ void load_tail(const float* p, int valid, const float* end) {
-        if (p + 8 > end) { load_part(p, valid); return; }
-        load(p);
+        if (p + 8 > end) load_part(p, valid);
+        else load(p);
+    }
+    __device__ void mask(int valid) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             if (e >= valid) lo[e] = 0.f;
@@ -611,6 +616,12 @@ __device__ inline void columns(const Expand& p, const RowTile& w, int r0, int co
             }
         }
         fetch(next, c + 256);
+        if constexpr (!WHOLE) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int s = 0; s < STEPS; ++s) m[j][s].mask(p.r - 8 * min(4 * s + q, last));
+        }
 #pragma unroll
         for (int a = 0; a < MT; ++a) {
             f32x4 acc[4];
