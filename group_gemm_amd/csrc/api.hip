@@ -299,6 +299,7 @@ size_t gg_workspace_bytes(gg_op op, int64_t m, int64_t k, int64_t n, int32_t g, 
         }
         case GG_OP_LORA_GRAD: {
             if (capacity < 1 || capacity > GG_MAX_RANK || !fits_i32(m) || !fits_i32(k) || !fits_i32(n) || in == GG_DT_E4M3) return 0;
+            if (!gg::lora_grad_grid_ok(m, k, n, g)) return 0;   // (and the sizes below stay within 64 bits)
             return kHeader + lora_grad_layout(m, k, n, (int)capacity, g, in).bytes;
         }
         default: break;
@@ -773,6 +774,7 @@ gg_status ragged_lora(const void* x, const void* a, const void* b, const int32_t
     gg::lora::Rows rows{};
     rows.group_sizes = group_sizes; rows.row_group = row_group; rows.status = (uint32_t*)workspace; rows.m = (int)m; rows.g = g;
     gg::lora_rows(rows);
+    if (!gg::lora_grid_ok(rows, n)) return GG_ERR_BAD_SHAPE;
     const int splits = gg::lora_splits(m, k, r, g);
     float* t = splits == 1 && v ? v : (float*)((char*)workspace + kHeader);
     gg::lora::Shrink sh{rows, x, a, t, x_stride, (int)k, r, splits};
@@ -808,6 +810,7 @@ gg_status ragged_lora_grad(const void* x, const uint8_t* x_scale, const float* v
         !aligned(scaling, 4) || !aligned(dbase, es) || !aligned(dx, es) || !aligned(da, gs) || !aligned(db, gs) || !aligned(workspace, 16))
         return GG_ERR_MISALIGNED;
     const size_t need = gg_workspace_bytes(GG_OP_LORA_GRAD, m, k, n, g, r, dtype);
+    if (need == 0) return GG_ERR_BAD_SHAPE;
     if (workspace_bytes < need) return GG_ERR_WORKSPACE_TOO_SMALL;
     const Span xs = dense(x, M * K * xb), xss = dense(x_scale, M * K / 32), vs = dense(v, 4 * M * r), dos = dense(dout, M * N * es),
                as = dense(a, G * K * es), bs = dense(b, G * N * es), ids = dense(group_sizes, 4ull * g), sc = dense(scaling, 4ull * g),
@@ -827,6 +830,7 @@ gg_status ragged_lora_grad(const void* x, const uint8_t* x_scale, const float* v
     gg::lora::Rows rows{};
     rows.group_sizes = group_sizes; rows.m = (int)m; rows.g = g;
     gg::lora_rows(rows);
+    if (!gg::lora_grid_ok(rows, k)) return GG_ERR_BAD_SHAPE;
     hipError_t e = gg::launch_lora_turn(b, ws + w.bt, (int)n, r, dx ? a : nullptr, ws + w.at, r, (int)k, bf16, g, s);
     if (e != hipSuccess) return launched(e);
     gg::lora::Shrink sh{rows, dout, ws + w.bt, t, n, (int)n, r, splits};

@@ -203,6 +203,8 @@ struct Outer {                     // da[h] = scaling[h] sum u^T x, db[h] = scal
 void lora_rows(lora::Rows& r);
 int lora_splits(int64_t m, int64_t k, int r, int g);
 int lora_chunk(int64_t m, int64_t k, int64_t n);
+bool lora_grid_ok(const lora::Rows& r, int64_t n);
+bool lora_grad_grid_ok(int64_t m, int64_t k, int64_t n, int g);
 bool lora_both_ok(const lora::Shrink& p, bool bf16);   // one launch serves the shrink and the expand of its t
 hipError_t launch_lora_both(const lora::Shrink& sh, const lora::Expand& p, bool bf16, bool out_bf16, hipStream_t s);
 hipError_t launch_lora_shrink(const lora::Shrink& p, bool bf16, hipStream_t s);

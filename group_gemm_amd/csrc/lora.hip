@@ -1426,6 +1426,15 @@ static int64_t lora_tiles(const lora::Rows& r, int tm) {
 }
 static int lora_nb(int r) { return r <= 16 ? 1 : r <= 32 ? 2 : r <= 64 ? 4 : r <= 128 ? 8 : 16; }
 
+// Whether every launch over these rows and columns of the second product stays below a launch's workgroups: a call is
+// refused before the first of its launches or not at all.
+bool lora_grid_ok(const lora::Rows& r, int64_t n) { return lora_tiles(r, 16) * std::max<int64_t>(1, up64(n, 2048)) <= kMaxBlocks; }
+// the same for what the gradients add: both weights turned, and the row sums over 64 columns at the narrowest
+bool lora_grad_grid_ok(int64_t m, int64_t k, int64_t n, int g) {
+    const int64_t sums = (up64(m, lora_chunk(m, k, n)) + g) * (up64(k, 64) + up64(n, 64));
+    return sums <= kMaxBlocks && g * (up64(k, 16) + up64(n, 16)) <= kMaxBlocks;
+}
+
 template <typename T, int NB, int MT>
 static hipError_t shrink_t(const lora::Shrink& p, hipStream_t s) {
     constexpr int U = NB + MT <= 2 ? 4 : NB + MT <= 6 ? 2 : 1;

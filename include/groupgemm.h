@@ -282,6 +282,7 @@ gg_status ragged_dot_k_mxfp8(const void* lhs, const uint8_t* lhs_scale, const vo
  * x . a^T and the sum are fp32 (bf16 operands: x . a^T enters the second product as two bf16 values, 16 bits of fraction),
  * one rounding.  Rows of other adapters never meet a row's values, whatever they hold.  Results do not depend on the
  * launch, but rows sorted and rows in any order, and calls of other m, may add in other orders.
+ * Tiles of 16 rows and 2048 columns number up to 2^24 - 1 (GG_ERR_BAD_SHAPE past that).
  * Workspace: gg_workspace_bytes(GG_OP_LORA, m, k, n, g, r, dtype); status and errors as ragged_dot_m (with row_group the
  * status is 0). */
 gg_status ragged_lora(const void* x, const void* a, const void* b, const int32_t* group_sizes, const int32_t* row_group,

@@ -161,6 +161,23 @@ def test_workspace_bytes():
     assert need(6, 4096, 4096, 4096, 8, 16, BF16) < 256 + 2 * 8 * 16 * 8192 + 34 * 4096 * 16 * 4 + 2 * 17 * 8192 * 16 * 4
 
 
+def test_launch_limits():
+    """Shapes that need more workgroups than a launch holds are refused before the first of a call's launches."""
+    far = [(1 << 44) * i for i in range(1, 13)]
+    L = B.lib()
+
+    def lora_far(m, n, g, any_order):
+        ids = (None, far[3]) if any_order else (far[3], None)
+        return L.ragged_lora(far[0], far[1], far[2], *ids, None, far[4], far[5], None, m, 8, n, 4, g, 8, n, n, BF16, BF16, far[6], 1 << 43, None)
+
+    def grad_far(m, k, n, g):
+        return L.ragged_lora_grad(far[0], None, far[1], far[2], far[3], far[4], far[5], None, None, far[6], far[7], far[8], m, k, n, 4, g, BF16, BF16, F32,
+                                  far[9], 1 << 43, None)
+
+    assert lora_far(1 << 28, 8, 1, False) == lora_far(1 << 27, 4096, 1, False) == lora_far(1 << 24, 1 << 16, 8, True) == BAD_SHAPE
+    assert grad_far(1 << 28, 8, 8, 1) == grad_far(1, 1 << 28, 8, 1) == grad_far(1, 8, 1 << 20, 1024) == BAD_SHAPE
+
+
 # the binding's own checks, with CPU tensors in the place of the GPU's
 
 def no_call(monkeypatch):
