@@ -439,14 +439,14 @@ def moe_unpermute_grad(dout, y, copy_to_sorted, sorted_to_copy, weights):
 # ---------------------------------------------------------------------------------------
 # 8-bit activation checkpoints (MXFP8 rows: e4m3 codes [rows, k], one E8M0 byte per 32 along k) and the gated unit
 
-_c = np.arange(127)
-E4M3 = np.where(_c < 8, _c * 2.0 ** -9, (8 + _c % 8) * 2.0 ** (_c // 8 - 10.0))   # the finite magnitudes, by code
+_code = np.arange(127)
+E4M3_VALUES = np.where(_code < 8, _code * 2.0 ** -9, (8 + _code % 8) * 2.0 ** (_code // 8 - 10.0))   # the finite magnitudes, by code
 
 
 def mxfp8_values(codes, scale):
     """fp64 values [rows, k]; a scale byte of 255 makes its 32 values NaN, and so does the code 127 (either sign)."""
     c = np.asarray(codes, dtype=np.uint8).astype(np.int64)
-    v = np.where(c & 128, -1.0, 1.0) * np.append(E4M3, np.nan)[c & 127]
+    v = np.where(c & 128, -1.0, 1.0) * np.append(E4M3_VALUES, np.nan)[c & 127]
     s = np.asarray(scale, dtype=np.uint8).astype(np.float64)
     return v * np.repeat(np.where(s == 255, np.nan, 2.0 ** (s - 127)), 32, axis=-1)
 
@@ -464,7 +464,7 @@ def mxfp8_quantize(x):
     f = np.where(amax > 0, np.ldexp(amax, -e), 0.5)
     e = np.where(amax > 0, np.maximum(e - 9 + (f > 0.875), -127), -127)
     a = np.ldexp(np.abs(b), -e[..., None])
-    mid = (E4M3[:-1] + E4M3[1:]) / 2
+    mid = (E4M3_VALUES[:-1] + E4M3_VALUES[1:]) / 2
     code = np.searchsorted(mid, a, side="left")              # midpoints below a
     tie = (code < 126) & (a == mid[np.minimum(code, 125)])
     code = np.where(tie & (code % 2 == 1), code + 1, code)
