@@ -284,7 +284,7 @@ gg_status ragged_dot_k_mxfp8(const void* lhs, const uint8_t* lhs_scale, const vo
  * launch, but rows sorted and rows in any order, and calls of other m, may add in other orders.
  * Tiles of 16 rows and 2048 columns number up to 2^24 - 1 (GG_ERR_BAD_SHAPE past that).
  * Workspace: gg_workspace_bytes(GG_OP_LORA, m, k, n, g, r, dtype); status and errors as ragged_dot_m (with row_group the
- * status is 0). */
+ * status is 0; m = 0 launches nothing). */
 gg_status ragged_lora(const void* x, const void* a, const void* b, const int32_t* group_sizes, const int32_t* row_group,
                       const float* scaling, const void* base, void* out, float* v, int64_t m, int64_t k, int64_t n,
                       int32_t r, int32_t g, int64_t x_stride, int64_t base_stride, int64_t out_stride, gg_dtype dtype,

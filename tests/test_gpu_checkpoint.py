@@ -327,11 +327,11 @@ def test_weight_gradient_past_32_bits():
     check_wgrad((val(out[:, :, :16]), F32), x, ones, [30, 7])
 
 
-@pytest.mark.parametrize("k,n", [(256, 264), (288, 264), (288, 263)])
+@pytest.mark.parametrize("m,k,n", [(150, 256, 264), (150, 288, 264), (150, 288, 263), (1700, 96, 40), (1700, 96, 41)])
 @pytest.mark.parametrize("out_dtype", [F32, BF])
-def test_weight_gradient_accumulates(k, n, out_dtype):
-    say("wgrad in place", k, n, out_dtype)
-    m, sizes = 150, [70, 0, 80]
+def test_weight_gradient_accumulates(m, k, n, out_dtype):
+    say("wgrad in place", m, k, n, out_dtype)
+    sizes = [m - 80, 0, 80]
     codes, scale, dout, x, d = wgrad_case(50, m, k, n, 3)
     gs = torch.tensor(sizes, dtype=torch.int32, device=DEV)
     old = torch.randn(3, k, n, device=DEV).to(out_dtype)

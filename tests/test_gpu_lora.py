@@ -120,7 +120,8 @@ def test_sorted_rows(case, types):
 
 # m, k, n, r, g, chance of none: fewer rows than adapters and more, one adapter, several chunks of rows
 ANY = [(1, 64, 40, 16, 1, 0.0), (1, 1024, 520, 16, 8, 0.0), (3, 65, 33, 5, 1024, 0.3), (96, 512, 264, 32, 64, 0.1), (300, 192, 130, 8, 3, 0.5), (700, 128, 77, 16, 1, 0.2),
-       (1300, 96, 40, 4, 5, 0.0), (2100, 64, 72, 64, 70, 0.1), (40, 256, 300, 120, 2, 1.0), (64, 320, 64, 256, 9, 0.1)]
+       (1300, 96, 40, 4, 5, 0.0), (2100, 64, 72, 64, 70, 0.1), (40, 256, 300, 120, 2, 1.0), (64, 320, 64, 256, 9, 0.1),
+       (700, 128, 80, 16, 2, 0.3), (1500, 256, 264, 64, 3, 0.1), (1100, 131, 520, 32, 1, 0.5), (600, 75, 40, 128, 2, 0.0), (500, 64, 1032, 256, 1, 0.2)]
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
@@ -176,13 +177,45 @@ def test_strides_in_place_no_base_no_scaling(dtype, any_order):
 
 
 @pytest.mark.parametrize("any_order", [False, True])
-def test_values_of_other_rows_and_adapters(any_order):
+@pytest.mark.parametrize("types", [(BF, BF), (BF, F32)])
+def test_whole_lines_in_place_strided_and_without_base(types, any_order):
+    """Many rows an adapter and widths of whole 16 bytes, with rows without an adapter: as above."""
+    say("lines", types, any_order)
+    m, k, n, r, g = 400, 128, 264, 24, 3
+    rng, x, a, b, s = make(17, m, k, n, r, g, types[0])
+    rows = oracle.row_groups([200, 0, 120], m)
+    pick = dict(row_group=ints(rows)) if any_order else dict(group_sizes=ints([200, 0, 120]))
+    plain = G.ragged_lora(x, a, b, scaling=s, out_dtype=types[1], **pick)
+    want, _ = oracle.ragged_lora(val(x), val(a), val(b), rows, val(s))
+    _, eo = bounds(val(x), val(a), val(b), rows, val(s), types[1], True, want)
+    within(val(plain), want, eo)
+    assert not bool(plain[320:].any())
+    base = rand(rng, (m, n), types[1])
+    dense = G.ragged_lora(x, a, b, base=base, scaling=s, **pick)
+    want, _ = oracle.ragged_lora(val(x), val(a), val(b), rows, val(s), val(base))
+    _, eo = bounds(val(x), val(a), val(b), rows, val(s), types[1], True, want, val(base))
+    within(val(dense), want, eo)
+    wide = torch.full((m, 3 * n), float("nan"), dtype=types[1], device=DEV)
+    out = wide[:, n:2 * n]
+    out.copy_(base)
+    G.ragged_lora(x, a, b, base=out, out=out, scaling=s, **pick)
+    assert torch.equal(out, dense) and bool(wide[:, :n].isnan().all()) and bool(wide[:, 2 * n:].isnan().all())
+    both = torch.zeros(m, 2 * n, dtype=types[1], device=DEV)
+    both[:, :n] = base
+    G.ragged_lora(x, a, b, base=both[:, :n], out=both[:, n:], scaling=s, **pick)
+    assert torch.equal(both, torch.cat([base, dense], 1))
+
+
+@pytest.mark.parametrize("any_order", [False, True])
+@pytest.mark.parametrize("wide", [1, 8])
+def test_values_of_other_rows_and_adapters(any_order, wide):
     """An adapter of NaN and infinities, rows of NaN and a base of NaN stay where they belong."""
-    say("non-finite", any_order)
-    m, k, n, r, g = 90, 200, 136, 16, 5
+    say("non-finite", any_order, wide)
+    m, k, n, r, g = 90 * wide, 200, 136, 16, 5
+    sizes = [20 * wide, 15 * wide, 20 * wide, 0, 20 * wide]
     rng, x, a, b, s = make(8, m, k, n, r, g, BF)
-    rows = rng.permutation(oracle.row_groups([20, 15, 20, 0, 20], m)) if any_order else oracle.row_groups([20, 15, 20, 0, 20], m)
-    pick = dict(row_group=ints(rows)) if any_order else dict(group_sizes=ints([20, 15, 20, 0, 20]))
+    rows = rng.permutation(oracle.row_groups(sizes, m)) if any_order else oracle.row_groups(sizes, m)
+    pick = dict(row_group=ints(rows)) if any_order else dict(group_sizes=ints(sizes))
     base = rand(rng, (m, n), BF)
     good = G.ragged_lora(x, a, b, base=base, scaling=s, **pick)
     a[1], b[3], b[1, 0] = float("nan"), float("inf"), float("inf")
