@@ -842,8 +842,7 @@ gg_status ragged_lora_grad(const void* x, const uint8_t* x_scale, const float* v
     o.group_sizes = group_sizes; o.status = (uint32_t*)workspace; o.x = x; o.x_scale = e4m3 ? x_scale : nullptr; o.dout = dout;
     o.u = u; o.v = v; o.scaling = scaling; o.parts = (float*)(ws + w.parts); o.da = da; o.db = db;
     o.m = (int)m; o.k = (int)k; o.n = (int)n; o.r = r; o.g = g; o.chunk = gg::lora_chunk(m, k, n); o.grads_bf16 = grad_dtype == GG_DT_BF16;
-    // With splits the expand sums them, so it goes first (without dx it does only that).  Without, the row sums read
-    // dout again, from its end, while the last-level cache still holds that.
+    // with splits the expand sums them for the row sums, so it goes first (without dx it does only that)
     if (both) {
         ex.v = u;
         e = gg::launch_lora_both(sh, ex, bf16, bf16, s);

@@ -5,12 +5,15 @@
 //   da[h] = s[h] sum_i u[i]^T x[i],  db[h] = s[h] sum_i dout[i]^T v[i].
 // r is small beside k and n, so all of it is bound by reading x, base and dout and writing out and dx once.
 //
-// Three kernels.  `shrink` contracts the long axis (v, u): a tile of rows of one adapter against its r rows of
-// weights, the axis split over the four waves of a workgroup and, for few rows, over workgroups.  `expand` contracts
-// r and adds the other term.  `outer` contracts the rows of a group (da, db), in chunks of rows that `join` adds up
-// in order where a group has more than one: no atomics, so results do not depend on the launch.
+// Three products.  `shrink` contracts the long axis (v, u): a tile of rows of one adapter against its r rows of
+// weights, the axis split over workgroups where the rows are few.  `expand` contracts r and adds the other term.
+// `outer` contracts the rows of a group (da, db), in chunks of rows that `join` adds up in order where a group has
+// more than one: no atomics, so results do not depend on the launch.
 // The backward pass is the forward one with the weights' axes swapped, so `turn` writes b as [g, r, n] and a as
 // [g, k, r] once a call, which is small, and `shrink` and `expand` serve both.
+// Each has a kernel for rows of whole 16 bytes (shrink_ring, expand_lines) and one or two for the rest; few rows take both
+// products in one launch (`both`).  Measured, 8192 bf16 rows, 4096 x 14336, rank 64: x is read in 25 us
+// (2.7 TB/s), base read and out written in 108 (4.3 TB/s; a copy reaches 4.9).
 //
 // Products of bf16 weights with the fp32 v and u run on the bf16 matrix instructions with v and u as a sum of two
 // bf16 values (16 bits of fraction, so their error stays below a bf16 result's and 2^-17 of an fp32 one), of three
@@ -30,7 +33,6 @@ constexpr int KC = 64;           // elements of the long axis that a wave takes 
 constexpr int MAXCHUNK = 1024;   // rows in any order: of these many, a workgroup takes those of its adapter
 constexpr int NONE = 64;         // and of these many those without one
 
-typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 // 16 bytes that may begin at any element (the target's global memory takes that)
 typedef i32x4 __attribute__((aligned(2))) i32x4_any;
@@ -208,14 +210,15 @@ __device__ inline RowTile row_tile(const Rows& p, int id, int tm, RowList& any, 
 __device__ inline int row_at(const RowTile& w, int i) { return w.list ? w.list[i] : w.first + i; }
 
 // ---------------------------------------------------------------------------------------------------------------
-// shrink: t[split, row, j] = x[row] . w[h][j], over the split's part of the long axis.  16 MT rows, 16 NB columns j.
-// The weights are the first operand, so a lane ends with four consecutive j of one row.
+// shrink: t[split, row, j] = x[row] . w[h][j], over the split's part of the long axis.  16 rows, 16 NB columns j.
+// The weights are the first operand, so a lane ends with four consecutive j of one row.  This one is for few rows of any
+// alignment: the four waves take the axis in turn, fragments come straight from memory.
 
-template <typename T, int NB, int MT, int U>   // U pieces of the axis in flight
+template <typename T, int NB, int U>   // U pieces of the axis in flight
 __global__ __launch_bounds__(NT) void shrink(Shrink p) {
-    constexpr int TM = 16 * MT;
+    constexpr int TM = 16;
     __shared__ RowList rs;
-    __shared__ union { f32x4 red[2][MT * NB * 64]; Tables tab; } sm;
+    __shared__ union { f32x4 red[2][NB * 64]; Tables tab; } sm;
     auto& red = sm.red;
     const RowTile w = row_tile(p.rows, blockIdx.x, TM, rs, &sm);
     if (w.h < 0 || w.rows == 0) return;
@@ -226,24 +229,19 @@ __global__ __launch_bounds__(NT) void shrink(Shrink p) {
 #pragma unroll
     for (int b = 0; b < NB; ++b) wp[b] = (const T*)p.w + ((int64_t)w.h * p.r + min(16 * b + i16, p.r - 1)) * p.k + 8 * q;
     for (int r0 = 0; r0 < w.rows; r0 += TM) {
-        const T* xp[MT];
+        const T* xp = (const T*)p.x + (int64_t)row_at(w, min(r0 + i16, w.rows - 1)) * p.stride + 8 * q;
+        f32x4 acc[NB];
 #pragma unroll
-        for (int a = 0; a < MT; ++a) xp[a] = (const T*)p.x + (int64_t)row_at(w, min(r0 + 16 * a + i16, w.rows - 1)) * p.stride + 8 * q;
-        f32x4 acc[MT][NB];
-#pragma unroll
-        for (int a = 0; a < MT; ++a)
-#pragma unroll
-            for (int b = 0; b < NB; ++b) acc[a][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int b = 0; b < NB; ++b) acc[b] = f32x4{0.f, 0.f, 0.f, 0.f};
         const int whole = min(c1, p.k / KC);   // chunks that lie inside the axis
         auto pieces = [&](int c, auto u_c) {
             constexpr int N = decltype(u_c)::value;
-            Frag<T> x[N][2][MT], m[N][2][NB];
+            Frag<T> x[N][2], m[N][2][NB];
 #pragma unroll
             for (int u = 0; u < N; ++u)
 #pragma unroll
                 for (int s = 0; s < 2; ++s) {
-#pragma unroll
-                    for (int a = 0; a < MT; ++a) x[u][s][a].load(xp[a] + (int64_t)(c + 4 * u) * KC + 32 * s);
+                    x[u][s].load(xp + (int64_t)(c + 4 * u) * KC + 32 * s);
 #pragma unroll
                     for (int b = 0; b < NB; ++b) m[u][s][b].load(wp[b] + (int64_t)(c + 4 * u) * KC + 32 * s);
                 }
@@ -252,9 +250,7 @@ __global__ __launch_bounds__(NT) void shrink(Shrink p) {
 #pragma unroll
                 for (int s = 0; s < 2; ++s)
 #pragma unroll
-                    for (int b = 0; b < NB; ++b)
-#pragma unroll
-                        for (int a = 0; a < MT; ++a) acc[a][b] = Frag<T>::mma(m[u][s][b], x[u][s][a], acc[a][b]);
+                    for (int b = 0; b < NB; ++b) acc[b] = Frag<T>::mma(m[u][s][b], x[u][s], acc[b]);
         };
         int c = c0 + wave;
         for (; c + 4 * (U - 1) < whole; c += 4 * U) pieces(c, std::integral_constant<int, U>{});
@@ -264,15 +260,12 @@ __global__ __launch_bounds__(NT) void shrink(Shrink p) {
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 const int valid = p.k - whole * KC - 32 * s - 8 * q;
-                Frag<T> x[MT], m[NB];
-#pragma unroll
-                for (int a = 0; a < MT; ++a) x[a].load_part(xp[a] + (int64_t)whole * KC + 32 * s, valid);
+                Frag<T> x, m[NB];
+                x.load_part(xp + (int64_t)whole * KC + 32 * s, valid);
 #pragma unroll
                 for (int b = 0; b < NB; ++b) m[b].load_part(wp[b] + (int64_t)whole * KC + 32 * s, valid);
 #pragma unroll
-                for (int b = 0; b < NB; ++b)
-#pragma unroll
-                    for (int a = 0; a < MT; ++a) acc[a][b] = Frag<T>::mma(m[b], x[a], acc[a][b]);
+                for (int b = 0; b < NB; ++b) acc[b] = Frag<T>::mma(m[b], x, acc[b]);
             }
         }
         // waves 2 and 3 to 0 and 1, then 1 to 0
@@ -280,30 +273,22 @@ __global__ __launch_bounds__(NT) void shrink(Shrink p) {
         for (int half = 2; half >= 1; half >>= 1) {
             if (wave >= half && wave < 2 * half)
 #pragma unroll
-                for (int a = 0; a < MT; ++a)
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) red[wave - half][(a * NB + b) * 64 + l] = acc[a][b];
+                for (int b = 0; b < NB; ++b) red[wave - half][b * 64 + l] = acc[b];
             __syncthreads();
             if (wave < half)
 #pragma unroll
-                for (int a = 0; a < MT; ++a)
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) acc[a][b] += red[wave][(a * NB + b) * 64 + l];
+                for (int b = 0; b < NB; ++b) acc[b] += red[wave][b * 64 + l];
             __syncthreads();
         }
-        if (wave == 0) {
+        if (wave == 0 && r0 + i16 < w.rows) {
+            float* to = p.t + ((int64_t)blockIdx.y * p.rows.m + row_at(w, r0 + i16)) * p.r;
 #pragma unroll
-            for (int a = 0; a < MT; ++a) {
-                if (r0 + 16 * a + i16 >= w.rows) continue;
-                float* to = p.t + ((int64_t)blockIdx.y * p.rows.m + row_at(w, r0 + 16 * a + i16)) * p.r;
+            for (int b = 0; b < NB; ++b)
 #pragma unroll
-                for (int b = 0; b < NB; ++b)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int j = 16 * b + 4 * q + e;
-                        if (j < p.r) to[j] = acc[a][b][e];
-                    }
-            }
+                for (int e = 0; e < 4; ++e) {
+                    const int j = 16 * b + 4 * q + e;
+                    if (j < p.r) to[j] = acc[b][e];
+                }
         }
     }
 }
@@ -1412,10 +1397,9 @@ int lora_chunk(int64_t m, int64_t k, int64_t n) {
     return (int)std::min<int64_t>(2048, std::max<int64_t>(512, c));
 }
 
-// Rows a tile (16 MT): more where a group has that many on average.
-static int lora_mt(const lora::Rows& r, int nb, int most) {
-    const int64_t rows = r.group_sizes ? r.m / r.g : std::min<int64_t>(r.m, r.chunk) / std::max(1, r.slots);
-    return rows >= 32 ? (nb >= 8 ? 2 : most) : 1;
+// Whether an adapter has enough rows on average to fill tiles of more than 16
+static bool lora_many(const lora::Rows& r) {
+    return (r.group_sizes ? r.m / r.g : std::min<int64_t>(r.m, r.chunk) / std::max(1, r.slots)) >= 32;
 }
 void lora_rows(lora::Rows& r) {
     r.chunk = (int)std::min<int64_t>(lora::MAXCHUNK, std::max<int64_t>(256, up64((int64_t)32 * r.g, 256) * 256));
@@ -1435,12 +1419,12 @@ bool lora_grad_grid_ok(int64_t m, int64_t k, int64_t n, int g) {
     return sums <= kMaxBlocks && g * (up64(k, 16) + up64(n, 16)) <= kMaxBlocks;
 }
 
-template <typename T, int NB, int MT>
+template <typename T, int NB>
 static hipError_t shrink_t(const lora::Shrink& p, hipStream_t s) {
-    constexpr int U = NB + MT <= 2 ? 4 : NB + MT <= 6 ? 2 : 1;
-    const int64_t tiles = lora_tiles(p.rows, 16 * MT);
+    constexpr int U = NB == 1 ? 4 : NB <= 4 ? 2 : 1;
+    const int64_t tiles = lora_tiles(p.rows, 16);
     if (tiles > kMaxBlocks) return hipErrorInvalidConfiguration;
-    hipLaunchKernelGGL((lora::shrink<T, NB, MT, U>), dim3((uint32_t)tiles, p.splits), dim3(lora::NT), 0, s, p);
+    hipLaunchKernelGGL((lora::shrink<T, NB, U>), dim3((uint32_t)tiles, p.splits), dim3(lora::NT), 0, s, p);
     return hipGetLastError();
 }
 template <typename T, int NB>
@@ -1462,17 +1446,18 @@ static bool shrink_lines(const lora::Shrink& p, int64_t es) {   // rows of whole
 }
 template <typename T>
 static hipError_t shrink_nb(const lora::Shrink& p, hipStream_t s) {
-    const int nb = lora_nb(p.r), mt = lora_mt(p.rows, nb, 2);
+    const int nb = lora_nb(p.r);
+    const bool many = lora_many(p.rows);
     if (shrink_lines(p, sizeof(T))) {
         switch (nb) {
-            case 1: return mt == 1 ? shrink_ring_t<T, 1, 1, 4>(p, s) : shrink_ring_t<T, 1, 4, 5>(p, s);
-            case 2: return mt == 1 ? shrink_ring_t<T, 2, 1, 3>(p, s) : shrink_ring_t<T, 2, 4, 5>(p, s);
-            case 4: return mt == 1 ? shrink_ring_t<T, 4, 1, 3>(p, s) : shrink_ring_t<T, 4, 4, 4>(p, s);
-            case 8: return mt == 1 ? shrink_ring_t<T, 8, 1, 2>(p, s) : shrink_ring_t<T, 8, 4, 3>(p, s);
+            case 1: return many ? shrink_ring_t<T, 1, 4, 5>(p, s) : shrink_ring_t<T, 1, 1, 4>(p, s);
+            case 2: return many ? shrink_ring_t<T, 2, 4, 5>(p, s) : shrink_ring_t<T, 2, 1, 3>(p, s);
+            case 4: return many ? shrink_ring_t<T, 4, 4, 4>(p, s) : shrink_ring_t<T, 4, 1, 3>(p, s);
+            case 8: return many ? shrink_ring_t<T, 8, 4, 3>(p, s) : shrink_ring_t<T, 8, 1, 2>(p, s);
             default: return shrink_ring_t<T, 16, 4, 3>(p, s);   // a ring a wave would not fit the LDS
         }
     }
-    if (mt > 1) {
+    if (many) {
         switch (nb) {
             case 1: return shrink_staged_t<T, 1>(p, s);
             case 2: return shrink_staged_t<T, 2>(p, s);
@@ -1482,11 +1467,11 @@ static hipError_t shrink_nb(const lora::Shrink& p, hipStream_t s) {
         }
     }
     switch (nb) {
-        case 1: return shrink_t<T, 1, 1>(p, s);
-        case 2: return shrink_t<T, 2, 1>(p, s);
-        case 4: return shrink_t<T, 4, 1>(p, s);
-        case 8: return shrink_t<T, 8, 1>(p, s);
-        default: return shrink_t<T, 16, 1>(p, s);
+        case 1: return shrink_t<T, 1>(p, s);
+        case 2: return shrink_t<T, 2>(p, s);
+        case 4: return shrink_t<T, 4>(p, s);
+        case 8: return shrink_t<T, 8>(p, s);
+        default: return shrink_t<T, 16>(p, s);
     }
 }
 hipError_t launch_lora_shrink(const lora::Shrink& p, bool bf16, hipStream_t s) {
@@ -1526,9 +1511,8 @@ template <typename O> static bool expand_lines_ok(const lora::Expand& p) {
 template <typename T, typename O>
 static hipError_t expand_nb(const lora::Expand& p, hipStream_t s) {
     if constexpr (sizeof(T) == 2) {
-        const int nb = lora_nb(p.r);
-        if (lora_mt(p.rows, nb, 4) > 1 && expand_lines_ok<O>(p)) {
-            switch (nb) {
+        if (lora_many(p.rows) && expand_lines_ok<O>(p)) {
+            switch (lora_nb(p.r)) {
                 case 1: return expand_lines_t<O, 1, 2>(p, s);
                 case 2: return expand_lines_t<O, 2, 2>(p, s);
                 case 4: return expand_lines_t<O, 4, 2>(p, s);
@@ -1538,21 +1522,21 @@ static hipError_t expand_nb(const lora::Expand& p, hipStream_t s) {
         }
     }
     // few rows and columns: small tiles (more workgroups, and half the instructions for each to fetch)
-    const int nb = lora_nb(p.r), mt = up64(p.rows.m, 64) * up64(p.n, 256) < 512 ? 1 : lora_mt(p.rows, nb, 2);
-    switch (nb) {
-        case 1: return mt == 1 ? expand_t<T, O, 1, 1>(p, s) : expand_t<T, O, 1, 2>(p, s);
-        case 2: return mt == 1 ? expand_t<T, O, 2, 1>(p, s) : expand_t<T, O, 2, 2>(p, s);
-        case 4: return mt == 1 ? expand_t<T, O, 4, 1>(p, s) : expand_t<T, O, 4, 2>(p, s);
-        case 8: return mt == 1 ? expand_t<T, O, 8, 1>(p, s) : expand_t<T, O, 8, 2>(p, s);
+    const bool many = up64(p.rows.m, 64) * up64(p.n, 256) >= 512 && lora_many(p.rows);
+    switch (lora_nb(p.r)) {
+        case 1: return many ? expand_t<T, O, 1, 2>(p, s) : expand_t<T, O, 1, 1>(p, s);
+        case 2: return many ? expand_t<T, O, 2, 2>(p, s) : expand_t<T, O, 2, 1>(p, s);
+        case 4: return many ? expand_t<T, O, 4, 2>(p, s) : expand_t<T, O, 4, 1>(p, s);
+        case 8: return many ? expand_t<T, O, 8, 2>(p, s) : expand_t<T, O, 8, 1>(p, s);
         default: return expand_t<T, O, 16, 1>(p, s);
     }
 }
 // Few rows an adapter, rows of whole 16 bytes, and first weights of at most 128 KiB an adapter: both products in one launch.
-// (One token at rank 16 and 4096 columns: 7.2 us in one launch, 4.1 + 5.2 in two, and the host's 2.8 for the second; 96 rows at 64
-// adapters of 448 KiB: 20 us in one, since every workgroup streams the weights for itself, 6.9 + 6.8 in two.)
+// (One token at rank 16 and 4096 columns: 7.7 us in one launch, 4.1 + 5.2 in two, and the host's 2.8 for the second; 96 rows at 64
+// adapters of 448 KiB: 20 us in one, since every workgroup streams the weights for itself, 7.8 + 6.0 in two.)
 bool lora_both_ok(const lora::Shrink& p, bool bf16) {
     const int64_t es = bf16 ? 2 : 4;
-    return lora_mt(p.rows, 1, 4) == 1 && p.r <= 64 && p.r * (int64_t)p.k * es <= (1 << 17) && shrink_lines(p, es);
+    return !lora_many(p.rows) && p.r <= 64 && p.r * (int64_t)p.k * es <= (1 << 17) && shrink_lines(p, es);
 }
 template <typename T, typename O, int NB, int D>
 static hipError_t both_t(const lora::Shrink& sh, lora::Expand p, hipStream_t s) {
@@ -1613,7 +1597,7 @@ static hipError_t outer_t(const lora::Outer& p, hipStream_t s) {
 }
 template <OuterX X, int P>
 static hipError_t outer_nb(const lora::Outer& p, hipStream_t s) {
-    // few workgroups: narrower ones (375 rows of 5 groups in fp32, k 1030, n 515: 15.2 -> 11.8 us)
+    // few workgroups: narrower ones (375 rows of 5 groups in fp32, k 1030, n 515: 15.2 us with wide ones, 7.5 with these)
     const int64_t groups = std::max<int64_t>(up64(p.m, p.chunk), std::min<int64_t>(p.g, up64(p.m, 32)));
     if (p.r <= 64 && groups * (up64(p.k, 256) + up64(p.n, 256)) < 256) {
         switch (lora_nb(p.r)) {

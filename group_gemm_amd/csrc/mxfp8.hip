@@ -12,7 +12,9 @@
 //   h = gate p up;   dgate = dh up (p + gate p (1 - p) y'),   dup = dh gate p.
 //
 // All kernels move each byte once and are bound by memory; eight elements a lane, so a block is four lanes and
-// its maximum two lane exchanges.
+// its maximum two lane exchanges.  Measured in bf16, 16384 rows of 5120 values: to 8 bits in 41 us (254 MB) and back in 36;
+// 8192 rows of width 14336: the unit with its checkpoint 140 us (947 MB with h), its gradient with h 193 (1182 MB; a copy's
+// rate would be 236, but part of what the caller just wrote is still in the last-level cache).
 #include "common.hpp"
 #include "launch.hpp"
 
@@ -267,7 +269,9 @@ __global__ __launch_bounds__(256) void gated_grad(GatedGradArgs p) {
 
 }  // namespace fp8
 
-constexpr int kU = 2;   // eights a lane: see launches
+// Eights a lane that the conversions of rows have on their way (16384 rows of 5120 bf16 values to 8 bits and back: 80 us with
+// one, 78 with two or four).  The gated unit's lanes load two or three arrays and take one eight.
+constexpr int kU = 2;
 static uint32_t fp8_blocks(uint32_t eights, int u) { return (eights + 256u * u - 1) / (256u * u); }
 
 hipError_t launch_fp8_quantize(const void* x, bool bf16, int64_t rows, int64_t k, int64_t stride, uint8_t* codes, uint8_t* scale,

@@ -118,7 +118,7 @@ __device__ inline float get(const float* p) { return *p; }
 __device__ inline float get(const uint16_t* p) { return __uint_as_float((uint32_t)*p << 16); }
 __device__ inline void put(float* p, float v) { *p = v; }
 // (stores that the caches may hold back: a row of odd length shares its first and last line with its neighbours, and with
-// the nontemporal hint each part went out by itself, 161 instead of 79 us for 32 groups of 12 rows, k 2880, n 1447)
+// the nontemporal hint each part went out by itself, 161 instead of 81 us for 32 groups of 12 rows, k 2880, n 1447)
 __device__ inline void put8(float* p, const float (&v)[8]) {
     *(f32x4_any*)p = f32x4{v[0], v[1], v[2], v[3]};
     *(f32x4_any*)(p + 4) = f32x4{v[4], v[5], v[6], v[7]};
@@ -270,6 +270,8 @@ __global__ __launch_bounds__(256) void add_up(const float* __restrict__ parts, O
 // (one) and turns them itself, during the first half of the iteration before the one that multiplies them: its own loads are
 // what it waits for, and the barrier that the iteration has anyway shows the bf16 slice to the other waves.  That is 16
 // conversions, four LDS reads and four writes a wave beside 32 matrix instructions.
+// Bound by the matrix instructions: 16384 rows of 16 groups, k 5120, n 8192, fp32 out, 1537 us or 895 TFLOP/s with groups of
+// one size (the bf16 kernel 1410 to 1465) and 1605 with uneven ones, whose 2.7 GB of output alone take 550 at a copy's rate.
 namespace kmxr {
 using namespace ring;
 
@@ -584,7 +586,7 @@ static void launch_kmx(const KmxParams& p, int per_cu, int cus, hipStream_t s) {
 }
 
 // Parts of a group's rows: where the tiles leave half the chip idle, as many as fill it, of at least 256 rows on average
-// (13232 rows of one group, k 192, n 4480, 18 tiles: 303 -> 45 us with 14 parts, 25 of them the sum of the parts).
+// (13232 rows of one group, k 192, n 4480, 18 tiles: 303 us in one part, 41 + 10 with 14, the 10 for their sum).
 int ragged_k_mx_splits(int64_t m, int64_t k, int64_t n, int g) {
     const int64_t tiles = g * ((k + 255) / 256) * ((n + 255) / 256);
     if (tiles == 0 || tiles >= 128) return 1;
