@@ -357,6 +357,24 @@ def test_weight_gradient_of_values_behind_the_groups(k):
     assert np.array_equal(np.isnan(got).all(-1), bad) and np.array_equal(np.isnan(got).any(-1), bad)
 
 
+@pytest.mark.parametrize("m,k,n", [(150, 96, 41), (150, 288, 264), (1700, 96, 40), (1700, 96, 41)])
+def test_weight_gradient_of_non_finite_neighbours(m, k, n):
+    """A group of NaN between two others, and NaN behind the last, reach neither, with the rows in parts too."""
+    say("wgrad neighbours", m, k, n)
+    sizes = [m // 2 - 3, m // 4 + 1, m // 8 + 5]
+    codes, scale, dout, x, d = wgrad_case(70, m, k, n, 3)
+    at = [slice(sizes[0], sum(sizes[:2])), slice(sum(sizes), m)]
+    for i in at:
+        scale[i], dout[i] = 255, float("inf")
+    out = val(G.ragged_dot_k(codes, dout, torch.tensor(sizes, dtype=torch.int32, device=DEV), lhs_scale=scale))
+    assert np.isnan(out[1]).all()
+    x, d = x.copy(), d.copy()
+    for i in at:
+        x[i], d[i] = 0, 0
+    out[1] = 0
+    check_wgrad((out, F32), x, d, sizes)
+
+
 # ---------------------------------------------------------------------------------------------------------------
 # together, captured, on other streams
 

@@ -233,6 +233,36 @@ def test_values_of_other_rows_and_adapters(any_order, wide):
     assert torch.equal(got[torch.from_numpy(~bad).to(DEV)], good[torch.from_numpy(~bad).to(DEV)])
 
 
+@pytest.mark.parametrize("any_order", [False, True])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("wide", [1, 10])
+@pytest.mark.parametrize("knr", [(131, 77, 11), (75, 264, 24), (128, 264, 40), (515, 131, 100), (192, 72, 3)])
+def test_non_finite_neighbours_at_odd_sizes(knr, wide, dtype, any_order):
+    """What lies behind a row's end, a rank's end and a column's weights is another row's, adapter's or column's."""
+    say("non-finite odd", knr, wide, dtype, any_order)
+    k, n, r = knr
+    sizes, m = [13 * wide, 9 * wide, 11 * wide], 37 * wide
+    rng, x, a, b, s = make(18, m, k, n, r, 3, dtype)
+    rows = rng.permutation(oracle.row_groups(sizes, m)) if any_order else oracle.row_groups(sizes, m)
+    pick = dict(row_group=ints(rows)) if any_order else dict(group_sizes=ints(sizes))
+    base = rand(rng, (m, n), dtype)
+    good = G.ragged_lora(x, a, b, base=base, scaling=s, **pick)
+    bad = np.zeros((m, n), bool)
+    a[1], b[1] = float("nan"), float("inf")                # the adapter behind the first and before the last
+    bad[rows == 1] = True
+    at = np.flatnonzero(rows != 1)[::3]                    # rows of infinities beside rows without
+    x[torch.from_numpy(at).to(DEV)] = float("inf")
+    bad[at] = True
+    bad[rows < 0] = False
+    for c in (0, n // 2, n - 1):                           # whole columns of infinities
+        b[0, c], b[2, c] = float("inf"), float("nan")
+        bad[(rows == 0) | (rows == 2), c] = True
+    got = G.ragged_lora(x, a, b, base=base, scaling=s, **pick)
+    ok = torch.from_numpy(~bad).to(DEV)
+    assert bool(ok.any()) and torch.equal(got[ok], good[ok])
+    assert not np.isfinite(val(got)[bad]).any()
+
+
 def test_same_result_twice_and_sorted_as_in_any_order():
     say("twice")
     m, k, n, r, g = 500, 1024, 640, 16, 3
@@ -349,6 +379,33 @@ def test_gradients_and_values_behind_the_groups(x8):
     v[73:], dout[73:], a[1], b[1], s[1] = float("nan"), float("inf"), float("nan"), float("nan"), float("nan")
     got = G.ragged_lora_grad(x, v, dout, a, b, ints(sizes), **args)
     assert all(torch.equal(p, q) for p, q in zip(good, got))
+
+
+@pytest.mark.parametrize("wide", [1, 16])
+@pytest.mark.parametrize("types", [(BF, False), (BF, True), (F32, False)])
+@pytest.mark.parametrize("knr", [(131, 77, 11), (75, 264, 24), (192, 136, 40), (515, 131, 100)])
+def test_gradients_of_non_finite_neighbours_at_odd_sizes(knr, types, wide):
+    """NaN in everything of one group, and behind the last, reaches no other group, also where a group ends inside a tile."""
+    say("grad non-finite odd", knr, types, wide)
+    dtype, x8 = types
+    k, n, r = knr[0] // 32 * 32 if x8 else knr[0], knr[1], knr[2]
+    sizes, m = [33 * wide, 21 * wide, 40 * wide], 101 * wide
+    rng, x, xs, xv, a, b, s, v, dout, dbase = grad_inputs(34, m, k, n, r, 3, dtype, x8)
+    args = dict(dbase=dbase, scaling=s, x_scale=xs)
+    good = G.ragged_lora_grad(x, v, dout, a, b, ints(sizes), **args)
+    for at in (slice(33 * wide, 54 * wide), slice(94 * wide, m)):
+        if x8:
+            xs[at] = 255
+        else:
+            x[at] = float("nan")
+        v[at], dout[at] = float("inf"), float("nan")
+    a[1], b[1] = float("inf"), float("nan")
+    got = G.ragged_lora_grad(x, v, dout, a, b, ints(sizes), **args)
+    keep = torch.ones(m, dtype=torch.bool, device=DEV)
+    keep[33 * wide:54 * wide] = False
+    assert torch.equal(got[0][keep], good[0][keep]) and bool(got[0][~keep].isnan().all())
+    for p, q in zip(got[1:], good[1:]):
+        assert torch.equal(p[[0, 2]], q[[0, 2]]) and not bool(p[1].isfinite().any())
 
 
 def test_gradients_against_differences():
