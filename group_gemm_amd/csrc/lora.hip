@@ -1597,8 +1597,9 @@ static hipError_t outer_t(const lora::Outer& p, hipStream_t s) {
 }
 template <OuterX X, int P>
 static hipError_t outer_nb(const lora::Outer& p, hipStream_t s) {
-    // few workgroups: narrower ones (375 rows of 5 groups in fp32, k 1030, n 515: 15.2 us with wide ones, 10 with these)
-    const int64_t groups = std::max<int64_t>(up64(p.m, p.chunk), std::min<int64_t>(p.g, up64(p.m, 32)));
+    // Few workgroups: narrower ones (375 fp32 rows of 5 groups, k 1030, n 515: 15 us with wide ones, 11 with these; 109 bf16
+    // rows over 64 groups, k 4081, n 384: 11 with wide ones, 25 with these).  Every row may be another group's.
+    const int64_t groups = std::max<int64_t>(up64(p.m, p.chunk), std::min<int64_t>(p.g, p.m));
     if (p.r <= 64 && groups * (up64(p.k, 256) + up64(p.n, 256)) < 256) {
         switch (lora_nb(p.r)) {
             case 1: return outer_t<X, 1, P, 1>(p, s);
