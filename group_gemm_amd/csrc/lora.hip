@@ -1542,6 +1542,8 @@ template <typename T, typename O, int NB, int D>
 static hipError_t both_t(const lora::Shrink& sh, lora::Expand p, hipStream_t s) {
     const int64_t tiles = lora_tiles(p.rows, 16);
     p.cols = 4096;
+    // about a workgroup a compute unit, as each contracts the rows again (64 rows of 64 adapters of rank 16, k = n = 4096:
+    // 11.4 us, with 512 workgroups 14, with 1024 18)
     while (p.cols > 256 && tiles * up64(p.n, p.cols) < 256) p.cols /= 2;
     p.col_tiles = (int)std::max<int64_t>(1, up64(p.n, p.cols));
     if (tiles * p.col_tiles > kMaxBlocks) return hipErrorInvalidConfiguration;
